@@ -32,12 +32,16 @@ FC_NOALLOC_WORKSPACE_BYTES = 4 << 20
 FC_ORDER_TREE, FC_ORDER_SEQUENTIAL, FC_ORDER_RING = 0, 1, 2
 FC_REDUCE_REGISTER, FC_REDUCE_STAGED, FC_REDUCE_STAGED_SHIFTED = 0, 1, 2
 FC_STEP_THREE_KERNELS, FC_STEP_ONE_LAUNCH, FC_STEP_ONE_CLUSTER = 0, 1, 2
+FC_TYPE_F32, FC_TYPE_F16, FC_TYPE_BF16 = 0, 1, 2
+FC_MAX_OPT_LAYERS = 1536
+FC_STATE_BLOCK = 256
 
 _lock = threading.Lock()
 _lib = None
 
 _P, _I32, _I64, _F32, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                              ctypes.c_float, ctypes.c_size_t)
+_F64, _U64 = ctypes.c_double, ctypes.c_uint64
 _SIGS = {
     "fc_last_error": (ctypes.c_char_p, []),
     "fc_version": (_I32, []),
@@ -72,6 +76,17 @@ _SIGS = {
                                _P, _P, _P, _P, _P, _P, _P, _F32, _P, _P, _SZ, _P]),
     "fc_step_noalloc": (ctypes.c_int, [_P, _I32, _I32, _P, _F32, _I64, _I64, _F32, _F32, _P,
                                        _P, _P, _P, _P, _P, _P, _P, _P, _P, _F32, _P, _P]),
+    "fc_grad_norm_workspace_size": (_SZ, []),
+    "fc_grad_norm": (ctypes.c_int, [_P, _I32, _I32, _P, _F32, _F32, _P, _P, _P, _SZ, _P]),
+    "fc_adamw_step": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _F64, _F64, _F64, _F64, _F64,
+                                     _P, _P, _I32, _P, _P, _P, _P]),
+    "fc_adamw8_step": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _F64, _F64, _F64, _F64, _F64,
+                                      _P, _P, _I32, _P, _P, _P, _P, _P, _U64, _P]),
+    "fc_layernorm_forward": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, _F32, _P,
+                                            _I64, _P, _P, _P]),
+    "fc_layernorm_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "fc_layernorm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _P, _I32, _P, _P, _I64,
+                                             _I64, _P, _I64, _P, _P, _I32, _P, _SZ, _P]),
 }
 
 
@@ -409,6 +424,200 @@ def fc_step_noalloc(grads, loss_scale: float, chunk: int, k: int, lr: float,
                                  _p(velocity), _p(weights), _p(weights_fp16), _p(norms),
                                  _p(idx), _p(mask), _p(packed), _p(packed_fp16),
                                  float(send_scale), _p(threshold), _s(stream)))
+
+
+# ---- training-step operators beside the aggregation -------------------------------
+
+_TYPES = {torch.float32: FC_TYPE_F32, torch.float16: FC_TYPE_F16, torch.bfloat16: FC_TYPE_BF16}
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise ValueError("%s must be float32, float16 or bfloat16, not %s"
+                         % (name, t.dtype)) from None
+
+
+def _on(t: torch.Tensor, dev: int, name: str) -> None:
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError("%s must be on the GPU of the other tensors, not on %s"
+                         % (name, t.device))
+
+
+def _flat(t: Optional[torch.Tensor], n: int, dtype, name: str, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor of n elements of a type on a GPU (None stays)."""
+    if t is None:
+        return None
+    _on(t, dev, name)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %d elements" % (name, n))
+    if t.dtype is not dtype and (not isinstance(dtype, tuple) or t.dtype not in dtype):
+        raise ValueError("%s must not be %s" % (name, t.dtype))
+    return t.data_ptr()
+
+
+class LayerGrads:
+    """Host table of L layers' gradient tensors (one type, each contiguous, at
+    any address), for fc_grad_norm and the AdamW steps.  `decay` holds a
+    factor on the weight decay for each layer (None: 1 for all).  The table
+    keeps the tensors; build it once where the gradients keep their places."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], decay: Optional[Sequence[float]] = None):
+        if not grads:
+            raise ValueError("no layers")
+        self.type = _type(grads[0], "the gradients")
+        for l, t in enumerate(grads):
+            if t.dtype != grads[0].dtype or not t.is_contiguous() or t.device != grads[0].device:
+                raise ValueError("gradient %d must be contiguous %s on %s"
+                                 % (l, grads[0].dtype, grads[0].device))
+        if decay is not None and len(decay) != len(grads):
+            raise ValueError("decay needs one factor for each of the %d layers" % len(grads))
+        self.dev = grads[0].get_device()
+        _on(grads[0], self.dev, "the gradients")
+        self.L = len(grads)
+        self.sizes = [int(t.numel()) for t in grads]
+        self.N = sum(self.sizes)
+        self._ptrs = (ctypes.c_void_p * self.L)(*[t.data_ptr() for t in grads])
+        self._sizes = _i64(self.sizes)
+        self._decay = None if decay is None else (ctypes.c_float * self.L)(*decay)
+        self._keep = list(grads)
+        self.ptrs = ctypes.cast(self._ptrs, _P)
+        self.sizes_c = ctypes.cast(self._sizes, _P)
+        self.decay_c = None if decay is None else ctypes.cast(self._decay, _P)
+
+
+def fc_grad_norm_workspace_size() -> int:
+    return int(lib().fc_grad_norm_workspace_size())
+
+
+def fc_grad_norm(grads: LayerGrads, loss_scale: float, max_norm: float, norm: torch.Tensor,
+                 scale: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """norm [1]: the global L2 norm of the layers over loss_scale; scale [1]:
+    the factor the AdamW steps take (clipping at max_norm, 0 for none; NaN
+    for a norm that is not finite).  workspace: zero-filled once."""
+    _on(workspace, grads.dev, "workspace")
+    _check(lib().fc_grad_norm(grads.ptrs, grads.type, grads.L, grads.sizes_c, loss_scale,
+                              max_norm, _flat(norm, 1, torch.float32, "norm", grads.dev),
+                              _flat(scale, 1, torch.float32, "scale", grads.dev), workspace.data_ptr(),
+                              workspace.nbytes, _s(stream)))
+
+
+_LOW = (torch.float16, torch.bfloat16)
+
+
+def fc_adamw_step(grads: LayerGrads, grad_scale: Optional[torch.Tensor], lr: float, beta1: float,
+                  beta2: float, eps: float, weight_decay: float, weights: torch.Tensor,
+                  weights_low: Optional[torch.Tensor], exp_avg: torch.Tensor,
+                  exp_avg_sq: torch.Tensor, steps: torch.Tensor, stream=None) -> None:
+    """One AdamW step in place on the fused weights and moments (fp32 [N])."""
+    n = grads.N
+    _check(lib().fc_adamw_step(
+        grads.ptrs, grads.type, grads.L, grads.sizes_c, grads.decay_c,
+        _flat(grad_scale, 1, torch.float32, "grad_scale", grads.dev), lr, beta1, beta2, eps, weight_decay,
+        _flat(weights, n, torch.float32, "weights", grads.dev), _flat(weights_low, n, _LOW, "weights_low", grads.dev),
+        0 if weights_low is None else _TYPES[weights_low.dtype],
+        _flat(exp_avg, n, torch.float32, "exp_avg", grads.dev),
+        _flat(exp_avg_sq, n, torch.float32, "exp_avg_sq", grads.dev),
+        _flat(steps, 2, torch.int32, "steps", grads.dev), _s(stream)))
+
+
+def state_blocks(N: int) -> int:
+    """Blocks (and so scales) of an 8-bit state of N elements."""
+    return -(-int(N) // FC_STATE_BLOCK)
+
+
+def fc_adamw8_step(grads: LayerGrads, grad_scale: Optional[torch.Tensor], lr: float,
+                   beta1: float, beta2: float, eps: float, weight_decay: float,
+                   weights: torch.Tensor, weights_low: Optional[torch.Tensor],
+                   exp_avg_q: torch.Tensor, exp_avg_scale: torch.Tensor,
+                   exp_rms_q: torch.Tensor, exp_rms_scale: torch.Tensor, steps: torch.Tensor,
+                   seed: int, stream=None) -> None:
+    """fc_adamw_step with the moments held as float8_e4m3fn [N] and one fp32
+    scale a block; an e4m3 tensor may be longer than N (whole blocks)."""
+    n, b = grads.N, state_blocks(grads.N)
+    for q, name in ((exp_avg_q, "exp_avg_q"), (exp_rms_q, "exp_rms_q")):
+        _on(q, grads.dev, name)
+        if q.dtype != torch.float8_e4m3fn or not q.is_contiguous() or q.numel() < n:
+            raise ValueError("%s must be contiguous float8_e4m3fn of at least %d elements"
+                             % (name, n))
+    _check(lib().fc_adamw8_step(
+        grads.ptrs, grads.type, grads.L, grads.sizes_c, grads.decay_c,
+        _flat(grad_scale, 1, torch.float32, "grad_scale", grads.dev), lr, beta1, beta2, eps, weight_decay,
+        _flat(weights, n, torch.float32, "weights", grads.dev), _flat(weights_low, n, _LOW, "weights_low", grads.dev),
+        0 if weights_low is None else _TYPES[weights_low.dtype], exp_avg_q.data_ptr(),
+        _flat(exp_avg_scale, b, torch.float32, "exp_avg_scale", grads.dev), exp_rms_q.data_ptr(),
+        _flat(exp_rms_scale, b, torch.float32, "exp_rms_scale", grads.dev),
+        _flat(steps, 2, torch.int32, "steps", grads.dev), int(seed) & 0xFFFFFFFFFFFFFFFF, _s(stream)))
+
+
+def _matrix(t: torch.Tensor, like: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(address, elements between rows) of a matrix like `like` with contiguous rows."""
+    _on(t, like.get_device(), name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must have two dimensions and contiguous rows" % name)
+    if t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError("%s must be %s of %s" % (name, tuple(like.shape), like.dtype))
+    # the stride of a single row says nothing
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _params(x: torch.Tensor, weight, bias) -> int:
+    """FC_TYPE_* of layer norm's parameters."""
+    kind = None
+    for p, name in ((weight, "weight"), (bias, "bias")):
+        if p is None:
+            continue
+        _flat(p, x.shape[1], (torch.float32, x.dtype), name, x.get_device())
+        if kind is not None and p.dtype != kind:
+            raise ValueError("weight and bias must have one type")
+        kind = p.dtype
+    return FC_TYPE_F32 if kind is None else _TYPES[kind]
+
+
+def fc_layernorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor],
+                         bias: Optional[torch.Tensor], eps: float, y: torch.Tensor,
+                         mean: Optional[torch.Tensor] = None,
+                         rstd: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Layer norm over the rows of x [rows, cols]; mean and rstd (fp32 [rows])
+    are what the backward pass needs."""
+    rows, cols = x.shape
+    px, ldx = _matrix(x, x, "x")
+    py, ldy = _matrix(y, x, "y")
+    _check(lib().fc_layernorm_forward(
+        px, rows, cols, ldx, _type(x, "x"), _p(weight), _p(bias), _params(x, weight, bias), eps,
+        py, ldy, _flat(mean, rows, torch.float32, "mean", x.get_device()),
+        _flat(rstd, rows, torch.float32, "rstd", x.get_device()), _s(stream)))
+
+
+def fc_layernorm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().fc_layernorm_backward_workspace_size(int(rows), int(cols)))
+
+
+def fc_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                          mean: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                          dweight: Optional[torch.Tensor], dbias: Optional[torch.Tensor],
+                          workspace: Optional[torch.Tensor], stream=None) -> None:
+    """Gradients of fc_layernorm_forward: dx, and the sums dweight and dbias
+    over the rows (any of the three types, one for both; None: not wanted)."""
+    rows, cols = x.shape
+    px, ldx = _matrix(x, x, "x")
+    pdy, lddy = _matrix(dy, x, "dy")
+    pdx, lddx = _matrix(dx, x, "dx")
+    kind = FC_TYPE_F32
+    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
+        if t is not None:
+            kind = _type(t, name)
+            _flat(t, cols, t.dtype, name, x.get_device())
+    if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
+        raise ValueError("dweight and dbias must have one type")
+    if workspace is not None:
+        _on(workspace, x.get_device(), "workspace")
+    _check(lib().fc_layernorm_backward(
+        pdy, lddy, px, ldx, _type(x, "x"), _p(weight), _params(x, weight, None),
+        _flat(mean, rows, torch.float32, "mean", x.get_device()), _flat(rstd, rows, torch.float32, "rstd", x.get_device()),
+        rows, cols, pdx, lddx, _p(dweight), _p(dbias), kind, _p(workspace),
+        0 if workspace is None else workspace.nbytes, _s(stream)))
 
 
 # ---- engine: device buffers for repeated steps ---------------------------------------

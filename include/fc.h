@@ -453,6 +453,158 @@ FC_API fc_status fc_step_noalloc(const void *const *grads, int32_t W,
                                  void *packed_fp16, float send_scale,
                                  float *threshold, void *stream);
 
+/* ---- training-step operators beside the aggregation ---------------------------- */
+
+/* Element types of the operators below (each argument says which it takes). */
+#define FC_TYPE_F32 0
+#define FC_TYPE_F16 1
+#define FC_TYPE_BF16 2
+
+/* Largest L that fc_grad_norm, fc_adamw_step and fc_adamw8_step accept in one
+ * call (their layer table travels as a kernel parameter). */
+#define FC_MAX_OPT_LAYERS 1536
+
+/* Elements of the fused vector that share one scale of an 8-bit state. */
+#define FC_STATE_BLOCK 256
+
+/* Bytes of scratch fc_grad_norm needs, whatever the layers.  Zero-filled
+ * before its first use; every call leaves its counter at zero again. */
+FC_API size_t fc_grad_norm_workspace_size(void);
+
+/* The global L2 norm of L gradient tensors, and from it the factor that the
+ * AdamW steps below apply to every gradient element:
+ *   norm[0]  = sqrt(sum over all layers and elements of g^2) / loss_scale
+ *   scale[0] = (1 / loss_scale) * min(1, max_norm / norm[0])
+ * max_norm = 0 means no clipping (scale[0] = 1 / loss_scale).  Where the norm
+ * is not finite (an infinity or a NaN among the gradients: an overflowed
+ * loss scale) scale[0] is NaN, which makes the step that reads it change
+ * nothing.  Squares and short sums in fp32, longer sums in float-float
+ * arithmetic in a fixed order: the same inputs on the same GPU give the same
+ * bits.  A square that overflows fp32 (|g| above 1.8e19) counts as infinite.
+ *  grads      host array of L device pointers, aligned to their element; an
+ *             empty layer's pointer is not looked at.
+ *  grad_type  FC_TYPE_* of all of them.
+ *  sizes      host [L] element counts (>= 0, sum >= 1).
+ *  norm, scale  device fp32 [1] outputs, 4-byte aligned.
+ *  workspace  device, fc_grad_norm_workspace_size() bytes, 256-aligned; not
+ *             shared by calls that may overlap on the GPU.
+ * 1 <= L <= FC_MAX_OPT_LAYERS; loss_scale finite and > 0; max_norm finite
+ * and >= 0. */
+FC_API fc_status fc_grad_norm(const void *const *grads, int32_t grad_type, int32_t L,
+                              const int64_t *sizes, float loss_scale, float max_norm,
+                              float *norm, float *scale, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* One AdamW step over L tensors at once, moments in fp32.  The weights and
+ * the moments are in the fused layout (fc_layout of `sizes`); the gradients
+ * are the L separate tensors, read in place.  With s = grad_scale[0] (1 if
+ * NULL), t = steps[0] + 1, c1 = 1 - beta1^t, c2 = 1 - beta2^t, for element i
+ * of layer l:
+ *   g = s * grads[l][i - offsets[l]]
+ *   m = beta1 * m + (1 - beta1) * g
+ *   v = beta2 * v + (1 - beta2) * g^2
+ *   w = w - lr * weight_decay * decay[l] * w
+ *         - (lr / c1) * m / (sqrt(v) / sqrt(c2) + eps)
+ *   weights_low[i] = w rounded to nearest, if asked for.
+ * All of it in fp32; then steps[0] = t.  If s is not finite the step is
+ * skipped: no moment, no weight and no count changes, and weights_low still
+ * receives the unchanged weights.
+ *  grads, grad_type, L, sizes  as for fc_grad_norm.
+ *  decay        host [L] factors on weight_decay (finite, >= 0), or NULL: 1.
+ *  grad_scale   device fp32 [1] (fc_grad_norm's scale), or NULL.
+ *  weights, exp_avg (m), exp_avg_sq (v)  device fp32 [N], updated in place.
+ *  weights_low  device [N] of low_type (FC_TYPE_F16 or FC_TYPE_BF16), or
+ *               NULL; 16-byte aligned.
+ *  steps        device int32 [2], zero-filled at the start of training:
+ *               steps[0] counts the steps applied, steps[1] belongs to the
+ *               kernel (zero between calls).
+ * lr, weight_decay finite and >= 0; 0 <= beta1, beta2 < 1; eps > 0 in fp32.
+ * The moments, weights and gradients must not overlap one another. */
+FC_API fc_status fc_adamw_step(const void *const *grads, int32_t grad_type, int32_t L,
+                               const int64_t *sizes, const float *decay,
+                               const float *grad_scale, double lr, double beta1,
+                               double beta2, double eps, double weight_decay,
+                               float *weights, void *weights_low, int32_t low_type,
+                               float *exp_avg, float *exp_avg_sq, int32_t *steps,
+                               void *stream);
+
+/* fc_adamw_step with the moments held in 8 bits between steps: 2 bytes an
+ * element instead of 8, and two fp32 scales for each block of FC_STATE_BLOCK
+ * elements of the fused vector (blocks run across layer boundaries; the last
+ * may be short).  What is held is m and r = sqrt(v), as e4m3 values (4 bits
+ * of exponent, 3 of mantissa, largest 448) times their block's scale:
+ *   m = exp_avg_q[i] * exp_avg_scale[b],  r = exp_rms_q[i] * exp_rms_scale[b],
+ *   v = r^2,  b = i / FC_STATE_BLOCK.
+ * The step is fc_adamw_step's, in fp32, and the weights see the new moments
+ * before they are rounded.  Then, with M = the largest |m| and R the largest
+ * sqrt(v) of the block (a block whose largest is below 2^-110 holds zeros):
+ *   exp_avg_scale = M / 448, exp_avg_q = e4m3 nearest to m * (448 / M);
+ *   exp_rms_scale = R / 448, exp_rms_q = e4m3 value below or above
+ *     y = sqrt(v) * (448 / R), above with the probability (to 16 bits) of how
+ *     far y lies towards it; a value above 0 never becomes 0.
+ * v moves by 1 - beta2 of itself in a step, far less than half an e4m3 step,
+ * so rounding to nearest would leave it where it is.  The random bits are a
+ * hash of (seed, t, i / 2): the same arguments give the same bits.  The fp32
+ * arithmetic is scaled by 2^20, so that squares hold for |g| from 1e-24 to
+ * 1e13; above that v is infinite.
+ *  exp_avg_q, exp_rms_q  device e4m3 [N], 16-byte aligned, updated in place.
+ *  exp_avg_scale, exp_rms_scale  device fp32 [ceil(N / FC_STATE_BLOCK)].
+ * All zero at the start of training.  Everything else as fc_adamw_step. */
+FC_API fc_status fc_adamw8_step(const void *const *grads, int32_t grad_type, int32_t L,
+                                const int64_t *sizes, const float *decay,
+                                const float *grad_scale, double lr, double beta1,
+                                double beta2, double eps, double weight_decay,
+                                float *weights, void *weights_low, int32_t low_type,
+                                void *exp_avg_q, float *exp_avg_scale, void *exp_rms_q,
+                                float *exp_rms_scale, int32_t *steps, uint64_t seed,
+                                void *stream);
+
+/* Layer norm over the last dimension of x [rows, cols]:
+ *   mean = sum_j x[j] / cols,  rstd = 1 / sqrt(sum_j (x[j] - mean)^2 / cols + eps)
+ *   y[j] = (x[j] - mean) * rstd * weight[j] + bias[j]
+ * in fp32 (the variance from the differences, not from a difference of
+ * squares), y rounded once.
+ *  x, y        device [rows, cols] of `type`, rows ldx and ldy elements apart
+ *              (>= cols), aligned to their element; y must not overlap x.
+ *  weight, bias  device [cols] of param_type (FC_TYPE_F32, or `type`), aligned
+ *              to their element; either may be NULL (1 and 0).
+ *  mean, rstd  device fp32 [rows] outputs, 4-byte aligned, or both NULL.
+ * rows >= 0 (0: nothing is done), cols >= 1, eps >= 0 finite. */
+FC_API fc_status fc_layernorm_forward(const void *x, int64_t rows, int64_t cols, int64_t ldx,
+                                      int32_t type, const void *weight, const void *bias,
+                                      int32_t param_type, float eps, void *y, int64_t ldy,
+                                      float *mean, float *rstd, void *stream);
+
+/* Bytes of scratch fc_layernorm_backward needs for the column sums; 0 on bad
+ * arguments.  Needs no filling. */
+FC_API size_t fc_layernorm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/* Gradients of fc_layernorm_forward.  With h = (x - mean) * rstd and
+ * q = dy * weight, per row:
+ *   dx = rstd * (q - sum_j(q) / cols - h * sum_j(q * h) / cols)
+ * and over the rows:
+ *   dweight[j] = sum dy * h,  dbias[j] = sum dy
+ * in fp32, each rounded once.  grad_type may be the fp16 that the worker
+ * layers of fc_step take, so the two sums can be written straight into them.
+ * The sums run in a fixed order: the same inputs on the same GPU give the
+ * same bits.
+ *  dy, x, dx   device [rows, cols] of `type`, rows lddy, ldx, lddx elements
+ *              apart; dx must not overlap the inputs.
+ *  weight      as in the forward pass (NULL: 1).
+ *  mean, rstd  device fp32 [rows] from the forward pass.
+ *  dweight, dbias  device [cols] outputs of grad_type (any FC_TYPE_*), aligned
+ *              to their element; either may be NULL (not wanted).
+ *  workspace   device, fc_layernorm_backward_workspace_size(rows, cols) bytes,
+ *              256-aligned; may be NULL if neither sum is wanted.
+ * rows = 0 writes zeros to dweight and dbias. */
+FC_API fc_status fc_layernorm_backward(const void *dy, int64_t lddy, const void *x,
+                                       int64_t ldx, int32_t type, const void *weight,
+                                       int32_t param_type, const float *mean,
+                                       const float *rstd, int64_t rows, int64_t cols,
+                                       void *dx, int64_t lddx, void *dweight, void *dbias,
+                                       int32_t grad_type, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
 /* ---- test hook ------------------------------------------------------------------- */
 
 /* Exercises the failure path of the TMA-staged phase 1 (not part of the
