@@ -17,26 +17,74 @@
 // sits at its own address, so its groups of 4 may be shifted against the
 // fused index by 1 to 3 elements, the same shift for a whole layer: then a
 // lane loads the two aligned groups around its own and selects, which keeps
-// wide loads for layers of any size.  A unit that holds a layer boundary or
-// the end of the vector goes element by element (at most two units a layer).
+// wide loads for layers of any size.  A unit that holds a layer boundary
+// reads its gradient element by element (at most two units a layer), and so
+// does everything of the last unit where N is not a multiple of 256.
 //
-// Warps of a persistent grid take units in rounds.  The first unit's loads
-// are issued before the step's scalars (count, factor) are awaited.
+// Two kernels hold the same arithmetic: k_adamw_ring streams weights and
+// moments through shared memory with bulk copies in both directions;
+// k_adamw_direct loads and stores them from registers, which starts faster and
+// serves what is resident at once.  Measured (ring): 280 us for 62.4M elements
+// with fp32 moments, fp32 gradients and an fp16 copy (1.87 GB, 6.7 TB/s); 158
+// us with 8-bit moments and fp16 gradients (1.0 GB, 6.3 TB/s); direct: 3.9 us
+// for 133k elements.
 #include <cuda_fp8.h>
 
+#include "fc_bulk.cuh"
 #include "fc_opt.h"
 
 namespace fc {
 
 #define FC_ADAM_BLOCK 256
 
+// Consumer warps of the ring kernel (so units a tile) and its stages.  A tile
+// of 20 units is copied in pieces of 20 KB; with 8 KB pieces the 62M-element
+// step with fp32 moments took 320 us, with 16 KB 286, with 20 KB 282.  With
+// 8-bit moments the update itself needs the warps: 24 of them and 4 stages
+// took 161 us, 16 took 171, 31 (3 stages) 164; 5 and 3 stages took 175 and
+// 177 us, 8 took 205.
+#ifndef FC_ADAM_CW32
+#define FC_ADAM_CW32 20
+#endif
+#ifndef FC_ADAM_S32
+#define FC_ADAM_S32 3
+#endif
+#ifndef FC_ADAM_CW8
+#define FC_ADAM_CW8 24
+#endif
+#ifndef FC_ADAM_S8
+#define FC_ADAM_S8 4
+#endif
+
+struct AdamState {
+    int64_t N;
+    AdamHyper h;
+    const float *scale;
+    float *w;
+    void *low;
+    int ltype;
+    float *m, *v;                // fp32 moments
+    uint8_t *m8, *r8;            // 8-bit moments
+    float *m_scale, *r_scale;
+    int32_t *steps;
+    uint64_t seed;
+};
+
 struct StepScalars {
-    float s;    // factor on the gradient
-    float lrc;  // lr / c1
-    float rc2;  // 1 / sqrt(c2)
+    float s;     // factor on the gradient (times 2^20 for 8-bit moments)
+    float lrc;   // lr / c1
+    float rc2;   // 1 / sqrt(c2)
     unsigned key;
+    int32_t t;
     int skip;
 };
+
+// The step with 8-bit moments runs in units of 2^-20: gradient, moments and
+// eps are multiplied by 2^20 (exact, and folded into factors that are there
+// anyway), so that g^2 stays a normal fp32 number down to |g| = 1e-24, well
+// below the smallest moments that the blocks can hold relative to each other
+// (fp32 moments end at |g| = 1e-19).
+#define FC_ADAM8_UNIT 0x1p20f
 
 // 32-bit mixing by multiplications and xor-shifts (a bijection of 32 bits).
 __device__ __forceinline__ unsigned mix32(unsigned x)
@@ -49,35 +97,52 @@ __device__ __forceinline__ unsigned mix32(unsigned x)
     return x;
 }
 
-// Read by one thread of each CTA.  A CTA arrives at steps[1] once it has read
-// steps[0]; the last one to arrive counts the step, so no CTA can read the
-// new count.
-__device__ __forceinline__ void load_scalars(StepScalars &sc, const AdamHyper &h,
-                                             const float *scale, int32_t *steps,
-                                             uint64_t seed)
+// Called by one warp of each CTA; the caller's barrier shows `sh` to the rest.
+template <int BITS>
+__device__ __forceinline__ void load_scalars(StepScalars &sh, const AdamState &st)
 {
-    const float s = scale ? __ldcg(scale) : 1.f;
-    const int32_t done = __ldcg(steps);
-    const float t = (float)(done + 1);
-    const float c1 = -expm1f(t * h.lnb1);
-    const float c2 = -expm1f(t * h.lnb2);
-    sc.s = s;
-    sc.lrc = __fdiv_rn(h.lr, c1);
-    sc.rc2 = __fdiv_rn(1.f, __fsqrt_rn(c2));
-    sc.skip = !isfinite(s);
-    sc.key = mix32((unsigned)seed ^ mix32((unsigned)(seed >> 32) ^ mix32((unsigned)(done + 1))));
-    if (!sc.skip) {
-        __threadfence();
-        if (atomicAdd(reinterpret_cast<unsigned *>(steps) + 1, 1u) == gridDim.x - 1) {
-            steps[0] = done + 1;
-            steps[1] = 0;
-        }
+    const int lane = threadIdx.x & 31;
+    const float s = st.scale ? __ldcg(st.scale) : 1.f;
+    const int32_t t = __ldcg(st.steps) + 1;
+    // lane 0 forms c1, lane 1 c2
+    const float c = -expm1f((float)t * (lane == 0 ? st.h.lnb1 : st.h.lnb2));
+    if (lane == 0) {
+        sh.lrc = __fdividef(st.h.lr, c);
+        sh.s = BITS == 8 ? s * FC_ADAM8_UNIT : s;
+        sh.t = t;
+        sh.skip = !isfinite(s);
+        sh.key = mix32((unsigned)st.seed ^ mix32((unsigned)(st.seed >> 32) ^ mix32((unsigned)t)));
+    } else if (lane == 1) {
+        sh.rc2 = rsqrtf(c);
+    }
+}
+
+// Each CTA arrives at steps[1] once it has read steps[0], and the last to
+// arrive counts the step, so no CTA can read the new count.  The arrival is
+// issued early and its answer only looked at when the CTA's work is done.
+__device__ __forceinline__ unsigned arrive_step(int32_t *steps)
+{
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                 : "=r"(old)
+                 : "l"(steps + 1)
+                 : "memory");
+    return old;
+}
+
+__device__ __forceinline__ void count_step(int32_t *steps, unsigned arrived, int32_t t)
+{
+    if (arrived == gridDim.x - 1) {
+        steps[0] = t;
+        steps[1] = 0;
     }
 }
 
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// ---- gradients ------------------------------------------------------------------------
 
 // A lane's four gradient elements as they are loaded.
 template <class GT>
@@ -184,6 +249,194 @@ __device__ __forceinline__ int find_segment(const Tab &t, int64_t f)
     return lo;
 }
 
+// The gradient of a unit that lies inside one segment.
+template <class GT>
+struct UnitGrad {
+    Raw4<GT> g[2];
+    float decay;
+    int sg;      // segment of the unit's first element
+    bool whole;  // the unit is whole and inside that segment
+};
+
+// Issues the gradient loads of the unit at `lo` if it is whole and inside one
+// segment; `sg` is moved on to the unit's first segment.
+template <class GT, class Tab>
+__device__ __forceinline__ void load_unit_grad(const Tab &tab, int64_t lo, int lane, int &sg,
+                                               UnitGrad<GT> &u)
+{
+    if (!(tab.off[sg] <= lo && lo < tab.off[sg + 1])) sg = find_segment(tab, lo);
+    const int64_t off = tab.off[sg], oend = tab.off[sg + 1];
+    u.sg = sg;
+    u.whole = lo + FC_STATE_BLOCK <= oend;
+    if (!u.whole) return;
+    const GT *first = static_cast<const GT *>(tab.ptr[sg]);
+    const GT *p = first + (lo - off) + 4 * lane;
+    const GT *end = first + (oend - off);
+    const int d = (int)(((uintptr_t)p / sizeof(GT)) & 3);
+    u.decay = tab.decay[sg];
+    u.g[0] = load4(p, first, end, d);
+    u.g[1] = load4(p + 128, first, end, d);
+}
+
+// Gradient and decay of a lane's eight elements of any unit (0 past N), `sg`
+// the segment of the unit's first element.  All eight loads are in flight
+// before the first is used.
+template <class GT, class Tab>
+__device__ __forceinline__ void gather_unit(const Tab &tab, int64_t N, int64_t lo, int lane,
+                                            int sg, float *g, float *d)
+{
+    GT x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t a = lo + 4 * lane + 128 * (j >> 2) + (j & 3);
+        const int64_t f = a < N ? a : N - 1;
+        while (tab.off[sg + 1] <= f) ++sg;
+        x[j] = static_cast<const GT *>(tab.ptr[sg])[f - tab.off[sg]];
+        d[j] = tab.decay[sg];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t a = lo + 4 * lane + 128 * (j >> 2) + (j & 3);
+        g[j] = a < N ? as_f32(x[j]) : 0.f;
+    }
+}
+
+// ---- arithmetic -----------------------------------------------------------------------
+
+__device__ __forceinline__ float fast_sqrt(float x)
+{
+    float y;  // at most one unit in the last place off
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float fast_rcp_ftz(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// sqrt(x) for x = 0 or in [2^-126, 2^127]: the approximate reciprocal root, and
+// one Newton step on the root's remainder, after which all but about one root
+// in a million is the nearest fp32 number.
+__device__ __forceinline__ float newton_sqrt(float x)
+{
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 0x1p-126f)));
+    const float s = x * y;
+    return fmaf(fmaf(-s, s, x), 0.5f * y, s);
+}
+
+// One element with fp32 moments.  The quotient is the fast division (2 units
+// in the last place): it enters w scaled by lr, far below w's own rounding.
+__device__ __forceinline__ void adam1(float graw, float decay, const AdamHyper &h,
+                                      const StepScalars &sc, float &m, float &v, float &w)
+{
+    const float g = graw * sc.s;
+    m = fmaf(h.b1, m, h.omb1 * g);
+    v = fmaf(h.b2, v, h.omb2 * g * g);
+    const float step = __fdividef(sc.lrc * m, fmaf(fast_sqrt(v), sc.rc2, h.eps));
+    w = fmaf(-h.lrwd * decay, w, w) - step;
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float y;  // a NaN among the three is the result
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// A lane's eight elements of a unit with 8-bit moments.  w: updated; mq, rq:
+// e4m3 codes in and out; ms, rs: block scales in and out.  UNIFORM: d[0] is
+// the decay of all eight.
+//
+// The moments are formed by the definition's operations one by one, each
+// rounded once (no fused multiply-add), and the root and the blocks' factors
+// to the nearest: a code is a step function of its value, so a last place
+// would turn some code in a million into its neighbour, 6 % away, and the
+// next step's block maximum with it.  The weights take the fast quotient.
+//
+// Rounding r by chance: y = r * 448 / top lies in [0, 448].  Scaled by 2^-120
+// an e4m3 number is the top of an fp32 number's bits: e4m3's smallest normal
+// 2^-6 falls on fp32's 2^-126, so that below it both formats are linear, and
+// the code is the bits above bit 20 everywhere.  Adding 20 random bits (16
+// drawn, centred) below the code and cutting rounds up with the probability
+// of what is cut off.  A code of 0 for r > 0 becomes 1.
+template <bool UNIFORM>
+__device__ __forceinline__ void adam8_unit(const float *graw, const float *d, const AdamHyper &h,
+                                           const StepScalars &sc, int64_t i0, float *w,
+                                           uint32_t *mq, uint32_t *rq, float &ms, float &rs)
+{
+    float m[8], r[8];
+    const float ma = ms * FC_ADAM8_UNIT, ra = rs * FC_ADAM8_UNIT;
+    const float wd0 = -h.lrwd * d[0];
+    float mtop = 0.f, rtop = 0.f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const float2 cm = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)(mq[p >> 1] >> (16 * (p & 1))), __NV_E4M3)));
+        const float2 cr = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)(rq[p >> 1] >> (16 * (p & 1))), __NV_E4M3)));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int j = 2 * p + e;
+            const float g = __fmul_rn(graw[j], sc.s);
+            const float r0 = __fmul_rn(e ? cr.y : cr.x, ra);
+            m[j] = __fadd_rn(__fmul_rn(__fmul_rn(e ? cm.y : cm.x, ma), h.b1),
+                             __fmul_rn(g, h.omb1));
+            const float v = __fadd_rn(__fmul_rn(__fmul_rn(r0, r0), h.b2),
+                                      __fmul_rn(__fmul_rn(g, g), h.omb2));
+            r[j] = newton_sqrt(v);
+            const float rden = fast_rcp_ftz(fmaf(r[j], sc.rc2, h.eps));
+            const float kept = fmaf(UNIFORM ? wd0 : -h.lrwd * d[j], w[j], w[j]);
+            w[j] = fmaf(-sc.lrc * m[j], rden, kept);
+        }
+        mtop = max3_nan(mtop, fabsf(m[2 * p]), fabsf(m[2 * p + 1]));
+        rtop = max3_nan(rtop, r[2 * p], r[2 * p + 1]);
+    }
+    // magnitudes compare as their bits; a NaN is above all numbers
+    mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
+    rtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rtop)));
+    // a block below 2^-110 holds zeros; a NaN or an infinity goes into the scale
+    const bool mdead = mtop < 0x1p-110f * FC_ADAM8_UNIT;
+    const bool rdead = rtop < 0x1p-110f * FC_ADAM8_UNIT;
+    ms = mdead ? 0.f : mtop * (1.f / 448.f / FC_ADAM8_UNIT);
+    rs = rdead ? 0.f : rtop * (1.f / 448.f / FC_ADAM8_UNIT);
+    // even lanes divide for m, odd ones for r
+    const float q448 = 448.f * __frcp_rn((threadIdx.x & 1) ? rtop : mtop);
+    const float mto = mdead ? 0.f : __shfl_sync(0xffffffffu, q448, 0);
+    const float rto = rdead ? 0.f : __shfl_sync(0xffffffffu, q448, 1);
+    const float least = rdead ? 0.f : 0x1p-129f;  // e4m3's 2^-9
+    const uint64_t pair = (uint64_t)i0 >> 1;
+    const uint32_t x = (uint32_t)pair + sc.key + (uint32_t)(pair >> 32) * 0x9E3779B9u;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const float *mm = m + 4 * q;
+        mq[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(mm[0] * mto, mm[1] * mto),
+                                                   __NV_SATFINITE, __NV_E4M3) |
+                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(mm[2] * mto, mm[3] * mto),
+                                                   __NV_SATFINITE, __NV_E4M3)
+                    << 16;
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t bits = mix32(x + 64 * q + e);
+            // 24 bits: the 16 drawn, then 0x80
+            const uint32_t lo = __byte_perm(bits, 0x80u, 0x5104);
+            const uint32_t hi = __byte_perm(bits, 0x80u, 0x5324);
+            const float ra0 = r[4 * q + 2 * e], ra1 = r[4 * q + 2 * e + 1];
+            // r > 0 is at least 2^-63 here
+            const float y0 = fmaxf(ra0 * rto * 0x1p-120f, fminf(ra0, least));
+            const float y1 = fmaxf(ra1 * rto * 0x1p-120f, fminf(ra1, least));
+            u[2 * e] = (__float_as_uint(y0) << 4) + lo;
+            u[2 * e + 1] = (__float_as_uint(y1) << 4) + hi;
+        }
+        rq[q] = __byte_perm(__byte_perm(u[0], u[1], 0x0073), __byte_perm(u[2], u[3], 0x0073),
+                            0x5410);
+    }
+}
+
 __device__ __forceinline__ void store_low4(void *low, int ltype, int64_t i, const float *w)
 {
     uint2 q;
@@ -208,373 +461,449 @@ __device__ __forceinline__ void store_low1(void *low, int ltype, int64_t i, floa
         static_cast<__nv_bfloat16 *>(low)[i] = __float2bfloat16_rn(w);
 }
 
-__device__ __forceinline__ float fast_sqrt(float x)
-{
-    float y;  // at most one unit in the last place off
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+// ---- units from and to global memory ----------------------------------------------------
 
-// One element; returns sqrt(v).  The quotient is the fast division (2 units
-// in the last place): it enters w scaled by lr, far below w's own rounding.
-__device__ __forceinline__ float adam1(float graw, float decay, const AdamHyper &h,
-                                       const StepScalars &sc, float &m, float &v, float &w)
-{
-    const float g = graw * sc.s;
-    m = fmaf(h.b1, m, h.omb1 * g);
-    v = fmaf(h.b2, v, h.omb2 * g * g);
-    const float r = fast_sqrt(v);
-    const float step = __fdividef(sc.lrc * m, fmaf(r, sc.rc2, h.eps));
-    w = fmaf(-h.lrwd * decay, w, w) - step;
-    return r;
-}
-
-// The part of a unit that both state formats share.
-template <class GT>
-struct UnitGrad {
-    Raw4<GT> g[2];
-    float decay;
+// Any unit in registers: weights, moments, gradient and decay of a lane's
+// eight elements (0 past N).  Groups that lie inside one layer and inside the
+// vector are read and written as vectors, the others element by element.
+template <int BITS>
+struct UnitRegs {
+    float w[8], g[8], d[8];
+    float m[BITS == 32 ? 8 : 1], v[BITS == 32 ? 8 : 1];
+    uint32_t mq[2], rq[2];
+    float ms, rs;
 };
 
-// True if the unit at `lo` is whole and inside segment `sg` (moved on to the
-// unit's first segment); then its gradient loads are issued.
-template <class GT, class Tab>
-__device__ __forceinline__ bool load_unit_grad(const Tab &tab, int64_t lo, int64_t N, int lane,
-                                               int &sg, UnitGrad<GT> &u)
+__device__ __forceinline__ void get4(float *to, const float *from, bool whole, int have)
 {
-    if (!(tab.off[sg] <= lo && lo < tab.off[sg + 1])) sg = find_segment(tab, lo);
-    const int64_t off = tab.off[sg], oend = tab.off[sg + 1];
-    if (lo + FC_STATE_BLOCK > oend) return false;
-    const GT *first = static_cast<const GT *>(tab.ptr[sg]);
-    const GT *p = first + (lo - off) + 4 * lane;
-    const GT *end = first + (oend - off);
-    const int d = (int)(((uintptr_t)p / sizeof(GT)) & 3);
-    u.decay = tab.decay[sg];
-    u.g[0] = load4(p, first, end, d);
-    u.g[1] = load4(p + 128, first, end, d);
-    return true;
+    if (whole) {
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(from));
+        to[0] = x.x;
+        to[1] = x.y;
+        to[2] = x.z;
+        to[3] = x.w;
+    } else {
+        to[0] = have > 0 ? from[0] : 0.f;
+        to[1] = have > 1 ? from[1] : 0.f;
+        to[2] = have > 2 ? from[2] : 0.f;
+        to[3] = 0.f;
+    }
 }
 
-// ---- fp32 moments ---------------------------------------------------------------------
+__device__ __forceinline__ void put4(float *to, const float *from, bool whole, int have)
+{
+    if (whole) {
+        __stcs(reinterpret_cast<float4 *>(to), make_float4(from[0], from[1], from[2], from[3]));
+    } else {
+        if (have > 0) to[0] = from[0];
+        if (have > 1) to[1] = from[1];
+        if (have > 2) to[2] = from[2];
+    }
+}
 
-template <class GT, class Tab>
+__device__ __forceinline__ uint32_t get4(const uint8_t *from, bool whole, int have)
+{
+    if (whole) return __ldcs(reinterpret_cast<const unsigned *>(from));
+    uint32_t q = 0;
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (e < have) q |= (uint32_t)from[e] << (8 * e);
+    return q;
+}
+
+__device__ __forceinline__ void put4(uint8_t *to, uint32_t q, bool whole, int have)
+{
+    if (whole) {
+        __stcs(reinterpret_cast<unsigned *>(to), q);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (e < have) to[e] = (uint8_t)(q >> (8 * e));
+}
+
+template <class GT, int BITS, class Tab>
+__device__ __forceinline__ void load_unit(const Tab &tab, const AdamState &st, int64_t un,
+                                          int lane, UnitRegs<BITS> &u)
+{
+    const int64_t lo = un * FC_STATE_BLOCK;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t a = lo + 4 * lane + 128 * i;
+        const bool whole = a + 4 <= st.N;
+        const int have = a < st.N ? (int)(st.N - a) : 0;  // only looked at if not whole
+        get4(u.w + 4 * i, st.w + a, whole, have);
+        if constexpr (BITS == 32) {
+            get4(u.m + 4 * i, st.m + a, whole, have);
+            get4(u.v + 4 * i, st.v + a, whole, have);
+        } else {
+            u.mq[i] = get4(st.m8 + a, whole, have);
+            u.rq[i] = get4(st.r8 + a, whole, have);
+        }
+    }
+    if constexpr (BITS == 8) {
+        u.ms = __ldcs(st.m_scale + un);
+        u.rs = __ldcs(st.r_scale + un);
+    }
+    int sg = find_segment(tab, lo);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t a = lo + 4 * lane + 128 * i;
+        float *const g = u.g + 4 * i, *const d = u.d + 4 * i;
+        while (sg + 1 < tab.L && tab.off[sg + 1] <= a) ++sg;
+        const int64_t off = tab.off[sg], oend = tab.off[sg + 1];
+        const GT *first = static_cast<const GT *>(tab.ptr[sg]);
+        d[0] = d[1] = d[2] = d[3] = tab.decay[sg];
+        if (a + 4 <= oend) {
+            const GT *p = first + (a - off);
+            unpack4(load4(p, first, first + (oend - off), (int)(((uintptr_t)p / sizeof(GT)) & 3)),
+                    g);
+        } else {
+            int se = sg;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[e] = 0.f;
+                if (a + e < st.N) {
+                    while (tab.off[se + 1] <= a + e) ++se;
+                    g[e] = as_f32(static_cast<const GT *>(tab.ptr[se])[a + e - tab.off[se]]);
+                    d[e] = tab.decay[se];
+                }
+            }
+        }
+    }
+}
+
+template <int BITS>
+__device__ __forceinline__ void update_unit(const AdamState &st, const StepScalars &sc, int64_t un,
+                                            int lane, UnitRegs<BITS> &u)
+{
+    const int64_t lo = un * FC_STATE_BLOCK;
+    if (!sc.skip) {
+        if constexpr (BITS == 32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                adam1(u.g[j], u.d[j], st.h, sc, u.m[j], u.v[j], u.w[j]);
+        } else {
+            adam8_unit<false>(u.g, u.d, st.h, sc, lo + 4 * lane, u.w, u.mq, u.rq, u.ms, u.rs);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t a = lo + 4 * lane + 128 * i;
+        const bool whole = a + 4 <= st.N;
+        const int have = a < st.N ? (int)(st.N - a) : 0;
+        if (!sc.skip) {
+            put4(st.w + a, u.w + 4 * i, whole, have);
+            if constexpr (BITS == 32) {
+                put4(st.m + a, u.m + 4 * i, whole, have);
+                put4(st.v + a, u.v + 4 * i, whole, have);
+            } else {
+                put4(st.m8 + a, u.mq[i], whole, have);
+                put4(st.r8 + a, u.rq[i], whole, have);
+            }
+        }
+        if (st.low) {
+            if (whole) {
+                store_low4(st.low, st.ltype, a, u.w + 4 * i);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (e < have) store_low1(st.low, st.ltype, a + e, u.w[4 * i + e]);
+            }
+        }
+    }
+    if constexpr (BITS == 8) {
+        if (lane == 0 && !sc.skip) {
+            st.m_scale[un] = u.ms;
+            st.r_scale[un] = u.rs;
+        }
+    }
+}
+
+// ---- direct kernel ----------------------------------------------------------------------
+
+template <class GT, int BITS, class Tab>
 __global__ void __launch_bounds__(FC_ADAM_BLOCK)
-    k_adamw(const __grid_constant__ Tab tab, const int64_t N, const AdamHyper h,
-            const float *__restrict__ scale, float *__restrict__ w, void *__restrict__ low,
-            const int ltype, float *__restrict__ m, float *__restrict__ v,
-            int32_t *__restrict__ steps)
+    k_adamw_direct(const __grid_constant__ Tab tab, const __grid_constant__ AdamState st)
 {
     __shared__ StepScalars sh;
     wait_for_prior_grid();
     allow_dependent_launch();
     const int lane = threadIdx.x & 31;
-    const int64_t units = (N + FC_STATE_BLOCK - 1) / FC_STATE_BLOCK;
+    const int64_t units = (st.N + FC_STATE_BLOCK - 1) / FC_STATE_BLOCK;
     const int64_t stride = (int64_t)gridDim.x * (FC_ADAM_BLOCK / 32);
     int64_t un = (int64_t)blockIdx.x * (FC_ADAM_BLOCK / 32) + (threadIdx.x >> 5);
-    int sg = 0;
-    UnitGrad<GT> u;
-    float4 w4[2], m4[2], v4[2];
-    bool whole = false;
-
-    auto load = [&]() {
-        const int64_t lo = un * FC_STATE_BLOCK;
-        whole = load_unit_grad<GT>(tab, lo, N, lane, sg, u);
-        if (!whole) return;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t a = lo + 4 * lane + 128 * i;
-            w4[i] = __ldcs(reinterpret_cast<const float4 *>(w + a));
-            m4[i] = __ldcs(reinterpret_cast<const float4 *>(m + a));
-            v4[i] = __ldcs(reinterpret_cast<const float4 *>(v + a));
-        }
-    };
-    if (un < units) load();
-    if (threadIdx.x == 0) {
-        StepScalars t;
-        load_scalars(t, h, scale, steps, 0);
-        sh = t;
-    }
+    UnitRegs<BITS> u;
+    // the first unit's loads before the step's scalars are awaited
+    if (un < units) load_unit<GT, BITS>(tab, st, un, lane, u);
+    if (threadIdx.x < 32) load_scalars<BITS>(sh, st);
     __syncthreads();
     const StepScalars sc = sh;
-    if (sc.skip && !low) return;
-    for (; un < units;) {
-        const int64_t lo = un * FC_STATE_BLOCK;
-        if (whole) {
-            if (sc.skip) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    store_low4(low, ltype, lo + 4 * lane + 128 * i, &w4[i].x);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float g[4];
-                    unpack4(u.g[i], g);
-                    adam1(g[0], u.decay, h, sc, m4[i].x, v4[i].x, w4[i].x);
-                    adam1(g[1], u.decay, h, sc, m4[i].y, v4[i].y, w4[i].y);
-                    adam1(g[2], u.decay, h, sc, m4[i].z, v4[i].z, w4[i].z);
-                    adam1(g[3], u.decay, h, sc, m4[i].w, v4[i].w, w4[i].w);
-                    const int64_t a = lo + 4 * lane + 128 * i;
-                    __stcs(reinterpret_cast<float4 *>(w + a), w4[i]);
-                    __stcs(reinterpret_cast<float4 *>(m + a), m4[i]);
-                    __stcs(reinterpret_cast<float4 *>(v + a), v4[i]);
-                    if (low) store_low4(low, ltype, a, &w4[i].x);
-                }
-            }
-        } else {
-            for (int e = 0; e < 8; ++e) {
-                const int64_t a = lo + lane + 32 * e;
-                if (a >= N) break;
-                const int sa = find_segment(tab, a);
-                float wi = w[a];
-                if (!sc.skip) {
-                    const float g = as_f32(static_cast<const GT *>(tab.ptr[sa])[a - tab.off[sa]]);
-                    float mi = m[a], vi = v[a];
-                    adam1(g, tab.decay[sa], h, sc, mi, vi, wi);
-                    w[a] = wi;
-                    m[a] = mi;
-                    v[a] = vi;
-                }
-                if (low) store_low1(low, ltype, a, wi);
-            }
-        }
+    unsigned arrived = 0;
+    if (threadIdx.x == 0 && !sc.skip) arrived = arrive_step(st.steps);
+    while (un < units) {
+        update_unit<BITS>(st, sc, un, lane, u);
         un += stride;
-        if (un < units) load();
+        if (un < units) load_unit<GT, BITS>(tab, st, un, lane, u);
     }
+    if (threadIdx.x == 0 && !sc.skip) count_step(st.steps, arrived, sc.t);
 }
 
-// ---- 8-bit moments --------------------------------------------------------------------
+// ---- ring kernel ------------------------------------------------------------------------
+//
+// One CTA per SM.  A tile is CW units; a stage holds a tile's weights and
+// moments.  One thread copies tiles in (bulk copies counted on the stage's
+// `full` barrier), CW warps update one unit each in place, and the same
+// thread copies the stage out again once all have arrived at its `done`
+// barrier; a stage is refilled when its copy out has read it.  The gradient
+// comes straight from its tensor (any alignment), one tile ahead in
+// registers, and the low-precision copy goes out from registers.
 
-#define FC_E4M3_TOP 448.f
+#define FC_ADAM_WAIT_NS 2000000000ull
 
-// The step with 8-bit moments runs in units of 2^-20: gradient, moments and
-// eps are multiplied by 2^20 (exact, and folded into factors that are there
-// anyway), so that g^2 stays a normal fp32 number down to |g| = 1e-24, well
-// below the smallest moments that the blocks can hold relative to each other
-// (fp32 moments end at |g| = 1e-19).
-#define FC_ADAM8_UNIT 0x1p20f
+template <int BITS, int CW>
+struct RingStage {
+    static constexpr int T = CW * FC_STATE_BLOCK;
+    static constexpr int WB = T * 4;
+    static constexpr int AB = BITS == 32 ? T * 4 : T;
+    static constexpr int BYTES = WB + 2 * AB;
+};
 
-// Factor onto the e4m3 range for a block whose largest value is `top` units,
-// and the scale that undoes it; a block below 2^-110 (near where its scale
-// would leave the normal numbers) holds zeros.  A NaN or an infinity in the
-// block goes into the scale.
-__device__ __forceinline__ void block_scale(float top, float &to, float &scale)
+template <class GT, int BITS, int CW, class Tab>
+__global__ void __launch_bounds__((CW + 1) * 32)
+    k_adamw_ring(const __grid_constant__ Tab tab, const __grid_constant__ AdamState st,
+                 const int64_t tiles, const int S)
 {
-    const bool dead = top < 0x1p-110f * FC_ADAM8_UNIT;
-    to = dead ? 0.f : __fdiv_rn(FC_E4M3_TOP, top);
-    scale = dead ? 0.f : top * (1.f / FC_E4M3_TOP) * (1.f / FC_ADAM8_UNIT);
-}
-
-__device__ __forceinline__ void from_e4m3(uint32_t q, float scale, float *x)
-{
-    const __half2_raw a =
-        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q >> 16), __NV_E4M3);
-    const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
-    x[0] = fa.x * scale;
-    x[1] = fa.y * scale;
-    x[2] = fb.x * scale;
-    x[3] = fb.y * scale;
-}
-
-// Nearest e4m3, magnitudes above 448 (from the factor's rounding) to 448.
-__device__ __forceinline__ uint32_t to_e4m3(float a, float b, float c, float d)
-{
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | hi << 16;
-}
-
-// The e4m3 value below or above y in [0, 448], by 16 random bits.  Normal
-// e4m3 values differ from fp32 by 20 cut mantissa bits; below 2^-6 the
-// spacing is 2^-9, which is what fp32 values in [2^-6, 2^-5) are cut to.
-__device__ __forceinline__ float stochastic_e4m3(float y, unsigned bits16)
-{
-    y = fminf(y, FC_E4M3_TOP);
-    const float base = y < 0x1p-6f ? 0x1p-6f : 0.f;
-    const unsigned t = (__float_as_uint(y + base) + (bits16 * 16u + 8u)) & ~0xfffffu;
-    const float q = fmaxf(__uint_as_float(t) - base, 0x1p-9f);
-    return y > 0.f ? q : 0.f;
-}
-
-__device__ __forceinline__ unsigned pair_bits(unsigned key, int64_t i)
-{
-    const uint64_t p = (uint64_t)i >> 1;
-    return mix32((unsigned)p + key + (unsigned)(p >> 32) * 0x9E3779B9u);
-}
-
-template <class GT, class Tab>
-__global__ void __launch_bounds__(FC_ADAM_BLOCK)
-    k_adamw8(const __grid_constant__ Tab tab, const int64_t N, const AdamHyper h,
-             const float *__restrict__ scale, float *__restrict__ w, void *__restrict__ low,
-             const int ltype, uint8_t *__restrict__ m8, float *__restrict__ m_scale,
-             uint8_t *__restrict__ r8, float *__restrict__ r_scale,
-             int32_t *__restrict__ steps, const uint64_t seed)
-{
-    // h.eps comes in units
+    using St = RingStage<BITS, CW>;
+    extern __shared__ __align__(128) unsigned char stages[];
+    __shared__ uint64_t bars[2 * 32];  // full [S], done [S]
     __shared__ StepScalars sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&bars[s]), 1);
+            mbar_init(smem_u32(&bars[S + s]), CW);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     wait_for_prior_grid();
     allow_dependent_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t units = (N + FC_STATE_BLOCK - 1) / FC_STATE_BLOCK;
-    const int64_t stride = (int64_t)gridDim.x * (FC_ADAM_BLOCK / 32);
-    int64_t un = (int64_t)blockIdx.x * (FC_ADAM_BLOCK / 32) + (threadIdx.x >> 5);
-    int sg = 0;
-    UnitGrad<GT> u;
-    float4 w4[2];
-    uint32_t mq[2], rq[2];
-    float ms = 0.f, rs = 0.f;
-    bool whole = false;
+    const int64_t n = blockIdx.x < tiles ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
 
-    auto load = [&]() {
-        const int64_t lo = un * FC_STATE_BLOCK;
-        whole = load_unit_grad<GT>(tab, lo, N, lane, sg, u);
-        ms = __ldcs(m_scale + un) * FC_ADAM8_UNIT;
-        rs = __ldcs(r_scale + un) * FC_ADAM8_UNIT;
-        if (!whole) return;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t a = lo + 4 * lane + 128 * i;
-            w4[i] = __ldcs(reinterpret_cast<const float4 *>(w + a));
-            mq[i] = __ldcs(reinterpret_cast<const unsigned *>(m8 + a));
-            rq[i] = __ldcs(reinterpret_cast<const unsigned *>(r8 + a));
+    if (warp == CW) {
+        if (lane != 0) return;
+        const char *const gw = reinterpret_cast<const char *>(st.w);
+        const char *const ga = BITS == 32 ? reinterpret_cast<const char *>(st.m)
+                                          : reinterpret_cast<const char *>(st.m8);
+        const char *const gb = BITS == 32 ? reinterpret_cast<const char *>(st.v)
+                                          : reinterpret_cast<const char *>(st.r8);
+        auto fill = [&](int64_t it) {
+            const int s = (int)(it % S);
+            const int64_t t = blockIdx.x + it * gridDim.x;
+            const uint32_t full = smem_u32(&bars[s]);
+            const uint32_t to = smem_u32(stages) + (uint32_t)s * St::BYTES;
+            mbar_expect_tx(full, St::BYTES);
+            bulk_g2s(to, gw + t * St::WB, St::WB, full);
+            bulk_g2s(to + St::WB, ga + t * St::AB, St::AB, full);
+            bulk_g2s(to + St::WB + St::AB, gb + t * St::AB, St::AB, full);
+        };
+        int64_t filled = 0;
+        for (; filled < n && filled < S; ++filled) fill(filled);
+        for (int64_t it = 0; it < n; ++it) {
+            const int s = (int)(it % S);
+            if (!mbar_wait(smem_u32(&bars[S + s]), (uint32_t)(it / S) & 1, FC_ADAM_WAIT_NS)) {
+                // not expected: no more copies out; those coming in must have
+                // landed before the shared memory may go
+                atomicOr(reinterpret_cast<unsigned *>(st.steps) + 1, 0x80000000u);
+                for (int64_t j = it; j < filled; ++j)
+                    mbar_wait(smem_u32(&bars[j % S]), (uint32_t)(j / S) & 1, FC_ADAM_WAIT_NS);
+                break;
+            }
+            if (!sh.skip) {
+                const int64_t t = blockIdx.x + it * gridDim.x;
+                const uint32_t from = smem_u32(stages) + (uint32_t)s * St::BYTES;
+                bulk_s2g(const_cast<char *>(gw) + t * St::WB, from, St::WB);
+                bulk_s2g(const_cast<char *>(ga) + t * St::AB, from + St::WB, St::AB);
+                bulk_s2g(const_cast<char *>(gb) + t * St::AB, from + St::WB + St::AB, St::AB);
+            }
+            bulk_commit();
+            // the stage before this one has been read by now, or nearly
+            if (it >= 1 && filled < n) {
+                bulk_wait_read<1>();
+                fill(filled++);
+            }
+        }
+        bulk_wait_all();
+        return;
+    }
+
+    // the consumers
+    int sg = 0;
+    UnitGrad<GT> next;
+    float nms = 0.f, nrs = 0.f;
+    auto unit = [&](int64_t it) { return (blockIdx.x + it * gridDim.x) * CW + warp; };
+    auto load = [&](int64_t un) {
+        load_unit_grad<GT>(tab, un * FC_STATE_BLOCK, lane, sg, next);
+        if constexpr (BITS == 8) {
+            nms = __ldcs(st.m_scale + un);
+            nrs = __ldcs(st.r_scale + un);
         }
     };
-    if (un < units) load();
-    if (threadIdx.x == 0) {
-        StepScalars t;
-        load_scalars(t, h, scale, steps, seed);
-        t.s *= FC_ADAM8_UNIT;
-        sh = t;
-    }
-    __syncthreads();
+    if (n > 0) load(unit(0));
+    if (warp == 0) load_scalars<BITS>(sh, st);
+    asm volatile("bar.sync 1, %0;" ::"n"(CW * 32) : "memory");
     const StepScalars sc = sh;
-    if (sc.skip && !low) return;
-    for (; un < units;) {
-        const int64_t lo = un * FC_STATE_BLOCK;
-        if (sc.skip) {
-            for (int e = 0; e < 8; ++e) {
-                const int64_t a = lo + lane + 32 * e;
-                if (a < N) store_low1(low, ltype, a, w[a]);
-            }
-        } else {
-            // element order of x[8]: of the lane's two groups where the unit
-            // is whole, lo + lane + 32 e where it is not
-            float mv[8], rv[8];
-            unsigned mtop = 0u, rtop = 0u;
-            if (whole) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int64_t a = lo + 4 * lane + 128 * i;
-                    float g[4];
-                    unpack4(u.g[i], g);
-                    from_e4m3(mq[i], ms, mv + 4 * i);
-                    from_e4m3(rq[i], rs, rv + 4 * i);
-                    float *wp = &w4[i].x;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = rv[4 * i + e] * rv[4 * i + e];
-                        rv[4 * i + e] = adam1(g[e], u.decay, h, sc, mv[4 * i + e], v, wp[e]);
-                    }
-                    __stcs(reinterpret_cast<float4 *>(w + a), w4[i]);
-                    if (low) store_low4(low, ltype, a, wp);
-                }
-            } else {
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t a = lo + lane + 32 * e;
-                    mv[e] = rv[e] = 0.f;
-                    if (a >= N) continue;
-                    const int sa = find_segment(tab, a);
-                    const float g = as_f32(static_cast<const GT *>(tab.ptr[sa])[a - tab.off[sa]]);
-                    float wi = w[a];
-                    const __half_raw hm = __nv_cvt_fp8_to_halfraw(m8[a], __NV_E4M3);
-                    const __half_raw hr = __nv_cvt_fp8_to_halfraw(r8[a], __NV_E4M3);
-                    mv[e] = __half2float(__half(hm)) * ms;
-                    const float r = __half2float(__half(hr)) * rs;
-                    float v = r * r;
-                    rv[e] = adam1(g, tab.decay[sa], h, sc, mv[e], v, wi);
-                    w[a] = wi;
-                    if (low) store_low1(low, ltype, a, wi);
-                }
-            }
-            // magnitudes compare as their bit patterns; a NaN is above all
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                mtop = max(mtop, __float_as_uint(mv[e]) & 0x7fffffffu);
-                rtop = max(rtop, __float_as_uint(rv[e]) & 0x7fffffffu);
-            }
-            mtop = __reduce_max_sync(0xffffffffu, mtop);
-            rtop = __reduce_max_sync(0xffffffffu, rtop);
-            float mto, mnew, rto, rnew;
-            block_scale(__uint_as_float(mtop), mto, mnew);
-            block_scale(__uint_as_float(rtop), rto, rnew);
-            if (lane == 0) {
-                __stcs(m_scale + un, mnew);
-                __stcs(r_scale + un, rnew);
-            }
-            if (whole) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int64_t a = lo + 4 * lane + 128 * i;
-                    const float *x = mv + 4 * i;
-                    __stcs(reinterpret_cast<unsigned *>(m8 + a),
-                           to_e4m3(x[0] * mto, x[1] * mto, x[2] * mto, x[3] * mto));
-                    const unsigned h0 = pair_bits(sc.key, a), h1 = pair_bits(sc.key, a + 2);
-                    const float *y = rv + 4 * i;
-                    __stcs(reinterpret_cast<unsigned *>(r8 + a),
-                           to_e4m3(stochastic_e4m3(y[0] * rto, h0 & 0xffffu),
-                                   stochastic_e4m3(y[1] * rto, h0 >> 16),
-                                   stochastic_e4m3(y[2] * rto, h1 & 0xffffu),
-                                   stochastic_e4m3(y[3] * rto, h1 >> 16)));
-                }
-            } else {
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t a = lo + lane + 32 * e;
-                    if (a >= N) continue;
-                    m8[a] = (uint8_t)to_e4m3(mv[e] * mto, 0.f, 0.f, 0.f);
-                    const unsigned hb = pair_bits(sc.key, a);
-                    const float q = stochastic_e4m3(rv[e] * rto, a & 1 ? hb >> 16 : hb & 0xffffu);
-                    r8[a] = (uint8_t)to_e4m3(q, 0.f, 0.f, 0.f);
-                }
-            }
+    unsigned arrived = 0;
+    if (threadIdx.x == 0 && !sc.skip) arrived = arrive_step(st.steps);
+    int s = 0;
+    uint32_t phase = 0;
+    for (int64_t it = 0; it < n; ++it) {
+        unsigned char *const stage = stages + (size_t)s * St::BYTES;
+        if (!mbar_wait(smem_u32(&bars[s]), phase, FC_ADAM_WAIT_NS)) {
+            if (lane == 0) atomicOr(reinterpret_cast<unsigned *>(st.steps) + 1, 0x80000000u);
+            return;
         }
-        un += stride;
-        if (un < units) load();
+        const int64_t un = unit(it);
+        const int64_t lo = un * FC_STATE_BLOCK;
+        const UnitGrad<GT> cur = next;
+        float ms = nms, rs = nrs;
+        if (it + 1 < n) load(unit(it + 1));
+        const int at = warp * 64 + lane;  // in groups of 4 elements
+        float4 *const sw = reinterpret_cast<float4 *>(stage) + at;
+        float w[8];
+        {
+            const float4 a = sw[0], b = sw[32];
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+        }
+        if (!sc.skip) {
+            if constexpr (BITS == 32) {
+                float4 *sm = reinterpret_cast<float4 *>(stage + St::WB) + at;
+                float4 *sv = reinterpret_cast<float4 *>(stage + St::WB + St::AB) + at;
+                float4 m4[2] = {sm[0], sm[32]}, v4[2] = {sv[0], sv[32]};
+                float g[8], d[8];
+                if (cur.whole) {
+                    unpack4(cur.g[0], g);
+                    unpack4(cur.g[1], g + 4);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[j] = cur.decay;
+                } else {
+                    gather_unit<GT>(tab, st.N, lo, lane, cur.sg, g, d);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    adam1(g[j], d[j], st.h, sc, (&m4[j >> 2].x)[j & 3], (&v4[j >> 2].x)[j & 3],
+                          w[j]);
+                sm[0] = m4[0];
+                sm[32] = m4[1];
+                sv[0] = v4[0];
+                sv[32] = v4[1];
+            } else {
+                uint32_t *qm = reinterpret_cast<uint32_t *>(stage + St::WB) + at;
+                uint32_t *qr =
+                    reinterpret_cast<uint32_t *>(stage + St::WB + St::AB) + at;
+                uint32_t mq[2] = {qm[0], qm[32]}, rq[2] = {qr[0], qr[32]};
+                float g[8];
+                if (cur.whole) {
+                    unpack4(cur.g[0], g);
+                    unpack4(cur.g[1], g + 4);
+                    adam8_unit<true>(g, &cur.decay, st.h, sc, lo + 4 * lane, w, mq, rq, ms, rs);
+                } else {
+                    float d[8];
+                    gather_unit<GT>(tab, st.N, lo, lane, cur.sg, g, d);
+                    adam8_unit<false>(g, d, st.h, sc, lo + 4 * lane, w, mq, rq, ms, rs);
+                }
+                qm[0] = mq[0];
+                qm[32] = mq[1];
+                qr[0] = rq[0];
+                qr[32] = rq[1];
+                if (lane == 0) {
+                    __stcs(st.m_scale + un, ms);
+                    __stcs(st.r_scale + un, rs);
+                }
+            }
+            sw[0] = make_float4(w[0], w[1], w[2], w[3]);
+            sw[32] = make_float4(w[4], w[5], w[6], w[7]);
+        }
+        if (st.low) {
+            store_low4(st.low, st.ltype, lo + 4 * lane, w);
+            store_low4(st.low, st.ltype, lo + 4 * lane + 128, w + 4);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars[S + s]));
+        if (++s == S) {
+            s = 0;
+            phase ^= 1;
+        }
     }
-}
-
-template <class F>
-static int units_grid(F kernel, int64_t N)
-{
-    const int64_t per = FC_ADAM_BLOCK / 32;
-    const int64_t ctas = ((N + FC_STATE_BLOCK - 1) / FC_STATE_BLOCK + per - 1) / per;
-    int grid = grid_for((const void *)kernel, FC_ADAM_BLOCK, 0, ctas);
-    if (ctas > grid) {  // as many rounds as needed, all of the same length
-        const int64_t rounds = (ctas + grid - 1) / grid;
-        grid = (int)((ctas + rounds - 1) / rounds);
+    // what is left behind the last whole tile, by the CTA with the fewest tiles
+    if (blockIdx.x == gridDim.x - 1) {
+        for (int64_t un = tiles * CW + warp; un * FC_STATE_BLOCK < st.N; un += CW) {
+            UnitRegs<BITS> u;
+            load_unit<GT, BITS>(tab, st, un, lane, u);
+            update_unit<BITS>(st, sc, un, lane, u);
+        }
     }
-    return grid;
+    if (threadIdx.x == 0 && !sc.skip) count_step(st.steps, arrived, sc.t);
 }
 
-template <class GT, class Tab>
-static cudaError_t launch_typed(const Tab &tab, int64_t N, const AdamHyper &h, const float *scale,
-                                float *w, void *low, int ltype, float *m, float *v,
-                                int32_t *steps, cudaStream_t s)
+// ---- launches ---------------------------------------------------------------------------
+
+// Passes the table by address: the launch copies it once into the launch's
+// own parameters.
+template <class Tab, class... Args>
+static cudaError_t launch_table(const void *kernel, unsigned grid, unsigned block, size_t smem,
+                                cudaStream_t s, const Tab &tab, const Args &...args)
 {
-    return launch_after_prior(k_adamw<GT, Tab>, (unsigned)units_grid(k_adamw<GT, Tab>, N),
-                              FC_ADAM_BLOCK, 0, s, tab, N, h, scale, w, low, ltype, m, v, steps);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *p[] = {const_cast<Tab *>(&tab), const_cast<Args *>(&args)...};
+    return cudaLaunchKernelExC(&cfg, kernel, p);
 }
 
-template <class GT, class Tab>
-static cudaError_t launch_typed8(const Tab &tab, int64_t N, const AdamHyper &h,
-                                 const float *scale, float *w, void *low, int ltype, uint8_t *m8,
-                                 float *m_scale, uint8_t *r8, float *r_scale, int32_t *steps,
-                                 uint64_t seed, cudaStream_t s)
+template <class GT, int BITS, class Tab>
+static cudaError_t launch_typed(const Tab &tab, const AdamState &st, cudaStream_t s)
 {
-    AdamHyper units = h;
-    units.eps *= FC_ADAM8_UNIT;
-    return launch_after_prior(k_adamw8<GT, Tab>, (unsigned)units_grid(k_adamw8<GT, Tab>, N),
-                              FC_ADAM_BLOCK, 0, s, tab, N, units, scale, w, low, ltype, m8, m_scale,
-                              r8, r_scale, steps, seed);
+    const int64_t units = (st.N + FC_STATE_BLOCK - 1) / FC_STATE_BLOCK;
+    const int64_t ctas = (units + FC_ADAM_BLOCK / 32 - 1) / (FC_ADAM_BLOCK / 32);
+    const void *direct = (const void *)k_adamw_direct<GT, BITS, Tab>;
+    const int resident = grid_for(direct, FC_ADAM_BLOCK, 0, INT64_MAX);
+    // The direct kernel serves what its resident CTAs take in one round (0.93M
+    // elements with fp32 moments, 1.2M with 8-bit ones).  Measured, direct
+    // against ring: 4.8 and 6.0 us at 0.8M elements, 7.7 and 6.4 us at 1.1M
+    // (fp32); 5.4 and 6.2 us at 1.1M, 9.3 and 6.4 us at 1.6M (8-bit).
+    if (ctas <= resident)
+        return launch_table(direct, (unsigned)ctas, FC_ADAM_BLOCK, 0, s, tab, st);
+    constexpr int CW = BITS == 32 ? FC_ADAM_CW32 : FC_ADAM_CW8;
+    constexpr int S = BITS == 32 ? FC_ADAM_S32 : FC_ADAM_S8;
+    static_assert(S >= 2 && S <= 32, "a stage is refilled while the next one is worked on");
+    using St = RingStage<BITS, CW>;
+    const size_t smem = (size_t)S * St::BYTES;
+    const int64_t tiles = st.N / St::T;
+    const void *ring = (const void *)k_adamw_ring<GT, BITS, CW, Tab>;
+    cudaError_t e =
+        cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = grid_for(ring, (CW + 1) * 32, smem, tiles);
+    return launch_table(ring, (unsigned)grid, (CW + 1) * 32, smem, s, tab, st, tiles, S);
+}
+
+template <int BITS, class Tab>
+static cudaError_t launch_bits(const Tab &tab, int gtype, const AdamState &st, cudaStream_t s)
+{
+    if (gtype == FC_TYPE_F32) return launch_typed<float, BITS>(tab, st, s);
+    if (gtype == FC_TYPE_F16) return launch_typed<__half, BITS>(tab, st, s);
+    return launch_typed<__nv_bfloat16, BITS>(tab, st, s);
 }
 
 template <class Tab>
@@ -582,11 +911,17 @@ cudaError_t launch_adamw(const Tab &tab, int gtype, int64_t N, const AdamHyper &
                          const float *scale, float *w, void *low, int ltype, float *m, float *v,
                          int32_t *steps, cudaStream_t s)
 {
-    if (gtype == FC_TYPE_F32)
-        return launch_typed<float>(tab, N, h, scale, w, low, ltype, m, v, steps, s);
-    if (gtype == FC_TYPE_F16)
-        return launch_typed<__half>(tab, N, h, scale, w, low, ltype, m, v, steps, s);
-    return launch_typed<__nv_bfloat16>(tab, N, h, scale, w, low, ltype, m, v, steps, s);
+    AdamState st = {};
+    st.N = N;
+    st.h = h;
+    st.scale = scale;
+    st.w = w;
+    st.low = low;
+    st.ltype = ltype;
+    st.m = m;
+    st.v = v;
+    st.steps = steps;
+    return launch_bits<32>(tab, gtype, st, s);
 }
 
 template <class Tab>
@@ -595,14 +930,21 @@ cudaError_t launch_adamw8(const Tab &tab, int gtype, int64_t N, const AdamHyper 
                           float *m_scale, uint8_t *r8, float *r_scale, int32_t *steps,
                           uint64_t seed, cudaStream_t s)
 {
-    if (gtype == FC_TYPE_F32)
-        return launch_typed8<float>(tab, N, h, scale, w, low, ltype, m8, m_scale, r8, r_scale,
-                                    steps, seed, s);
-    if (gtype == FC_TYPE_F16)
-        return launch_typed8<__half>(tab, N, h, scale, w, low, ltype, m8, m_scale, r8, r_scale,
-                                     steps, seed, s);
-    return launch_typed8<__nv_bfloat16>(tab, N, h, scale, w, low, ltype, m8, m_scale, r8, r_scale,
-                                        steps, seed, s);
+    AdamState st = {};
+    st.N = N;
+    st.h = h;
+    st.h.eps *= FC_ADAM8_UNIT;
+    st.scale = scale;
+    st.w = w;
+    st.low = low;
+    st.ltype = ltype;
+    st.m8 = m8;
+    st.r8 = r8;
+    st.m_scale = m_scale;
+    st.r_scale = r_scale;
+    st.steps = steps;
+    st.seed = seed;
+    return launch_bits<8>(tab, gtype, st, s);
 }
 
 #define FC_INST(Tab)                                                                            \

@@ -537,7 +537,8 @@ FC_API fc_status fc_adamw_step(const void *const *grads, int32_t grad_type, int3
  *   v = r^2,  b = i / FC_STATE_BLOCK.
  * The step is fc_adamw_step's, in fp32, and the weights see the new moments
  * before they are rounded.  Then, with M = the largest |m| and R the largest
- * sqrt(v) of the block (a block whose largest is below 2^-110 holds zeros):
+ * sqrt(v) of the block (a block whose largest is below 2^-110 holds zeros; 448 / M
+ * and 448 / R are formed as 448 times the reciprocal):
  *   exp_avg_scale = M / 448, exp_avg_q = e4m3 nearest to m * (448 / M);
  *   exp_rms_scale = R / 448, exp_rms_q = e4m3 value below or above
  *     y = sqrt(v) * (448 / R), above with the probability (to 16 bits) of how

@@ -236,6 +236,37 @@ def test_adamw_shifted_layers(shift, dtype, bits):
     check_step(layers(sizes, dtype, shift), sizes, bits, BF16, done=3)
 
 
+# vectors long enough for the streamed kernel: whole tiles only; a ragged end; layer
+# boundaries inside units, inside tiles and in the last units; many layers
+LONG = [[1 << 20], [(1 << 20) + 1], [1 << 20, 3000, 77], [700001, 13, 500000, 255, 4099],
+        [(1 << 21) + 2048 * 3 + 255], [9001] * 200, [1] * 300 + [1500000] + [3] * 300]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("k", range(len(LONG)))
+def test_adamw_long(k, dtype, bits):
+    check_step(layers(LONG[k], dtype, shift=k % 4, seed=k + 1), LONG[k], bits,
+               (F16, None, BF16)[k % 3], done=k)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("low", [None, F16])
+def test_adamw_long_skip(bits, low):
+    sizes = [700001, 13, 500000, 255, 4099]
+    grads = layers(sizes, F16)
+    grads[0][5] = math.inf
+    st = State(sum(sizes), bits, low, done=4)
+    before = st.copies()
+    st.step(fc.LayerGrads(grads), torch.tensor([math.nan], device="cuda"))
+    torch.cuda.synchronize()
+    after = st.copies()
+    for k in before:
+        assert torch.equal(before[k].view(torch.uint8), after[k].view(torch.uint8)), k
+    assert low is None or torch.equal(st.low, st.w.to(low))
+    st.check_guards()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 def test_adamw_reads_no_gradient_outside_a_layer(dtype, bits):
