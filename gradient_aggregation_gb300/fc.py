@@ -427,32 +427,44 @@ def fc_step_noalloc(grads, loss_scale: float, chunk: int, k: int, lr: float,
 
 
 # ---- training-step operators beside the aggregation -------------------------------
+#
+# Small calls are bound by the host, so these bindings look at each tensor once
+# and read the current stream without building a Stream object.
 
 _TYPES = {torch.float32: FC_TYPE_F32, torch.float16: FC_TYPE_F16, torch.bfloat16: FC_TYPE_BF16}
+_F32_ONLY = (torch.float32,)
+_I32_ONLY = (torch.int32,)
+_E4M3_ONLY = (torch.float8_e4m3fn,)
+_LOW = (torch.float16, torch.bfloat16)
+
+
+def _stream(stream, dev: int):
+    """Raw handle of `stream`, or of the current stream of GPU `dev`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) or None
+    return _s(stream)
 
 
 def _type(t: torch.Tensor, name: str) -> int:
-    try:
-        return _TYPES[t.dtype]
-    except KeyError:
-        raise ValueError("%s must be float32, float16 or bfloat16, not %s"
-                         % (name, t.dtype)) from None
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        raise ValueError("%s must be float32, float16 or bfloat16, not %s" % (name, t.dtype))
+    return kind
 
 
-def _on(t: torch.Tensor, dev: int, name: str) -> None:
-    if dev < 0 or t.get_device() != dev:
-        raise ValueError("%s must be on the GPU of the other tensors, not on %s"
-                         % (name, t.device))
+def _off(t: torch.Tensor, name: str) -> ValueError:
+    return ValueError("%s must be on the GPU of the other tensors, not on %s" % (name, t.device))
 
 
-def _flat(t: Optional[torch.Tensor], n: int, dtype, name: str, dev: int) -> Optional[int]:
-    """Address of a contiguous tensor of n elements of a type on a GPU (None stays)."""
+def _flat(t: Optional[torch.Tensor], n: int, dtypes, name: str, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor of n elements on GPU `dev` (None stays)."""
     if t is None:
         return None
-    _on(t, dev, name)
+    if t.get_device() != dev:
+        raise _off(t, name)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d elements" % (name, n))
-    if t.dtype is not dtype and (not isinstance(dtype, tuple) or t.dtype not in dtype):
+    if t.dtype not in dtypes:
         raise ValueError("%s must not be %s" % (name, t.dtype))
     return t.data_ptr()
 
@@ -466,25 +478,24 @@ class LayerGrads:
     def __init__(self, grads: Sequence[torch.Tensor], decay: Optional[Sequence[float]] = None):
         if not grads:
             raise ValueError("no layers")
-        self.type = _type(grads[0], "the gradients")
+        kind, dtype, self.dev = _type(grads[0], "the gradients"), grads[0].dtype, grads[0].get_device()
+        if self.dev < 0:
+            raise ValueError("the gradients must be on a GPU")
         for l, t in enumerate(grads):
-            if t.dtype != grads[0].dtype or not t.is_contiguous() or t.device != grads[0].device:
-                raise ValueError("gradient %d must be contiguous %s on %s"
-                                 % (l, grads[0].dtype, grads[0].device))
+            if t.dtype != dtype or not t.is_contiguous() or t.get_device() != self.dev:
+                raise ValueError("gradient %d must be contiguous %s on GPU %d" % (l, dtype, self.dev))
         if decay is not None and len(decay) != len(grads):
             raise ValueError("decay needs one factor for each of the %d layers" % len(grads))
-        self.dev = grads[0].get_device()
-        _on(grads[0], self.dev, "the gradients")
         self.L = len(grads)
-        self.sizes = [int(t.numel()) for t in grads]
+        self.sizes = [t.numel() for t in grads]
         self.N = sum(self.sizes)
+        self._keep = list(grads)
         self._ptrs = (ctypes.c_void_p * self.L)(*[t.data_ptr() for t in grads])
         self._sizes = _i64(self.sizes)
         self._decay = None if decay is None else (ctypes.c_float * self.L)(*decay)
-        self._keep = list(grads)
-        self.ptrs = ctypes.cast(self._ptrs, _P)
-        self.sizes_c = ctypes.cast(self._sizes, _P)
-        self.decay_c = None if decay is None else ctypes.cast(self._decay, _P)
+        # the leading arguments of the calls
+        self.head = (ctypes.addressof(self._ptrs), kind, self.L, ctypes.addressof(self._sizes))
+        self.decay = None if decay is None else ctypes.addressof(self._decay)
 
 
 def fc_grad_norm_workspace_size() -> int:
@@ -496,14 +507,15 @@ def fc_grad_norm(grads: LayerGrads, loss_scale: float, max_norm: float, norm: to
     """norm [1]: the global L2 norm of the layers over loss_scale; scale [1]:
     the factor the AdamW steps take (clipping at max_norm, 0 for none; NaN
     for a norm that is not finite).  workspace: zero-filled once."""
-    _on(workspace, grads.dev, "workspace")
-    _check(lib().fc_grad_norm(grads.ptrs, grads.type, grads.L, grads.sizes_c, loss_scale,
-                              max_norm, _flat(norm, 1, torch.float32, "norm", grads.dev),
-                              _flat(scale, 1, torch.float32, "scale", grads.dev), workspace.data_ptr(),
-                              workspace.nbytes, _s(stream)))
-
-
-_LOW = (torch.float16, torch.bfloat16)
+    dev = grads.dev
+    if workspace.get_device() != dev:
+        raise _off(workspace, "workspace")
+    st = (_lib or lib()).fc_grad_norm(
+        *grads.head, loss_scale, max_norm, _flat(norm, 1, _F32_ONLY, "norm", dev),
+        _flat(scale, 1, _F32_ONLY, "scale", dev), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def fc_adamw_step(grads: LayerGrads, grad_scale: Optional[torch.Tensor], lr: float, beta1: float,
@@ -511,15 +523,17 @@ def fc_adamw_step(grads: LayerGrads, grad_scale: Optional[torch.Tensor], lr: flo
                   weights_low: Optional[torch.Tensor], exp_avg: torch.Tensor,
                   exp_avg_sq: torch.Tensor, steps: torch.Tensor, stream=None) -> None:
     """One AdamW step in place on the fused weights and moments (fp32 [N])."""
-    n = grads.N
-    _check(lib().fc_adamw_step(
-        grads.ptrs, grads.type, grads.L, grads.sizes_c, grads.decay_c,
-        _flat(grad_scale, 1, torch.float32, "grad_scale", grads.dev), lr, beta1, beta2, eps, weight_decay,
-        _flat(weights, n, torch.float32, "weights", grads.dev), _flat(weights_low, n, _LOW, "weights_low", grads.dev),
+    n, dev = grads.N, grads.dev
+    st = (_lib or lib()).fc_adamw_step(
+        *grads.head, grads.decay, _flat(grad_scale, 1, _F32_ONLY, "grad_scale", dev), lr, beta1,
+        beta2, eps, weight_decay, _flat(weights, n, _F32_ONLY, "weights", dev),
+        _flat(weights_low, n, _LOW, "weights_low", dev),
         0 if weights_low is None else _TYPES[weights_low.dtype],
-        _flat(exp_avg, n, torch.float32, "exp_avg", grads.dev),
-        _flat(exp_avg_sq, n, torch.float32, "exp_avg_sq", grads.dev),
-        _flat(steps, 2, torch.int32, "steps", grads.dev), _s(stream)))
+        _flat(exp_avg, n, _F32_ONLY, "exp_avg", dev),
+        _flat(exp_avg_sq, n, _F32_ONLY, "exp_avg_sq", dev),
+        _flat(steps, 2, _I32_ONLY, "steps", dev), _stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def state_blocks(N: int) -> int:
@@ -533,46 +547,44 @@ def fc_adamw8_step(grads: LayerGrads, grad_scale: Optional[torch.Tensor], lr: fl
                    exp_avg_q: torch.Tensor, exp_avg_scale: torch.Tensor,
                    exp_rms_q: torch.Tensor, exp_rms_scale: torch.Tensor, steps: torch.Tensor,
                    seed: int, stream=None) -> None:
-    """fc_adamw_step with the moments held as float8_e4m3fn [N] and one fp32
-    scale a block; an e4m3 tensor may be longer than N (whole blocks)."""
-    n, b = grads.N, state_blocks(grads.N)
-    for q, name in ((exp_avg_q, "exp_avg_q"), (exp_rms_q, "exp_rms_q")):
-        _on(q, grads.dev, name)
-        if q.dtype != torch.float8_e4m3fn or not q.is_contiguous() or q.numel() < n:
-            raise ValueError("%s must be contiguous float8_e4m3fn of at least %d elements"
-                             % (name, n))
-    _check(lib().fc_adamw8_step(
-        grads.ptrs, grads.type, grads.L, grads.sizes_c, grads.decay_c,
-        _flat(grad_scale, 1, torch.float32, "grad_scale", grads.dev), lr, beta1, beta2, eps, weight_decay,
-        _flat(weights, n, torch.float32, "weights", grads.dev), _flat(weights_low, n, _LOW, "weights_low", grads.dev),
-        0 if weights_low is None else _TYPES[weights_low.dtype], exp_avg_q.data_ptr(),
-        _flat(exp_avg_scale, b, torch.float32, "exp_avg_scale", grads.dev), exp_rms_q.data_ptr(),
-        _flat(exp_rms_scale, b, torch.float32, "exp_rms_scale", grads.dev),
-        _flat(steps, 2, torch.int32, "steps", grads.dev), int(seed) & 0xFFFFFFFFFFFFFFFF, _s(stream)))
+    """fc_adamw_step with the moments held as float8_e4m3fn and one fp32 scale
+    a block; an e4m3 tensor has N elements or fills its last block."""
+    n, dev = grads.N, grads.dev
+    b = -(-n // FC_STATE_BLOCK)
+    nm = n if exp_avg_q.numel() == n else b * FC_STATE_BLOCK
+    nr = n if exp_rms_q.numel() == n else b * FC_STATE_BLOCK
+    st = (_lib or lib()).fc_adamw8_step(
+        *grads.head, grads.decay, _flat(grad_scale, 1, _F32_ONLY, "grad_scale", dev), lr, beta1,
+        beta2, eps, weight_decay, _flat(weights, n, _F32_ONLY, "weights", dev),
+        _flat(weights_low, n, _LOW, "weights_low", dev),
+        0 if weights_low is None else _TYPES[weights_low.dtype],
+        _flat(exp_avg_q, nm, _E4M3_ONLY, "exp_avg_q", dev),
+        _flat(exp_avg_scale, b, _F32_ONLY, "exp_avg_scale", dev),
+        _flat(exp_rms_q, nr, _E4M3_ONLY, "exp_rms_q", dev),
+        _flat(exp_rms_scale, b, _F32_ONLY, "exp_rms_scale", dev),
+        _flat(steps, 2, _I32_ONLY, "steps", dev), seed & 0xFFFFFFFFFFFFFFFF,
+        _stream(stream, dev))
+    if st:
+        _check(st)
 
 
-def _matrix(t: torch.Tensor, like: torch.Tensor, name: str) -> Tuple[int, int]:
-    """(address, elements between rows) of a matrix like `like` with contiguous rows."""
-    _on(t, like.get_device(), name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must have two dimensions and contiguous rows" % name)
-    if t.shape != like.shape or t.dtype != like.dtype:
-        raise ValueError("%s must be %s of %s" % (name, tuple(like.shape), like.dtype))
+def _matrix(t: torch.Tensor, shape, dtype, name: str, dev: int) -> Tuple[int, int]:
+    """(address, elements between rows) of a matrix with contiguous rows."""
+    if t.get_device() != dev or dev < 0:
+        raise _off(t, name)
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s of %s" % (name, tuple(shape), dtype))
+    between, inside = t.stride()
+    if inside != 1 and shape[1] > 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
     # the stride of a single row says nothing
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return t.data_ptr(), (between if shape[0] > 1 else shape[1])
 
 
-def _params(x: torch.Tensor, weight, bias) -> int:
-    """FC_TYPE_* of layer norm's parameters."""
-    kind = None
-    for p, name in ((weight, "weight"), (bias, "bias")):
-        if p is None:
-            continue
-        _flat(p, x.shape[1], (torch.float32, x.dtype), name, x.get_device())
-        if kind is not None and p.dtype != kind:
-            raise ValueError("weight and bias must have one type")
-        kind = p.dtype
-    return FC_TYPE_F32 if kind is None else _TYPES[kind]
+def _two(shape) -> Tuple[int, int]:
+    if len(shape) != 2:
+        raise ValueError("x must have two dimensions, not %d" % len(shape))
+    return shape
 
 
 def fc_layernorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor],
@@ -580,14 +592,26 @@ def fc_layernorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor],
                          mean: Optional[torch.Tensor] = None,
                          rstd: Optional[torch.Tensor] = None, stream=None) -> None:
     """Layer norm over the rows of x [rows, cols]; mean and rstd (fp32 [rows])
-    are what the backward pass needs."""
-    rows, cols = x.shape
-    px, ldx = _matrix(x, x, "x")
-    py, ldy = _matrix(y, x, "y")
-    _check(lib().fc_layernorm_forward(
-        px, rows, cols, ldx, _type(x, "x"), _p(weight), _p(bias), _params(x, weight, bias), eps,
-        py, ldy, _flat(mean, rows, torch.float32, "mean", x.get_device()),
-        _flat(rstd, rows, torch.float32, "rstd", x.get_device()), _s(stream)))
+    are what the backward pass needs.  weight and bias have one type: fp32 or
+    that of x."""
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    rows, cols = _two(shape)
+    kind = _type(x, "x")
+    px, ldx = _matrix(x, shape, dtype, "x", dev)
+    py, ldy = _matrix(y, shape, dtype, "y", dev)
+    pkind, params = FC_TYPE_F32, (torch.float32, dtype)
+    if weight is not None:
+        params = (weight.dtype,) if weight.dtype in params else params
+        pkind = _TYPES.get(weight.dtype)
+    elif bias is not None:
+        pkind = _TYPES.get(bias.dtype)
+    st = (_lib or lib()).fc_layernorm_forward(
+        px, rows, cols, ldx, kind, _flat(weight, cols, params, "weight", dev),
+        _flat(bias, cols, params, "bias", dev), pkind, eps, py, ldy,
+        _flat(mean, rows, _F32_ONLY, "mean", dev), _flat(rstd, rows, _F32_ONLY, "rstd", dev),
+        _stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def fc_layernorm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -600,24 +624,28 @@ def fc_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[to
                           workspace: Optional[torch.Tensor], stream=None) -> None:
     """Gradients of fc_layernorm_forward: dx, and the sums dweight and dbias
     over the rows (any of the three types, one for both; None: not wanted)."""
-    rows, cols = x.shape
-    px, ldx = _matrix(x, x, "x")
-    pdy, lddy = _matrix(dy, x, "dy")
-    pdx, lddx = _matrix(dx, x, "dx")
-    kind = FC_TYPE_F32
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    rows, cols = _two(shape)
+    kind = _type(x, "x")
+    px, ldx = _matrix(x, shape, dtype, "x", dev)
+    pdy, lddy = _matrix(dy, shape, dtype, "dy", dev)
+    pdx, lddx = _matrix(dx, shape, dtype, "dx", dev)
+    gkind, grads = FC_TYPE_F32, _F32_ONLY
     for t, name in ((dweight, "dweight"), (dbias, "dbias")):
         if t is not None:
-            kind = _type(t, name)
-            _flat(t, cols, t.dtype, name, x.get_device())
-    if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
-        raise ValueError("dweight and dbias must have one type")
-    if workspace is not None:
-        _on(workspace, x.get_device(), "workspace")
-    _check(lib().fc_layernorm_backward(
-        pdy, lddy, px, ldx, _type(x, "x"), _p(weight), _params(x, weight, None),
-        _flat(mean, rows, torch.float32, "mean", x.get_device()), _flat(rstd, rows, torch.float32, "rstd", x.get_device()),
-        rows, cols, pdx, lddx, _p(dweight), _p(dbias), kind, _p(workspace),
-        0 if workspace is None else workspace.nbytes, _s(stream)))
+            gkind, grads = _type(t, name), (t.dtype,)
+    if workspace is not None and workspace.get_device() != dev:
+        raise _off(workspace, "workspace")
+    st = (_lib or lib()).fc_layernorm_backward(
+        pdy, lddy, px, ldx, kind, _flat(weight, cols, (torch.float32, dtype), "weight", dev),
+        FC_TYPE_F32 if weight is None else _TYPES.get(weight.dtype),
+        _flat(mean, rows, _F32_ONLY, "mean", dev), _flat(rstd, rows, _F32_ONLY, "rstd", dev),
+        rows, cols, pdx, lddx, _flat(dweight, cols, grads, "dweight", dev),
+        _flat(dbias, cols, grads, "dbias", dev), gkind,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes, _stream(stream, dev))
+    if st:
+        _check(st)
 
 
 # ---- engine: device buffers for repeated steps ---------------------------------------
