@@ -74,15 +74,13 @@ template bool fill_table<TableL>(TableL &, const void *const *, int32_t,
 // selection and update kernels took it to 527 us, and the 7M-element steps
 // gained 1.5 us, with each kernel's own time unchanged.  At 100 % the update
 // kernel ran 15 % slower.
-#ifndef FC_CARVEOUT
-#define FC_CARVEOUT 50
-#endif
+// (FC_CARVEOUT in fc_internal.h; -1: no preference.)
 
 // SM count and resident blocks per SM are looked up once per (kernel,
 // device) and cached, so that later calls (for instance while a stream is
 // being captured into a CUDA graph) make no further runtime queries.  The
 // carveout preference is set at the same first lookup.
-int grid_for(const void *kernel, int block, size_t smem, int64_t work)
+int grid_for(const void *kernel, int block, size_t smem, int64_t work, int carveout)
 {
     struct Entry {
         const void *kernel;
@@ -107,10 +105,9 @@ int grid_for(const void *kernel, int block, size_t smem, int64_t work)
     if (blocks == 0) {
         int sms = 0, per_sm = 0;
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-#if FC_CARVEOUT >= 0
-        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             FC_CARVEOUT);
-#endif
+        if (carveout >= 0)
+            cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 carveout);
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block,
                                                           smem) != cudaSuccess ||
             per_sm < 1)

@@ -171,7 +171,13 @@ cudaError_t launch_after_prior(void (*kernel)(KArgs...), unsigned grid,
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+#ifndef FC_CARVEOUT
+#define FC_CARVEOUT 50
+#endif
+
 // Blocks to launch for a grid-stride kernel: min(work, SMs * resident).
-int grid_for(const void *kernel, int block, size_t smem, int64_t work);
+// carveout: the preferred share of shared memory in percent.
+int grid_for(const void *kernel, int block, size_t smem, int64_t work,
+             int carveout = FC_CARVEOUT);
 
 }  // namespace fc

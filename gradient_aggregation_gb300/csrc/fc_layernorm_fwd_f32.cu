@@ -1,0 +1,7 @@
+#include "fc_layernorm_fwd.cuh"
+
+namespace fc {
+
+template cudaError_t ln_forward<float>(const LnForward &, cudaStream_t);
+
+}  // namespace fc

@@ -362,7 +362,8 @@ size_t fc_layernorm_backward_workspace_size(int64_t rows, int64_t cols)
 {
     if (rows < 0 || cols < 1 || cols > ((int64_t)1 << 31)) return 0;
     const int64_t parts = ln_max_parts(rows, cols) < 1 ? 1 : ln_max_parts(rows, cols);
-    return (size_t)parts * (size_t)cols * 2 * sizeof(float);
+    // sets of column sums, rows of whole 32-byte groups
+    return (size_t)parts * (size_t)((cols + 7) / 8 * 8) * 2 * sizeof(float);
 }
 
 fc_status fc_layernorm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,

@@ -96,6 +96,50 @@ def test_odd_widths(cols, dtype):
     check(23, cols, dtype, ptype=dtype if cols % 3 else F32, eps=1e-3)
 
 
+# enough rows for the kernels that take many, at both sides of every width class, aligned
+# and with rows that start anywhere
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("cols", [136, 256, 260, 384, 512, 520, 768, 776, 1024, 1032, 1536, 1544,
+                                  2048, 2056, 3080, 4096, 4104, 6152, 8192, 8200, 12296, 16384])
+def test_many_rows_aligned(cols, dtype):
+    check(300000 // cols + 3, cols, dtype, ptype=dtype if cols % 3 else F32)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("cols,pad,shift", [
+    (129, 0, 0), (130, 1, 3), (255, 0, 1), (257, 0, 0), (333, 2, 5), (511, 0, 7), (513, 0, 0),
+    (770, 0, 0), (1001, 0, 0), (1001, 7, 0), (1025, 0, 2), (1537, 0, 0), (2049, 3, 1), (3073, 0, 0),
+    (4097, 0, 0), (6145, 0, 4), (8191, 0, 0), (8193, 0, 0), (12289, 0, 6), (16381, 1, 0),
+    (1000, 5, 0), (1024, 0, 1), (512, 3, 2)])
+def test_many_rows_anywhere(cols, pad, shift, dtype):
+    check(300000 // cols + 3, cols, dtype, pad, shift, ptype=F32 if cols % 3 else dtype,
+          pshift=shift % 2)
+
+
+def test_shifted_rows_read_nothing_outside_the_matrix():
+    """NaN before, between and behind the rows reaches no output."""
+    for dtype in TYPES:
+        for cols, pad, shift, rows in ((1001, 3, 1, 400), (515, 6, 3, 700), (133, 0, 5, 9)):
+            def poisoned(seed):
+                buf = torch.full((shift + rows * (cols + pad) + 16,), float("nan"), dtype=dtype,
+                                 device="cuda")
+                m = buf[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+                m.copy_(matrix(rows, cols, dtype, seed=seed)[0])
+                return m
+            x, dy = poisoned(1), poisoned(2)
+            w, b = params(cols, F32, 3)
+            y, dx = torch.empty_like(x.contiguous()), torch.empty_like(x.contiguous())
+            mu, rs = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+            dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+            ws = torch.empty(fc.fc_layernorm_backward_workspace_size(rows, cols),
+                             dtype=torch.uint8, device="cuda")
+            fc.fc_layernorm_forward(x, w, b, EPS, y, mu, rs)
+            fc.fc_layernorm_backward(dy, x, w, mu, rs, dx, dw, db, ws)
+            torch.cuda.synchronize()
+            for t in (y, mu, rs, dx, dw, db):
+                assert bool(t.isfinite().all())
+
+
 @pytest.mark.parametrize("rows", [1, 2, 3, 5, 17, 255, 1000, 5003])
 @pytest.mark.parametrize("cols", [64, 257, 1024])
 def test_row_counts(rows, cols):
