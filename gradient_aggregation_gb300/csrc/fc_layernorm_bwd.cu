@@ -10,9 +10,9 @@ extern template cudaError_t ln_backward<__half>(const LnBackward &, cudaStream_t
 extern template cudaError_t ln_backward<__nv_bfloat16>(const LnBackward &, cudaStream_t);
 
 // Adds `parts` sets of column sums; blockIdx.y: 0 for dweight, 1 for dbias.
-// 32 columns a block, each by 16 threads that take every 16th set, four
+// 32 columns a block, each by 32 threads that take every 32nd set, all their
 // loads in flight.
-#define FC_LN_JOIN 16
+#define FC_LN_JOIN 32
 
 __global__ void __launch_bounds__(32 * FC_LN_JOIN)
     k_ln_join(const float *__restrict__ partials, const int parts, const int64_t cols,
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(32 * FC_LN_JOIN)
     const float *p = partials + (int64_t)blockIdx.y * parts * padded + c;
     float s = 0.f;
     if (c < cols) {
-#pragma unroll 4
+#pragma unroll 10
         for (int i = q; i < parts; i += FC_LN_JOIN) s += __ldcg(p + i * padded);
     }
     sm[q][lane] = s;

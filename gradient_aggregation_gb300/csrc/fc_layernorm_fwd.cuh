@@ -21,22 +21,6 @@
 #include "fc_layernorm.cuh"
 #include "fc_pairs.cuh"
 
-#ifndef FC_LN_ANY_D
-#define FC_LN_ANY_D 3
-#endif
-#ifndef FC_LN_ANY_K
-#define FC_LN_ANY_K 4
-#endif
-#ifndef FC_LN_RW1
-#define FC_LN_RW1 4
-#endif
-#ifndef FC_LN_RW2
-#define FC_LN_RW2 4
-#endif
-#ifndef FC_LN_RW4
-#define FC_LN_RW4 2
-#endif
-
 namespace fc {
 
 // ---- many rows --------------------------------------------------------------------------------
@@ -517,7 +501,7 @@ static cudaError_t go_rows(const LnForward &a, cudaStream_t s)
 template <class T, int K, int TPR>
 static cudaError_t go_any(const LnForward &a, cudaStream_t s)
 {
-    constexpr int BLOCK = TPR >= 256 ? 512 : 256, D = FC_LN_ANY_D;
+    constexpr int BLOCK = TPR >= 256 ? 512 : 256, D = 3;
     const auto kernel = k_ln_fwd_any<T, K, TPR, BLOCK, D>;
     const size_t smem = (size_t)D * (BLOCK / 32) * warp_slots<K, true>() * 16 +
                         2 * sizeof(float) * (size_t)((a.cols + 255) & ~(int64_t)255);
@@ -534,10 +518,10 @@ static cudaError_t go_any(const LnForward &a, cudaStream_t s)
 template <class T>
 static cudaError_t many_rows(const LnForward &a, int64_t n, cudaStream_t s)
 {
-    if (n <= 32) return go_rows<T, 1, 32, FC_LN_RW1>(a, s);
-    if (n <= 64) return go_rows<T, 2, 32, FC_LN_RW2>(a, s);
+    if (n <= 32) return go_rows<T, 1, 32, 4>(a, s);
+    if (n <= 64) return go_rows<T, 2, 32, 4>(a, s);
     if (n <= 96) return go_rows<T, 3, 32, 2>(a, s);
-    if (n <= 128) return go_rows<T, 4, 32, FC_LN_RW4>(a, s);
+    if (n <= 128) return go_rows<T, 4, 32, 2>(a, s);
     if (n <= 192) return go_rows<T, 6, 32, 1>(a, s);
     if (n <= 256) return go_rows<T, 8, 32, 1>(a, s);
     if (n <= 384) return go_rows<T, 6, 64, 1>(a, s);
@@ -553,17 +537,10 @@ static cudaError_t many_rows_any(const LnForward &a, int64_t n, cudaStream_t s)
 {
     if (n <= 32) return go_any<T, 1, 32>(a, s);
     if (n <= 64) return go_any<T, 2, 32>(a, s);
-#if FC_LN_ANY_K == 4
     if (n <= 128) return go_any<T, 4, 32>(a, s);
     if (n <= 256) return go_any<T, 4, 64>(a, s);
     if (n <= 512) return go_any<T, 4, 128>(a, s);
     if (n <= 1024) return go_any<T, 4, 256>(a, s);
-#else
-    if (n <= 128) return go_any<T, 2, 64>(a, s);
-    if (n <= 256) return go_any<T, 2, 128>(a, s);
-    if (n <= 512) return go_any<T, 2, 256>(a, s);
-    if (n <= 1024) return go_any<T, 2, 512>(a, s);
-#endif
     return go_any<T, 4, 512>(a, s);
 }
 

@@ -76,8 +76,8 @@ fc_status check_layers(const void *const *grads, int32_t grad_type, int32_t L,
         if (sizes[l] < 0)
             return fail(FC_ERR_INVALID_ARG, "sizes[%d] = %lld < 0", l, (long long)sizes[l]);
         if (sizes[l] == 0) continue;
-        // the norm counts its tiles in 32 bits: 2^31 tiles of 4096 elements
-        if (sizes[l] > ((int64_t)1 << 42) || (N += sizes[l]) > ((int64_t)1 << 42))
+        // the norm counts its tiles in 32 bits: 2^31 tiles of 8 KB
+        if (sizes[l] > ((int64_t)1 << 41) || (N += sizes[l]) > ((int64_t)1 << 41))
             return fail(FC_ERR_INVALID_ARG, "sizes too large");
         if (!grads[l]) return fail(FC_ERR_INVALID_ARG, "grads[%d] is NULL", l);
         if ((uintptr_t)grads[l] & (align - 1))

@@ -47,7 +47,7 @@ struct AdamHyper {
 
 // partials: FF [FC_NORM_MAX_GRID]; done: zero on entry and on exit.
 #define FC_NORM_MAX_GRID 4096
-#define FC_NORM_TILE 16384  // bytes of gradient a block takes at a time
+#define FC_NORM_TILE 8192  // bytes of gradient a block takes at a time
 template <class Tab>
 cudaError_t launch_grad_norm(const Tab &tab, int gtype, float loss_scale, float max_norm,
                              FF *partials, unsigned *done, float *norm, float *scale,
