@@ -742,3 +742,91 @@ class Engine:
         self.residual.copy_(sd["residual"])
         self.velocity.copy_(sd["velocity"])
         self.weights.copy_(sd["weights"])
+
+
+class AdamWEngine:
+    """Owns the device state and scratch of repeated data-parallel AdamW steps.
+
+    One step sums W workers' fp16 layer gradients (scaled by ``loss_scale``)
+    into their mean, takes the mean's global norm, and applies AdamW with the
+    clip factor; a step whose norm is not finite changes nothing.
+
+    State (caller-visible tensors): ``weights`` (fp32 [N], fused layout),
+    ``weights_low`` (their 16-bit copy, if ``low`` names a type), ``steps``
+    (int32 [2]: steps applied), the moments (``exp_avg`` and ``exp_avg_sq``
+    for ``bits`` 32, ``exp_avg_q``, ``exp_avg_scale``, ``exp_rms_q`` and
+    ``exp_rms_scale`` for 8).  Per step: ``a`` (the mean gradient), ``norm``
+    and ``scale`` [1].  ``lr`` may be changed between steps.
+
+    The workers are summed in worker order (``order``: FC_ORDER_SEQUENTIAL or
+    FC_ORDER_RING).  FC_ORDER_TREE is refused: its staged kernel reports a lost
+    copy through the selection of chunks, which this step does not have.
+    """
+
+    STATE = {32: ("exp_avg", "exp_avg_sq"),
+             8: ("exp_avg_q", "exp_avg_scale", "exp_rms_q", "exp_rms_scale")}
+
+    def __init__(self, sizes: Sequence[int], W: int, weights: torch.Tensor, lr: float,
+                 loss_scale: float, betas: Tuple[float, float] = (0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: float = 0.01,
+                 decay: Optional[Sequence[float]] = None, max_norm: float = 0.0, bits: int = 32,
+                 low: Optional[torch.dtype] = None, seed: int = 0,
+                 order: int = FC_ORDER_SEQUENTIAL):
+        if bits not in self.STATE:
+            raise ValueError("bits must be 32 or 8, not %r" % (bits,))
+        if order not in (FC_ORDER_SEQUENTIAL, FC_ORDER_RING):
+            raise ValueError("order must be FC_ORDER_SEQUENTIAL or FC_ORDER_RING")
+        if low is not None and low not in _LOW:
+            raise ValueError("low must be float16 or bfloat16, not %s" % low)
+        dev = weights.device
+        self.sizes = [int(s) for s in sizes]
+        self.W, self.N, self.bits, self.order = int(W), sum(self.sizes), bits, order
+        if weights.numel() != self.N:
+            raise ValueError("weights must have %d elements" % self.N)
+        self.lr, self.betas, self.eps = float(lr), tuple(betas), float(eps)
+        self.weight_decay, self.loss_scale = float(weight_decay), float(loss_scale)
+        self.max_norm, self.seed = float(max_norm), int(seed)
+        self.weights = weights.detach().reshape(-1).to(torch.float32).clone()
+        self.weights_low = None if low is None else self.weights.to(low)
+        self.steps = torch.zeros(2, dtype=torch.int32, device=dev)
+        n, b = self.N, state_blocks(self.N)
+        if bits == 32:
+            self.exp_avg = torch.zeros(n, device=dev)
+            self.exp_avg_sq = torch.zeros(n, device=dev)
+        else:
+            self.exp_avg_q = torch.zeros(n, device=dev).to(torch.float8_e4m3fn)
+            self.exp_rms_q = torch.zeros(n, device=dev).to(torch.float8_e4m3fn)
+            self.exp_avg_scale = torch.zeros(b, device=dev)
+            self.exp_rms_scale = torch.zeros(b, device=dev)
+        self.a = torch.empty(n, device=dev)
+        self.norm, self.scale = torch.zeros(1, device=dev), torch.zeros(1, device=dev)
+        offsets, _ = fc_layout(self.sizes)
+        self.table = LayerGrads([self.a[o:o + s] for o, s in zip(offsets, self.sizes)], decay)
+        # zero-filled once; the calls leave their counters at zero
+        self._chunk = 4096
+        self._reduce_ws = torch.zeros(fc_step_workspace_size(n, self._chunk), dtype=torch.uint8,
+                                      device=dev)
+        self._norm_ws = torch.zeros(fc_grad_norm_workspace_size(), dtype=torch.uint8, device=dev)
+
+    def step(self, grads, stream=None) -> None:
+        fc_step_reduce_ordered(grads, self.loss_scale, self._chunk, None, self.a, self.order,
+                               self._reduce_ws, stream)
+        # the mean is unscaled already
+        fc_grad_norm(self.table, 1.0, self.max_norm, self.norm, self.scale, self._norm_ws, stream)
+        head = (self.table, self.scale, self.lr, *self.betas, self.eps, self.weight_decay,
+                self.weights, self.weights_low)
+        if self.bits == 32:
+            fc_adamw_step(*head, self.exp_avg, self.exp_avg_sq, self.steps, stream)
+        else:
+            fc_adamw8_step(*head, self.exp_avg_q, self.exp_avg_scale, self.exp_rms_q,
+                           self.exp_rms_scale, self.steps, self.seed, stream)
+
+    def state_dict(self) -> dict:
+        return {k: getattr(self, k).clone()
+                for k in ("weights", "steps") + self.STATE[self.bits]}
+
+    def load_state_dict(self, sd: dict) -> None:
+        for k in ("weights", "steps") + self.STATE[self.bits]:
+            getattr(self, k).copy_(sd[k])
+        if self.weights_low is not None:
+            self.weights_low.copy_(self.weights)
