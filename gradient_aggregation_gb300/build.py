@@ -3,6 +3,10 @@
 Every ``csrc/*.cu`` file is compiled for sm_103a in parallel with nvcc and
 linked into one shared library with the CUDA runtime linked statically (the
 library then needs only the driver at run time).  No CMake, no setuptools.
+
+Beside them ``csrc/fc_bind.cpp``, the tensor checks of the training-step
+operators' Python binding, becomes a Python module for the torch that is
+installed (``BIND_PATH``).  The library does not need it.
 """
 
 from __future__ import annotations
@@ -13,6 +17,9 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +28,10 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libfc.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
+BIND_SRC = os.path.join(CSRC, "fc_bind.cpp")
+# one for each Python and torch: the module is of no use to another
+BIND_PATH = os.path.join(OUT_DIR, "_fcbind.%s.torch-%s.so" % (
+    sys.implementation.cache_tag, torch.__version__.replace("+", "-")))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -54,9 +65,45 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _bind_command(target: str):
+    """The compiler call that makes the Python module."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("a C++ compiler is required to build the Python binding")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    home = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(home, "include"),
+           os.path.join(home, "include", "torch", "csrc", "api", "include"), cuda]
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+            *["-I" + d for d in inc], BIND_SRC, "-o", target,
+            "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+            "-lc10"]
+
+
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if needed) and return the path of libfc.so."""
+    """Compile (if needed) the library and the Python module beside it; returns
+    the path of libfc.so."""
     os.makedirs(OUT_DIR, exist_ok=True)
+    bind = None
+    if force or _stale(BIND_PATH, [BIND_SRC, os.path.join(INCLUDE, "fc.h"), __file__]):
+        part = BIND_PATH + ".tmp.%d" % os.getpid()
+        bind = subprocess.Popen(_bind_command(part), stdout=subprocess.PIPE,
+                                stderr=subprocess.STDOUT, text=True)
+    try:
+        _build_cuda(force, verbose)
+    finally:
+        if bind is not None:
+            out = bind.communicate()[0]
+    if bind is not None:
+        if bind.returncode != 0:
+            sys.stderr.write(out)
+            raise RuntimeError("building the Python binding failed")
+        os.replace(part, BIND_PATH)
+    return LIB_PATH
+
+
+def _build_cuda(force: bool, verbose: bool) -> str:
     srcs = _sources()
     hdrs = _headers()
     if not force and not _stale(LIB_PATH, srcs + hdrs + [__file__]):

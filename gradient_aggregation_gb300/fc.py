@@ -10,6 +10,7 @@ first call raises.  PyTorch provides device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import List, Optional, Sequence, Tuple
@@ -428,45 +429,38 @@ def fc_step_noalloc(grads, loss_scale: float, chunk: int, k: int, lr: float,
 
 # ---- training-step operators beside the aggregation -------------------------------
 #
-# Small calls are bound by the host, so these bindings look at each tensor once
-# and read the current stream without building a Stream object.
+# The checks of their tensors and the marshalling are in csrc/fc_bind.cpp: small
+# calls are bound by the host.
 
 _TYPES = {torch.float32: FC_TYPE_F32, torch.float16: FC_TYPE_F16, torch.bfloat16: FC_TYPE_BF16}
-_F32_ONLY = (torch.float32,)
-_I32_ONLY = (torch.int32,)
-_E4M3_ONLY = (torch.float8_e4m3fn,)
 _LOW = (torch.float16, torch.bfloat16)
+_bind = None
 
 
-def _stream(stream, dev: int):
-    """Raw handle of `stream`, or of the current stream of GPU `dev`."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev) or None
-    return _s(stream)
+def _load_bind():
+    """The module of csrc/fc_bind.cpp, connected to the loaded library."""
+    global _bind
+    handle = lib()
+    from . import build
+    with _lock:
+        if _bind is None:
+            if not os.path.exists(build.BIND_PATH):
+                raise RuntimeError("the Python binding is not built for this torch (%s); run "
+                                   "`python -m gradient_aggregation_gb300.build`"
+                                   % build.BIND_PATH)
+            spec = importlib.util.spec_from_file_location("_fcbind", build.BIND_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.connect(*[ctypes.cast(getattr(handle, name), _P).value for name in (
+                "fc_grad_norm", "fc_adamw_step", "fc_adamw8_step", "fc_layernorm_forward",
+                "fc_layernorm_backward")])
+            _bind = module
+    return _bind
 
 
-def _type(t: torch.Tensor, name: str) -> int:
-    kind = _TYPES.get(t.dtype)
-    if kind is None:
-        raise ValueError("%s must be float32, float16 or bfloat16, not %s" % (name, t.dtype))
-    return kind
-
-
-def _off(t: torch.Tensor, name: str) -> ValueError:
-    return ValueError("%s must be on the GPU of the other tensors, not on %s" % (name, t.device))
-
-
-def _flat(t: Optional[torch.Tensor], n: int, dtypes, name: str, dev: int) -> Optional[int]:
-    """Address of a contiguous tensor of n elements on GPU `dev` (None stays)."""
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise _off(t, name)
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with %d elements" % (name, n))
-    if t.dtype not in dtypes:
-        raise ValueError("%s must not be %s" % (name, t.dtype))
-    return t.data_ptr()
+def _raw(stream):
+    """None for the current stream of the tensors' GPU, or a raw handle."""
+    return None if stream is None else _s(stream) or 0
 
 
 class LayerGrads:
@@ -478,12 +472,14 @@ class LayerGrads:
     def __init__(self, grads: Sequence[torch.Tensor], decay: Optional[Sequence[float]] = None):
         if not grads:
             raise ValueError("no layers")
-        kind, dtype, self.dev = _type(grads[0], "the gradients"), grads[0].dtype, grads[0].get_device()
-        if self.dev < 0:
+        kind, dtype, dev = _TYPES.get(grads[0].dtype), grads[0].dtype, grads[0].get_device()
+        if kind is None:
+            raise ValueError("the gradients must be float32, float16 or bfloat16, not %s" % dtype)
+        if dev < 0:
             raise ValueError("the gradients must be on a GPU")
         for l, t in enumerate(grads):
-            if t.dtype != dtype or not t.is_contiguous() or t.get_device() != self.dev:
-                raise ValueError("gradient %d must be contiguous %s on GPU %d" % (l, dtype, self.dev))
+            if t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
+                raise ValueError("gradient %d must be contiguous %s on GPU %d" % (l, dtype, dev))
         if decay is not None and len(decay) != len(grads):
             raise ValueError("decay needs one factor for each of the %d layers" % len(grads))
         self.L = len(grads)
@@ -493,9 +489,9 @@ class LayerGrads:
         self._ptrs = (ctypes.c_void_p * self.L)(*[t.data_ptr() for t in grads])
         self._sizes = _i64(self.sizes)
         self._decay = None if decay is None else (ctypes.c_float * self.L)(*decay)
-        # the leading arguments of the calls
-        self.head = (ctypes.addressof(self._ptrs), kind, self.L, ctypes.addressof(self._sizes))
-        self.decay = None if decay is None else ctypes.addressof(self._decay)
+        # what the calls take: the arrays as addresses
+        self.packed = (ctypes.addressof(self._ptrs), kind, self.L, ctypes.addressof(self._sizes),
+                       0 if decay is None else ctypes.addressof(self._decay), self.N, dev)
 
 
 def fc_grad_norm_workspace_size() -> int:
@@ -507,13 +503,8 @@ def fc_grad_norm(grads: LayerGrads, loss_scale: float, max_norm: float, norm: to
     """norm [1]: the global L2 norm of the layers over loss_scale; scale [1]:
     the factor the AdamW steps take (clipping at max_norm, 0 for none; NaN
     for a norm that is not finite).  workspace: zero-filled once."""
-    dev = grads.dev
-    if workspace.get_device() != dev:
-        raise _off(workspace, "workspace")
-    st = (_lib or lib()).fc_grad_norm(
-        *grads.head, loss_scale, max_norm, _flat(norm, 1, _F32_ONLY, "norm", dev),
-        _flat(scale, 1, _F32_ONLY, "scale", dev), workspace.data_ptr(), workspace.nbytes,
-        _stream(stream, dev))
+    st = (_bind or _load_bind()).grad_norm(grads.packed, loss_scale, max_norm, norm, scale,
+                                           workspace, _raw(stream))
     if st:
         _check(st)
 
@@ -523,15 +514,9 @@ def fc_adamw_step(grads: LayerGrads, grad_scale: Optional[torch.Tensor], lr: flo
                   weights_low: Optional[torch.Tensor], exp_avg: torch.Tensor,
                   exp_avg_sq: torch.Tensor, steps: torch.Tensor, stream=None) -> None:
     """One AdamW step in place on the fused weights and moments (fp32 [N])."""
-    n, dev = grads.N, grads.dev
-    st = (_lib or lib()).fc_adamw_step(
-        *grads.head, grads.decay, _flat(grad_scale, 1, _F32_ONLY, "grad_scale", dev), lr, beta1,
-        beta2, eps, weight_decay, _flat(weights, n, _F32_ONLY, "weights", dev),
-        _flat(weights_low, n, _LOW, "weights_low", dev),
-        0 if weights_low is None else _TYPES[weights_low.dtype],
-        _flat(exp_avg, n, _F32_ONLY, "exp_avg", dev),
-        _flat(exp_avg_sq, n, _F32_ONLY, "exp_avg_sq", dev),
-        _flat(steps, 2, _I32_ONLY, "steps", dev), _stream(stream, dev))
+    st = (_bind or _load_bind()).adamw_step(grads.packed, grad_scale, lr, beta1, beta2, eps,
+                                            weight_decay, weights, weights_low, exp_avg,
+                                            exp_avg_sq, steps, _raw(stream))
     if st:
         _check(st)
 
@@ -549,42 +534,12 @@ def fc_adamw8_step(grads: LayerGrads, grad_scale: Optional[torch.Tensor], lr: fl
                    seed: int, stream=None) -> None:
     """fc_adamw_step with the moments held as float8_e4m3fn and one fp32 scale
     a block; an e4m3 tensor has N elements or fills its last block."""
-    n, dev = grads.N, grads.dev
-    b = -(-n // FC_STATE_BLOCK)
-    nm = n if exp_avg_q.numel() == n else b * FC_STATE_BLOCK
-    nr = n if exp_rms_q.numel() == n else b * FC_STATE_BLOCK
-    st = (_lib or lib()).fc_adamw8_step(
-        *grads.head, grads.decay, _flat(grad_scale, 1, _F32_ONLY, "grad_scale", dev), lr, beta1,
-        beta2, eps, weight_decay, _flat(weights, n, _F32_ONLY, "weights", dev),
-        _flat(weights_low, n, _LOW, "weights_low", dev),
-        0 if weights_low is None else _TYPES[weights_low.dtype],
-        _flat(exp_avg_q, nm, _E4M3_ONLY, "exp_avg_q", dev),
-        _flat(exp_avg_scale, b, _F32_ONLY, "exp_avg_scale", dev),
-        _flat(exp_rms_q, nr, _E4M3_ONLY, "exp_rms_q", dev),
-        _flat(exp_rms_scale, b, _F32_ONLY, "exp_rms_scale", dev),
-        _flat(steps, 2, _I32_ONLY, "steps", dev), seed & 0xFFFFFFFFFFFFFFFF,
-        _stream(stream, dev))
+    st = (_bind or _load_bind()).adamw8_step(grads.packed, grad_scale, lr, beta1, beta2, eps,
+                                             weight_decay, weights, weights_low, exp_avg_q,
+                                             exp_avg_scale, exp_rms_q, exp_rms_scale, steps,
+                                             seed, _raw(stream))
     if st:
         _check(st)
-
-
-def _matrix(t: torch.Tensor, shape, dtype, name: str, dev: int) -> Tuple[int, int]:
-    """(address, elements between rows) of a matrix with contiguous rows."""
-    if t.get_device() != dev or dev < 0:
-        raise _off(t, name)
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError("%s must be %s of %s" % (name, tuple(shape), dtype))
-    between, inside = t.stride()
-    if inside != 1 and shape[1] > 1:
-        raise ValueError("the rows of %s must be contiguous" % name)
-    # the stride of a single row says nothing
-    return t.data_ptr(), (between if shape[0] > 1 else shape[1])
-
-
-def _two(shape) -> Tuple[int, int]:
-    if len(shape) != 2:
-        raise ValueError("x must have two dimensions, not %d" % len(shape))
-    return shape
 
 
 def fc_layernorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor],
@@ -594,22 +549,8 @@ def fc_layernorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor],
     """Layer norm over the rows of x [rows, cols]; mean and rstd (fp32 [rows])
     are what the backward pass needs.  weight and bias have one type: fp32 or
     that of x."""
-    shape, dtype, dev = x.shape, x.dtype, x.get_device()
-    rows, cols = _two(shape)
-    kind = _type(x, "x")
-    px, ldx = _matrix(x, shape, dtype, "x", dev)
-    py, ldy = _matrix(y, shape, dtype, "y", dev)
-    pkind, params = FC_TYPE_F32, (torch.float32, dtype)
-    if weight is not None:
-        params = (weight.dtype,) if weight.dtype in params else params
-        pkind = _TYPES.get(weight.dtype)
-    elif bias is not None:
-        pkind = _TYPES.get(bias.dtype)
-    st = (_lib or lib()).fc_layernorm_forward(
-        px, rows, cols, ldx, kind, _flat(weight, cols, params, "weight", dev),
-        _flat(bias, cols, params, "bias", dev), pkind, eps, py, ldy,
-        _flat(mean, rows, _F32_ONLY, "mean", dev), _flat(rstd, rows, _F32_ONLY, "rstd", dev),
-        _stream(stream, dev))
+    st = (_bind or _load_bind()).layernorm_forward(x, weight, bias, eps, y, mean, rstd,
+                                                   _raw(stream))
     if st:
         _check(st)
 
@@ -624,26 +565,8 @@ def fc_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[to
                           workspace: Optional[torch.Tensor], stream=None) -> None:
     """Gradients of fc_layernorm_forward: dx, and the sums dweight and dbias
     over the rows (any of the three types, one for both; None: not wanted)."""
-    shape, dtype, dev = x.shape, x.dtype, x.get_device()
-    rows, cols = _two(shape)
-    kind = _type(x, "x")
-    px, ldx = _matrix(x, shape, dtype, "x", dev)
-    pdy, lddy = _matrix(dy, shape, dtype, "dy", dev)
-    pdx, lddx = _matrix(dx, shape, dtype, "dx", dev)
-    gkind, grads = FC_TYPE_F32, _F32_ONLY
-    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
-        if t is not None:
-            gkind, grads = _type(t, name), (t.dtype,)
-    if workspace is not None and workspace.get_device() != dev:
-        raise _off(workspace, "workspace")
-    st = (_lib or lib()).fc_layernorm_backward(
-        pdy, lddy, px, ldx, kind, _flat(weight, cols, (torch.float32, dtype), "weight", dev),
-        FC_TYPE_F32 if weight is None else _TYPES.get(weight.dtype),
-        _flat(mean, rows, _F32_ONLY, "mean", dev), _flat(rstd, rows, _F32_ONLY, "rstd", dev),
-        rows, cols, pdx, lddx, _flat(dweight, cols, grads, "dweight", dev),
-        _flat(dbias, cols, grads, "dbias", dev), gkind,
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.nbytes, _stream(stream, dev))
+    st = (_bind or _load_bind()).layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias,
+                                                    workspace, _raw(stream))
     if st:
         _check(st)
 
