@@ -24,8 +24,8 @@
 // Two kernels hold the same arithmetic: k_adamw_ring streams weights and
 // moments through shared memory with bulk copies in both directions;
 // k_adamw_direct loads and stores them from registers, which starts faster and
-// serves what is resident at once.  Measured (ring): 280 us for 62.4M elements
-// with fp32 moments, fp32 gradients and an fp16 copy (1.87 GB, 6.7 TB/s); 158
+// serves what is resident at once.  Measured (ring): 279 us for 62.4M elements
+// with fp32 moments, fp32 gradients and an fp16 copy (1.87 GB, 6.7 TB/s); 159
 // us with 8-bit moments and fp16 gradients (1.0 GB, 6.3 TB/s); direct: 3.9 us
 // for 133k elements.
 #include <cuda_fp8.h>
@@ -39,22 +39,15 @@ namespace fc {
 
 // Consumer warps of the ring kernel (so units a tile) and its stages.  A tile
 // of 20 units is copied in pieces of 20 KB; with 8 KB pieces the 62M-element
-// step with fp32 moments took 320 us, with 16 KB 286, with 20 KB 282.  With
-// 8-bit moments the update itself needs the warps: 24 of them and 4 stages
-// took 161 us, 16 took 171, 31 (3 stages) 164; 5 and 3 stages took 175 and
-// 177 us, 8 took 205.
-#ifndef FC_ADAM_CW32
+// step with fp32 moments took 320 us, with 16 KB 286, with 20 KB 279.  With
+// 8-bit moments the update itself needs the warps: 24 of them took 159 us, 23
+// 163, 20 189, 27 161.  Where gradients are shifted, 24 warps with 72 registers
+// are worse than 23 with 80: 27.8 and 26.3 us for 7M elements.
 #define FC_ADAM_CW32 20
-#endif
-#ifndef FC_ADAM_S32
 #define FC_ADAM_S32 3
-#endif
-#ifndef FC_ADAM_CW8
 #define FC_ADAM_CW8 24
-#endif
-#ifndef FC_ADAM_S8
+#define FC_ADAM_CW8_SHIFTED 23
 #define FC_ADAM_S8 4
-#endif
 
 struct AdamState {
     int64_t N;
@@ -249,33 +242,62 @@ __device__ __forceinline__ int find_segment(const Tab &t, int64_t f)
     return lo;
 }
 
-// The gradient of a unit that lies inside one segment.
-template <class GT>
+// The gradient of a unit that lies inside one segment.  SHIFTED: some segment
+// is shifted against the fused index; then both groups around a lane's four
+// elements are kept as they were loaded and selected when they are used, so
+// that no load is waited for before its unit's turn.
+template <class GT, bool SHIFTED>
 struct UnitGrad {
-    Raw4<GT> g[2];
+    Raw4<GT> g[SHIFTED ? 4 : 2];
     float decay;
-    int sg;      // segment of the unit's first element
-    bool whole;  // the unit is whole and inside that segment
+    int d;   // the segment's shift; -1: the unit is not whole
+    int sg;  // segment of the unit's first element
+    __device__ __forceinline__ void unpack(float *x) const
+    {
+        if constexpr (SHIFTED) {
+            Raw4<GT> a = g[0], b = g[2];
+            if (d) {
+                a.q = select4(a.q, g[1].q, d);
+                b.q = select4(b.q, g[3].q, d);
+            }
+            unpack4(a, x);
+            unpack4(b, x + 4);
+        } else {
+            unpack4(g[0], x);
+            unpack4(g[1], x + 4);
+        }
+    }
 };
 
-// Issues the gradient loads of the unit at `lo` if it is whole and inside one
-// segment; `sg` is moved on to the unit's first segment.
-template <class GT, class Tab>
+// Issues the gradient loads of the unit at `lo` if it is whole and lies inside
+// one segment together with the aligned groups around it; `sg` is moved on to
+// the unit's first segment.
+template <class GT, bool SHIFTED, class Tab>
 __device__ __forceinline__ void load_unit_grad(const Tab &tab, int64_t lo, int lane, int &sg,
-                                               UnitGrad<GT> &u)
+                                               UnitGrad<GT, SHIFTED> &u)
 {
     if (!(tab.off[sg] <= lo && lo < tab.off[sg + 1])) sg = find_segment(tab, lo);
-    const int64_t off = tab.off[sg], oend = tab.off[sg + 1];
+    const int64_t at = lo - tab.off[sg], len = tab.off[sg + 1] - tab.off[sg];
+    const GT *p = static_cast<const GT *>(tab.ptr[sg]) + at;
+    const int d = SHIFTED ? (int)(((uintptr_t)p / sizeof(GT)) & 3) : 0;
     u.sg = sg;
-    u.whole = lo + FC_STATE_BLOCK <= oend;
-    if (!u.whole) return;
-    const GT *first = static_cast<const GT *>(tab.ptr[sg]);
-    const GT *p = first + (lo - off) + 4 * lane;
-    const GT *end = first + (oend - off);
-    const int d = (int)(((uintptr_t)p / sizeof(GT)) & 3);
+    u.d = -1;
+    if (at < d || at + FC_STATE_BLOCK + (d ? 4 - d : 0) > len) return;
+    using Q = decltype(Raw4<GT>::q);
+    const Q *q = reinterpret_cast<const Q *>(p - d) + lane;
+    u.d = d;
     u.decay = tab.decay[sg];
-    u.g[0] = load4(p, first, end, d);
-    u.g[1] = load4(p + 128, first, end, d);
+    if constexpr (SHIFTED) {
+        u.g[0].q = __ldg(q);
+        u.g[2].q = __ldg(q + 32);
+        if (d) {
+            u.g[1].q = __ldg(q + 1);
+            u.g[3].q = __ldg(q + 33);
+        }
+    } else {
+        u.g[0].q = __ldcs(q);
+        u.g[1].q = __ldcs(q + 32);
+    }
 }
 
 // Gradient and decay of a lane's eight elements of any unit (0 past N), `sg`
@@ -669,7 +691,7 @@ struct RingStage {
     static constexpr int BYTES = WB + 2 * AB;
 };
 
-template <class GT, int BITS, int CW, class Tab>
+template <class GT, int BITS, int CW, bool SHIFTED, class Tab>
 __global__ void __launch_bounds__((CW + 1) * 32)
     k_adamw_ring(const __grid_constant__ Tab tab, const __grid_constant__ AdamState st,
                  const int64_t tiles, const int S)
@@ -740,11 +762,11 @@ __global__ void __launch_bounds__((CW + 1) * 32)
 
     // the consumers
     int sg = 0;
-    UnitGrad<GT> next;
+    UnitGrad<GT, SHIFTED> next;
     float nms = 0.f, nrs = 0.f;
     auto unit = [&](int64_t it) { return (blockIdx.x + it * gridDim.x) * CW + warp; };
     auto load = [&](int64_t un) {
-        load_unit_grad<GT>(tab, un * FC_STATE_BLOCK, lane, sg, next);
+        load_unit_grad(tab, un * FC_STATE_BLOCK, lane, sg, next);
         if constexpr (BITS == 8) {
             nms = __ldcs(st.m_scale + un);
             nrs = __ldcs(st.r_scale + un);
@@ -766,7 +788,7 @@ __global__ void __launch_bounds__((CW + 1) * 32)
         }
         const int64_t un = unit(it);
         const int64_t lo = un * FC_STATE_BLOCK;
-        const UnitGrad<GT> cur = next;
+        const UnitGrad<GT, SHIFTED> cur = next;
         float ms = nms, rs = nrs;
         if (it + 1 < n) load(unit(it + 1));
         const int at = warp * 64 + lane;  // in groups of 4 elements
@@ -783,9 +805,8 @@ __global__ void __launch_bounds__((CW + 1) * 32)
                 float4 *sv = reinterpret_cast<float4 *>(stage + St::WB + St::AB) + at;
                 float4 m4[2] = {sm[0], sm[32]}, v4[2] = {sv[0], sv[32]};
                 float g[8], d[8];
-                if (cur.whole) {
-                    unpack4(cur.g[0], g);
-                    unpack4(cur.g[1], g + 4);
+                if (cur.d >= 0) {
+                    cur.unpack(g);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) d[j] = cur.decay;
                 } else {
@@ -805,9 +826,8 @@ __global__ void __launch_bounds__((CW + 1) * 32)
                     reinterpret_cast<uint32_t *>(stage + St::WB + St::AB) + at;
                 uint32_t mq[2] = {qm[0], qm[32]}, rq[2] = {qr[0], qr[32]};
                 float g[8];
-                if (cur.whole) {
-                    unpack4(cur.g[0], g);
-                    unpack4(cur.g[1], g + 4);
+                if (cur.d >= 0) {
+                    cur.unpack(g);
                     adam8_unit<true>(g, &cur.decay, st.h, sc, lo + 4 * lane, w, mq, rq, ms, rs);
                 } else {
                     float d[8];
@@ -871,6 +891,34 @@ static cudaError_t launch_table(const void *kernel, unsigned grid, unsigned bloc
     return cudaLaunchKernelExC(&cfg, kernel, p);
 }
 
+// Whether the gradient of some whole unit starts off a boundary of 4 elements.
+template <class GT, class Tab>
+static bool any_shifted(const Tab &tab)
+{
+    for (int l = 0; l < tab.L; ++l)
+        if (tab.off[l + 1] - tab.off[l] >= FC_STATE_BLOCK &&
+            (((uintptr_t)tab.ptr[l] / sizeof(GT) - (uintptr_t)tab.off[l]) & 3))
+            return true;
+    return false;
+}
+
+template <class GT, int BITS, bool SHIFTED, class Tab>
+static cudaError_t launch_ring(const Tab &tab, const AdamState &st, cudaStream_t s)
+{
+    constexpr int CW = BITS == 32 ? FC_ADAM_CW32 : SHIFTED ? FC_ADAM_CW8_SHIFTED : FC_ADAM_CW8;
+    constexpr int S = BITS == 32 ? FC_ADAM_S32 : FC_ADAM_S8;
+    static_assert(S >= 2 && S <= 32, "a stage is refilled while the next one is worked on");
+    using St = RingStage<BITS, CW>;
+    const size_t smem = (size_t)S * St::BYTES;
+    const int64_t tiles = st.N / St::T;
+    const void *ring = (const void *)k_adamw_ring<GT, BITS, CW, SHIFTED, Tab>;
+    cudaError_t e =
+        cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = grid_for(ring, (CW + 1) * 32, smem, tiles);
+    return launch_table(ring, (unsigned)grid, (CW + 1) * 32, smem, s, tab, st, tiles, S);
+}
+
 template <class GT, int BITS, class Tab>
 static cudaError_t launch_typed(const Tab &tab, const AdamState &st, cudaStream_t s)
 {
@@ -884,18 +932,8 @@ static cudaError_t launch_typed(const Tab &tab, const AdamState &st, cudaStream_
     // (fp32); 5.4 and 6.2 us at 1.1M, 9.3 and 6.4 us at 1.6M (8-bit).
     if (ctas <= resident)
         return launch_table(direct, (unsigned)ctas, FC_ADAM_BLOCK, 0, s, tab, st);
-    constexpr int CW = BITS == 32 ? FC_ADAM_CW32 : FC_ADAM_CW8;
-    constexpr int S = BITS == 32 ? FC_ADAM_S32 : FC_ADAM_S8;
-    static_assert(S >= 2 && S <= 32, "a stage is refilled while the next one is worked on");
-    using St = RingStage<BITS, CW>;
-    const size_t smem = (size_t)S * St::BYTES;
-    const int64_t tiles = st.N / St::T;
-    const void *ring = (const void *)k_adamw_ring<GT, BITS, CW, Tab>;
-    cudaError_t e =
-        cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const int grid = grid_for(ring, (CW + 1) * 32, smem, tiles);
-    return launch_table(ring, (unsigned)grid, (CW + 1) * 32, smem, s, tab, st, tiles, S);
+    if (any_shifted<GT>(tab)) return launch_ring<GT, BITS, true>(tab, st, s);
+    return launch_ring<GT, BITS, false>(tab, st, s);
 }
 
 template <int BITS, class Tab>

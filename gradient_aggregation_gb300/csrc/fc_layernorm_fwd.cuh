@@ -544,9 +544,23 @@ static cudaError_t many_rows_any(const LnForward &a, int64_t n, cudaStream_t s)
     return go_any<T, 4, 512>(a, s);
 }
 
-#ifndef FC_LN_FEW
-#define FC_LN_FEW (1 << 18)
-#endif
+// Few rows: what counts is the latency of a row, so a row is spread over as many
+// threads as it has vectors (or four elements a thread), and no ring and no
+// copy of the parameters is set up first.  Where that ends is measured, few
+// against many in us: rows of vectors, 1 MB of 256 columns 1.85 and 2.44
+// (bf16), 2.50 and 2.47 (fp32), and 2 MB 3.02 and 2.49, 3.12 and 2.48; of 1024
+// columns 2 MB 2.93 and 3.49 (bf16), 3.04 and 2.51 (fp32), 4 MB 3.65 and 3.58
+// (bf16); of 2048 columns 2 MB 2.49 and 2.89 and 4 MB 3.75 and 2.99 (fp32), 4
+// MB 4.29 and 4.40 (bf16).  Rows word by word, 523 of 1001 columns 3.91 and 3.78
+// (bf16), 3.48 and 3.35 (fp32); 1047 rows 4.93 and 3.84, 4.45 and 4.01; 524 of
+// 2001 columns 4.79 and 4.91, 4.37 and 4.80.
+template <class T>
+static bool few_rows(int64_t rows, int64_t n, bool vectors)
+{
+    if (!vectors) return rows <= 512;
+    const int shift = sizeof(T) == 2 ? (n > 64 ? 18 : 16) : (n > 256 ? 17 : 16);
+    return rows * n <= (int64_t)1 << shift;
+}
 
 template <class T>
 cudaError_t ln_forward(const LnForward &a, cudaStream_t s)
@@ -558,7 +572,7 @@ cudaError_t ln_forward(const LnForward &a, cudaStream_t s)
     const bool pvec = ((uintptr_t)a.weight & 15) == 0 && ((uintptr_t)a.bias & 15) == 0;
     const int64_t c = a.cols, n = (c + V - 1) / V;
     const bool vectors = c % V == 0 && on16(a.x, a.ldx) && on16(a.y, a.ldy);
-    const bool few = a.rows * n <= FC_LN_FEW / V;
+    const bool few = few_rows<T>(a.rows, n, vectors);
     if (n > 2048) {
         const auto wide = k_ln_fwd_wide<T>;
         const int grid = grid_for((const void *)wide, FC_LN_WIDE_BLOCK, 0, a.rows);
