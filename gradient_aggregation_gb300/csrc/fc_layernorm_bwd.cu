@@ -37,12 +37,7 @@ __global__ void __launch_bounds__(32 * FC_LN_JOIN)
         s = 0.f;
 #pragma unroll
         for (int i = 0; i < FC_LN_JOIN; ++i) s += sm[i][lane];
-        if (gtype == FC_TYPE_F32)
-            static_cast<float *>(out)[c] = s;
-        else if (gtype == FC_TYPE_F16)
-            static_cast<__half *>(out)[c] = __float2half_rn(s);
-        else
-            static_cast<__nv_bfloat16 *>(out)[c] = __float2bfloat16_rn(s);
+        store_sum(out, gtype, c, s);
     }
 }
 

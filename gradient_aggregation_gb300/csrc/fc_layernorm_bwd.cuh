@@ -8,12 +8,14 @@
 // cost one shuffle reduction and, where a row spans several warps, one
 // exchange and one barrier.  A thread owns the same columns in every row, so
 // the column sums stay in its registers until its block has no more rows; each
-// block then leaves one set of sums, and a second kernel adds the sets in
-// their order (no atomics: the same inputs give the same bits).
+// block then leaves one set of sums, and a second kernel (for few narrow rows
+// the same one, as a cluster) adds the sets in their order (no atomics: the same
+// inputs give the same bits).
 #pragma once
 
 #include <algorithm>
 
+#include "fc_cluster.cuh"
 #include "fc_layernorm.cuh"
 #include "fc_pairs.cuh"
 
@@ -24,13 +26,50 @@ __host__ __device__ __forceinline__ int64_t ln_padded(int64_t cols) { return (co
 
 cudaError_t ln_join(const LnBackward &a, int parts, cudaStream_t s);
 
-template <class T, int VEC, int K, int TPR, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) k_ln_bwd(const LnBackward a, const bool pvec)
+__device__ __forceinline__ void store_sum(void *out, int gtype, int64_t c, float s)
 {
-    constexpr int G = BLOCK / TPR;
-    constexpr int WARPS = TPR > 32 ? TPR / 32 : 1;
-    constexpr bool HOLD = K * VEC <= 8;
-    __shared__ float2 part[2][G][WARPS];
+    if (gtype == FC_TYPE_F32)
+        static_cast<float *>(out)[c] = s;
+    else if (gtype == FC_TYPE_F16)
+        static_cast<__half *>(out)[c] = __float2half_rn(s);
+    else
+        static_cast<__nv_bfloat16 *>(out)[c] = __float2bfloat16_rn(s);
+}
+
+// Few narrow rows: the grid is one cluster, whose CTAs add the sets of column
+// sums that they have just left in the workspace, a slice of the columns each.
+// (Reading the sets from the other CTAs' shared memory instead took 0.4 to 0.7 us
+// more for 256 to 1024 columns.)
+#define FC_LN_CLUSTER 8
+
+template <int BLOCK>
+__device__ __forceinline__ void join_in_cluster(const LnBackward &a)
+{
+    cluster_sync();
+    const int cols = (int)a.cols, parts = (int)gridDim.x;
+    const int64_t padded = ln_padded(a.cols);
+    for (int i = blockIdx.x * BLOCK + threadIdx.x; i < 2 * cols; i += parts * BLOCK) {
+        const int which = i >= cols, c = which ? i - cols : i;
+        void *const out = which ? a.dbias : a.dweight;
+        if (!out) continue;
+        const float *const p = a.partials + which * parts * padded + c;
+        float v[FC_LN_CLUSTER], s = 0.f;
+#pragma unroll
+        for (int q = 0; q < FC_LN_CLUSTER; ++q) v[q] = q < parts ? __ldcg(p + q * padded) : 0.f;
+#pragma unroll
+        for (int q = 0; q < FC_LN_CLUSTER; ++q) s += v[q];
+        store_sum(out, a.gtype, c, s);
+    }
+}
+
+// Rows of at most 128 columns: TPR lanes of a warp hold a row, several rows a
+// warp; the next row is loaded while one is worked on.
+template <class T, int VEC, int K, int TPR, int BLOCK>
+__global__ void __launch_bounds__(BLOCK)
+    k_ln_bwd(const LnBackward a, const bool pvec, const bool joins)
+{
+    constexpr int G = BLOCK / TPR, W = TPR * K * VEC;
+    __shared__ float sums[2][G][W];
     wait_for_prior_grid();
     allow_dependent_launch();
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
@@ -43,18 +82,14 @@ __global__ void __launch_bounds__(BLOCK) k_ln_bwd(const LnBackward a, const bool
     const int64_t stride = (int64_t)gridDim.x * G;
     int64_t row = (int64_t)blockIdx.x * G + g;
 
-    float pw[HOLD ? K : 1][VEC];
-    if constexpr (HOLD) {
+    float pw[K][VEC], dw[K][VEC], db[K][VEC];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (t + k * TPR < nvec)
-                load_params<T, VEC>(a.weight, a.ptype, pvec, (t + k * TPR) * VEC, 1.f, pw[k]);
-    }
-    float dw[K][VEC], db[K][VEC];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+        if (t + k * TPR < nvec)
+            load_params<T, VEC>(a.weight, a.ptype, pvec, (t + k * TPR) * VEC, 1.f, pw[k]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
+    }
 
     Vec<T, VEC> nx[K], ny[K];
     float nmean = 0.f, nrstd = 0.f;
@@ -76,8 +111,7 @@ __global__ void __launch_bounds__(BLOCK) k_ln_bwd(const LnBackward a, const bool
     };
     load(row);
     const int64_t rounds = (a.rows + stride - 1) / stride;
-    int buf = 0;
-    for (int64_t it = 0; it < rounds; ++it, row += stride, buf ^= 1) {
+    for (int64_t it = 0; it < rounds; ++it, row += stride) {
         Vec<T, VEC> vx[K], vy[K];
         const float mean = nmean, rstd = nrstd;
 #pragma unroll
@@ -90,19 +124,13 @@ __global__ void __launch_bounds__(BLOCK) k_ln_bwd(const LnBackward a, const bool
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (t + k * TPR < nvec) {
-                float fx[VEC], fy[VEC], w[VEC];
+                float fx[VEC], fy[VEC];
                 vx[k].get(fx);
                 vy[k].get(fy);
-                if constexpr (HOLD) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) w[e] = pw[k][e];
-                } else {
-                    load_params<T, VEC>(a.weight, a.ptype, pvec, (t + k * TPR) * VEC, 1.f, w);
-                }
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float h = (fx[e] - mean) * rstd;
-                    const float q = fy[e] * w[e];
+                    const float q = fy[e] * pw[k][e];
                     s1 += q;
                     s2 = fmaf(q, h, s2);
                     dw[k][e] = fmaf(fy[e], h, dw[k][e]);
@@ -110,75 +138,44 @@ __global__ void __launch_bounds__(BLOCK) k_ln_bwd(const LnBackward a, const bool
                 }
             }
         }
-        s1 = lanes_sum<TPR>(s1);
-        s2 = lanes_sum<TPR>(s2);
-        if constexpr (WARPS > 1) {
-            if ((t & 31) == 0) part[buf][g][t >> 5] = make_float2(s1, s2);
-            group_sync<TPR, BLOCK>(g);
-            const float2 p = part[buf][g][threadIdx.x & (WARPS - 1)];
-            s1 = lanes_sum<WARPS>(p.x);
-            s2 = lanes_sum<WARPS>(p.y);
-        }
-        s1 *= inv_n;
-        s2 *= inv_n;
+        s1 = lanes_sum<TPR>(s1) * inv_n;
+        s2 = lanes_sum<TPR>(s2) * inv_n;
         if (row < a.rows) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (t + k * TPR < nvec) {
-                    const int c = (t + k * TPR) * VEC;
-                    float fx[VEC], fy[VEC], w[VEC];
+                    float fx[VEC], fy[VEC];
                     vx[k].get(fx);
                     vy[k].get(fy);
-                    if constexpr (HOLD) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) w[e] = pw[k][e];
-                    } else {
-                        load_params<T, VEC>(a.weight, a.ptype, pvec, c, 1.f, w);
-                    }
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         const float h = (fx[e] - mean) * rstd;
-                        fx[e] = rstd * (fmaf(fy[e], w[e], -s1) - h * s2);
+                        fx[e] = rstd * (fmaf(fy[e], pw[k][e], -s1) - h * s2);
                     }
-                    Vec<T, VEC>::store(dx + row * a.lddx + c, fx);
+                    Vec<T, VEC>::store(dx + row * a.lddx + (t + k * TPR) * VEC, fx);
                 }
             }
         }
     }
     if (!a.partials) return;
-    float *pdw = a.partials + blockIdx.x * ln_padded(cols);
-    float *pdb = pdw + gridDim.x * ln_padded(cols);
-    if constexpr (G == 1) {
+    // the row groups of the block are added in their order
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (t + k * TPR < nvec)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    pdw[(t + k * TPR) * VEC + e] = dw[k][e];
-                    pdb[(t + k * TPR) * VEC + e] = db[k][e];
-                }
-    } else {
-        // the row groups of the block are added in their order
-        __shared__ float sw[TPR * K * VEC], sb[TPR * K * VEC];
-        for (int r = 0; r < G; ++r) {
-            __syncthreads();
-            if (g == r) {
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const int c = (t + k * TPR) * VEC + e;
-                        sw[c] = r ? sw[c] + dw[k][e] : dw[k][e];
-                        sb[c] = r ? sb[c] + db[k][e] : db[k][e];
-                    }
-            }
+        for (int e = 0; e < VEC; ++e) {
+            sums[0][g][(t + k * TPR) * VEC + e] = dw[k][e];
+            sums[1][g][(t + k * TPR) * VEC + e] = db[k][e];
         }
-        __syncthreads();
-        for (int c = threadIdx.x; c < cols; c += BLOCK) {
-            pdw[c] = sw[c];
-            pdb[c] = sb[c];
-        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * W; i += BLOCK) {
+        const int which = i / W, c = i % W;
+        float v = sums[which][0][c];
+#pragma unroll
+        for (int r = 1; r < G; ++r) v += sums[which][r][c];
+        if (c < cols)
+            a.partials[(which * (int64_t)gridDim.x + blockIdx.x) * ln_padded(cols) + c] = v;
     }
+    if (joins) join_in_cluster<BLOCK>(a);
 }
 
 // ---- rows of more than 128 columns ----------------------------------------------------------
@@ -202,7 +199,7 @@ __global__ void __launch_bounds__(BLOCK) k_ln_bwd(const LnBackward a, const bool
 // into registers 197 / 161 / 178 / 200 us.
 template <class T, int K, int TPR, int BLOCK, int D, bool ANY>
 __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
-    k_ln_bwd_ring(const LnBackward a, const bool pvec)
+    k_ln_bwd_ring(const LnBackward a, const bool pvec, const bool joins)
 {
     constexpr int VEC = 16 / (int)sizeof(T), NP = K * VEC / 2;
     constexpr int G = BLOCK / TPR, WARPS = TPR / 32, STEP = pair_step<T>();
@@ -380,6 +377,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
         reinterpret_cast<float4 *>(a.partials)[(which * (int64_t)gridDim.x + blockIdx.x) *
                                                    (padded / 4) + q] = v;
     }
+    if (joins) join_in_cluster<BLOCK>(a);
 }
 
 // Rows wider than the registers hold: one block a row, two passes over it.
@@ -446,15 +444,57 @@ __global__ void __launch_bounds__(128) k_ln_colsum_wide(const LnBackward a)
 
 // ---- launches -------------------------------------------------------------------------------
 
+// CTAs of the one cluster that serves the call, if a CTA takes `group` rows at
+// a time, or 0 if the sums are joined by a launch of their own.  For rows of up
+// to 32 vectors (64 where they are aligned).  One launch saves 1.6 us of host
+// time a call (5.0 and 3.4 us); on the GPU, two launches and one, in us: 64
+// columns, bf16 3.0 and 2.5 for 128 rows, 3.2 and 3.3 for 512; 256 columns,
+// bf16 3.4 and 3.4 for 128 rows, 3.5 and 4.2 for 256, fp32 3.1 and 3.6 for 128
+// rows, 3.2 and 4.2 for 256; 1024 fp32 columns 3.1 and 3.7 for 8 rows, 3.3 and
+// 4.2 for 64.
+#define FC_LN_ONE_ROWS 128
+
+inline int joining_ctas(const LnBackward &a, int group)
+{
+    if (!a.partials || a.rows > FC_LN_ONE_ROWS) return 0;
+    int ctas = 1;
+    while (ctas < FC_LN_CLUSTER && ctas * group < a.rows && 2 * ctas <= a.rows) ctas *= 2;
+    return ctas;
+}
+
+// A launch of `grid` blocks as one cluster.
+template <class... KArgs, class... Args>
+static cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, unsigned block, size_t smem,
+                                  cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)grid;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 template <class T, int VEC, int K, int TPR, int BLOCK>
 static cudaError_t go(const LnBackward &a, bool pvec, cudaStream_t s)
 {
+    if (const int ctas = joining_ctas(a, BLOCK / TPR))
+        return launch_cluster(k_ln_bwd<T, VEC, K, TPR, BLOCK>, ctas, BLOCK, 0, s, a, pvec, true);
     const auto kernel = k_ln_bwd<T, VEC, K, TPR, BLOCK>;
     const int64_t ctas = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
     int grid = grid_for((const void *)kernel, BLOCK, 0, ctas);
     const int64_t most = ln_max_parts(a.rows, a.cols);
     if (grid > most) grid = (int)most;
-    cudaError_t e = launch_after_prior(kernel, (unsigned)grid, BLOCK, 0, s, a, pvec);
+    cudaError_t e = launch_after_prior(kernel, (unsigned)grid, BLOCK, 0, s, a, pvec, false);
     return e != cudaSuccess ? e : ln_join(a, grid, s);
 }
 
@@ -482,8 +522,13 @@ struct RingLaunch {
         const int64_t most = std::min<int64_t>(resident, ln_max_parts(a.rows, a.cols));
         const int grid = (int)std::min(ctas, most);
         cudaError_t e = launch_after_prior(k_ln_bwd_ring<T, K, TPR, BLOCK, D, ANY>, (unsigned)grid,
-                                           BLOCK, smem, s, a, pvec);
+                                           BLOCK, smem, s, a, pvec, false);
         return e != cudaSuccess ? e : ln_join(a, grid, s);
+    }
+    cudaError_t run_cluster(const LnBackward &a, bool pvec, int n, cudaStream_t s) const
+    {
+        return launch_cluster(k_ln_bwd_ring<T, K, TPR, BLOCK, D, ANY>, n, BLOCK, smem, s, a, pvec,
+                              true);
     }
 };
 
@@ -495,6 +540,13 @@ template <class T, int K, int TPR, bool ANY>
 static cudaError_t go_ring(const LnBackward &a, bool pvec, cudaStream_t s)
 {
     constexpr int SMALL = TPR == 512 ? 512 : 256, LARGE = K == 1 ? 256 : 512;
+    if constexpr (K <= (ANY ? 1 : 2) && TPR == 32) {
+        if (const int ctas = joining_ctas(a, LARGE / TPR)) {
+            RingLaunch<T, K, TPR, LARGE, ANY> one;
+            cudaError_t e = one.prepare(a);
+            return e != cudaSuccess ? e : one.run_cluster(a, pvec, ctas, s);
+        }
+    }
     RingLaunch<T, K, TPR, SMALL, ANY> small;
     cudaError_t e = small.prepare(a);
     if (e != cudaSuccess) return e;
