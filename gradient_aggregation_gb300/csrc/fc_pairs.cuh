@@ -50,27 +50,7 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b)
     return r;
 }
 
-// The pairs of a 16-byte vector: 4 of a 16-bit type, 2 of fp32.
-template <class T>
-__device__ __forceinline__ void to_pairs(const uint4 &q, F2 (&f)[8 / sizeof(T)])
-{
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    if constexpr (sizeof(T) == 4) {
-        f[0] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-        f[1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (__is_same(T, __half)) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                f[i] = f2(v.x, v.y);
-            } else {
-                f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-            }
-        }
-    }
-}
-
+// A 16-byte vector of its pairs: 4 of a 16-bit type, 2 of fp32, each rounded once.
 template <class T>
 __device__ __forceinline__ uint4 from_pairs(const F2 (&f)[8 / sizeof(T)])
 {

@@ -61,8 +61,9 @@
  *  - Inputs are assumed finite (no inf/NaN in the gradients).
  *  - On error nothing is launched and fc_last_error() describes the cause.
  *  - No kernel waits on the host.  Only the cooperative one-launch step's
- *    CTAs wait on one another (all resident by the cooperative launch), and
- *    every wait on the device is bounded (2 s), so no call can hang.
+ *    CTAs wait on one another through memory (all resident by the cooperative
+ *    launch), and every such wait, and every wait for a copy into shared
+ *    memory, is bounded (2 s), so no call can hang.
  */
 #ifndef FC_H_
 #define FC_H_
@@ -517,7 +518,9 @@ FC_API fc_status fc_grad_norm(const void *const *grads, int32_t grad_type, int32
  *               NULL; 16-byte aligned.
  *  steps        device int32 [2], zero-filled at the start of training:
  *               steps[0] counts the steps applied, steps[1] belongs to the
- *               kernel (zero between calls).
+ *               kernel (zero between calls).  steps[1] < 0 after a call says
+ *               that a bounded wait of the kernel ran out (not expected): the
+ *               state is updated in part and no further step is counted.
  * lr, weight_decay finite and >= 0; 0 <= beta1, beta2 < 1; eps > 0 in fp32.
  * The moments, weights and gradients must not overlap one another. */
 FC_API fc_status fc_adamw_step(const void *const *grads, int32_t grad_type, int32_t L,
