@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(BLOCK)
 // Measured at 134M elements of bf16 (805 MB), 768 / 1024 / 2048 / 4096 columns:
 // 127 / 130 / 131 / 134 us, 0.9 of the copy rate; with the rows loaded one ahead
 // into registers 197 / 161 / 178 / 200 us.
-template <class T, int K, int TPR, int BLOCK, int D, bool ANY>
+template <class T, int K, int TPR, int BLOCK, int D, bool ANY, int CL>
 __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
     k_ln_bwd_ring(const LnBackward a, const bool pvec, const bool joins)
 {
@@ -206,17 +206,20 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
     constexpr int SLOTS = warp_slots<K, ANY>();  // of one row of one matrix
     constexpr int ROW = BLOCK / 32 * 2 * SLOTS;
     extern __shared__ __align__(16) uint4 ring[];  // [D][warps][2][SLOTS]
-    __shared__ float2 part[2][G][WARPS];
+    static_assert(CL == 1 || (G == 1 && CL * WARPS == 32), "a cluster's sums are one a lane");
+    __shared__ float2 part[2][CL == 1 ? G : CL][WARPS];
     wait_for_prior_grid();
     allow_dependent_launch();
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR, lane = threadIdx.x & 31;
     const int cols = (int)a.cols;
-    const int base = (t >> 5) * (64 * NP);  // the warp's first column
+    const uint32_t rank = CL == 1 ? 0 : cluster_rank();
+    const int first = (int)rank * (TPR * K * VEC);  // the CTA's first column
+    const int base = first + (t >> 5) * (64 * NP);  // the warp's
     const uint4 *const mine = ring + (threadIdx.x >> 5) * (2 * SLOTS);
     const uint32_t slot = (uint32_t)__cvta_generic_to_shared(mine + lane);
     const T *const x = static_cast<const T *>(a.x), *const dy = static_cast<const T *>(a.dy);
     T *const dx = static_cast<T *>(a.dx);
-    const int64_t stride = (int64_t)gridDim.x * G;
+    const int64_t stride = (int64_t)gridDim.x / CL * G;
 
     // first column of pair p: vectors are contiguous, words interleaved
     auto column = [&](int p) {
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
         cp_async_commit();
     };
 
-    int64_t row = (int64_t)blockIdx.x * G + g;
+    int64_t row = (int64_t)blockIdx.x / CL * G + g;
     if constexpr (ANY) {
         for (int i = threadIdx.x; i < D * ROW; i += BLOCK) ring[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
@@ -264,6 +267,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
         }
     }
     const float inv_n = 1.f / (float)cols;
+    if constexpr (CL > 1) cluster_sync();  // the other CTAs run before they are written to
     int buf = 0, d = 0;
     float nmean = 0.f, nrstd = 0.f;
     if (row < a.rows) {
@@ -306,7 +310,18 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
         const float2 u1 = un2(a1), u2 = un2(a2);
         float s1 = lanes_sum<32>(u1.x + u1.y);
         float s2 = lanes_sum<32>(u2.x + u2.y);
-        if constexpr (WARPS > 1) {
+        if constexpr (CL > 1) {
+            if (lane < CL) {
+                const float2 *const to = &part[buf][rank][t >> 5];
+                st_cluster_u32(&to->x, (uint32_t)lane, __float_as_uint(s1));
+                st_cluster_u32(&to->y, (uint32_t)lane, __float_as_uint(s2));
+            }
+            cluster_sync();
+            const float2 p = part[buf][lane / WARPS][lane % WARPS];
+            s1 = lanes_sum<32>(p.x);
+            s2 = lanes_sum<32>(p.y);
+            buf ^= 1;
+        } else if constexpr (WARPS > 1) {
             if (lane == 0) part[buf][g][t >> 5] = make_float2(s1, s2);
             group_sync<TPR, BLOCK>(g);
             const float2 p = part[buf][g][threadIdx.x & (WARPS - 1)];
@@ -344,40 +359,43 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
     // Every group leaves its sums in shared memory (no more than the ring
     // held), and the block adds them in the groups' order.
     const int padded = (int)ln_padded(cols);
-    float *const sums = reinterpret_cast<float *>(ring);  // [2][G][padded]
+    const int width = CL == 1 ? padded : min(padded - first, TPR * K * VEC);
+    float *const sums = reinterpret_cast<float *>(ring);  // [2][G][width]
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int c = column(p);
         if (c >= cols) continue;
-        float *const to = sums + g * padded + c;
+        float *const to = sums + g * width + (c - first);
         const float2 w = un2(dw[p]), b = un2(db[p]);
         if constexpr (SECOND == 1) {
             *reinterpret_cast<float2 *>(to) = w;
-            *reinterpret_cast<float2 *>(to + G * padded) = b;
+            *reinterpret_cast<float2 *>(to + G * width) = b;
         } else {
             to[0] = w.x;
-            to[G * padded] = b.x;
+            to[G * width] = b.x;
             if (c + SECOND < cols) {
                 to[SECOND] = w.y;
-                to[G * padded + SECOND] = b.y;
+                to[G * width + SECOND] = b.y;
             }
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * (padded / 4); i += BLOCK) {
-        const int which = i >= padded / 4, q = which ? i - padded / 4 : i;
-        const float4 *from = reinterpret_cast<const float4 *>(sums + which * G * padded) + q;
+    for (int i = threadIdx.x; i < 2 * (width / 4); i += BLOCK) {
+        const int which = i >= width / 4, q = which ? i - width / 4 : i;
+        const float4 *from = reinterpret_cast<const float4 *>(sums + which * G * width) + q;
         float4 v = from[0];
 #pragma unroll
         for (int r = 1; r < G; ++r) {
-            const float4 u = from[r * (padded / 4)];
+            const float4 u = from[r * (width / 4)];
             v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
         }
-        reinterpret_cast<float4 *>(a.partials)[(which * (int64_t)gridDim.x + blockIdx.x) *
-                                                   (padded / 4) + q] = v;
+        const int64_t set = which * (int64_t)gridDim.x / CL + blockIdx.x / CL;
+        reinterpret_cast<float4 *>(a.partials + set * padded + first)[q] = v;
     }
-    if (joins) join_in_cluster<BLOCK>(a);
+    if constexpr (CL == 1) {
+        if (joins) join_in_cluster<BLOCK>(a);
+    }
 }
 
 // Rows wider than the registers hold: one block a row, two passes over it.
@@ -462,10 +480,10 @@ inline int joining_ctas(const LnBackward &a, int group)
     return ctas;
 }
 
-// A launch of `grid` blocks as one cluster.
+// A launch in clusters of `cluster` blocks.
 template <class... KArgs, class... Args>
-static cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, unsigned block, size_t smem,
-                                  cudaStream_t s, Args... args)
+static cudaError_t launch_clusters(void (*kernel)(KArgs...), int grid, int cluster, unsigned block,
+                                   size_t smem, cudaStream_t s, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -476,7 +494,7 @@ static cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, unsigned b
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)grid;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -488,7 +506,8 @@ template <class T, int VEC, int K, int TPR, int BLOCK>
 static cudaError_t go(const LnBackward &a, bool pvec, cudaStream_t s)
 {
     if (const int ctas = joining_ctas(a, BLOCK / TPR))
-        return launch_cluster(k_ln_bwd<T, VEC, K, TPR, BLOCK>, ctas, BLOCK, 0, s, a, pvec, true);
+        return launch_clusters(k_ln_bwd<T, VEC, K, TPR, BLOCK>, ctas, ctas, BLOCK, 0, s, a, pvec,
+                               true);
     const auto kernel = k_ln_bwd<T, VEC, K, TPR, BLOCK>;
     const int64_t ctas = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
     int grid = grid_for((const void *)kernel, BLOCK, 0, ctas);
@@ -498,18 +517,20 @@ static cudaError_t go(const LnBackward &a, bool pvec, cudaStream_t s)
     return e != cudaSuccess ? e : ln_join(a, grid, s);
 }
 
-template <class T, int K, int TPR, int BLOCK, bool ANY>
+template <class T, int K, int TPR, int BLOCK, bool ANY, int CL = 1>
 struct RingLaunch {
-    static constexpr int D = K == 4 ? 2 : 3, G = BLOCK / TPR;
+    static constexpr int D = CL == 1 && K == 4 ? 2 : 3, G = BLOCK / TPR;
+    static constexpr auto kernel = k_ln_bwd_ring<T, K, TPR, BLOCK, D, ANY, CL>;
     size_t smem;
     int64_t ctas;
     int resident;
 
     cudaError_t prepare(const LnBackward &a)
     {
-        const void *k = (const void *)k_ln_bwd_ring<T, K, TPR, BLOCK, D, ANY>;
+        const void *k = (const void *)kernel;
         smem = std::max<size_t>((size_t)D * (BLOCK / 32) * 2 * warp_slots<K, ANY>() * 16,
-                                2 * sizeof(float) * (size_t)G * ln_padded(a.cols));
+                                2 * sizeof(float) * (size_t)G *
+                                    (CL == 1 ? ln_padded(a.cols) : TPR * K * (16 / sizeof(T))));
         ctas = (a.rows + G - 1) / G;
         cudaError_t e =
             cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -517,18 +538,21 @@ struct RingLaunch {
             resident = grid_for(k, BLOCK, smem, INT64_MAX, cudaSharedmemCarveoutMaxShared);
         return e;
     }
+    // in groups of CL blocks, each of which leaves one set of sums
     cudaError_t run(const LnBackward &a, bool pvec, cudaStream_t s) const
     {
-        const int64_t most = std::min<int64_t>(resident, ln_max_parts(a.rows, a.cols));
+        const int64_t most = std::min<int64_t>(resident / CL, ln_max_parts(a.rows, a.cols));
         const int grid = (int)std::min(ctas, most);
-        cudaError_t e = launch_after_prior(k_ln_bwd_ring<T, K, TPR, BLOCK, D, ANY>, (unsigned)grid,
-                                           BLOCK, smem, s, a, pvec, false);
+        cudaError_t e;
+        if constexpr (CL == 1)
+            e = launch_after_prior(kernel, (unsigned)grid, BLOCK, smem, s, a, pvec, false);
+        else
+            e = launch_clusters(kernel, grid * CL, CL, BLOCK, smem, s, a, pvec, false);
         return e != cudaSuccess ? e : ln_join(a, grid, s);
     }
     cudaError_t run_cluster(const LnBackward &a, bool pvec, int n, cudaStream_t s) const
     {
-        return launch_cluster(k_ln_bwd_ring<T, K, TPR, BLOCK, D, ANY>, n, BLOCK, smem, s, a, pvec,
-                              true);
+        return launch_clusters(kernel, n, n, BLOCK, smem, s, a, pvec, true);
     }
 };
 
@@ -558,6 +582,19 @@ static cudaError_t go_ring(const LnBackward &a, bool pvec, cudaStream_t s)
     return e != cudaSuccess ? e : large.run(a, pvec, s);
 }
 
+// Rows wider than one CTA's registers hold with their sums: half a row in each
+// of two CTAs, which exchange the sums of their warps.  Measured at 805 MB: 16384
+// bf16 columns 209 us (one CTA of four vectors a thread, which spills: 234), 12288
+// and 16384 fp32 columns 171 and 152 us (two passes over the row: 360 and 387).  A
+// quarter of a row in each of four CTAs, two to an SM: 311, 241 and 211 us.
+template <class T, int K, bool ANY>
+static cudaError_t go_halves(const LnBackward &a, bool pvec, cudaStream_t s)
+{
+    RingLaunch<T, K, 512, 512, ANY, 2> halves;
+    const cudaError_t e = halves.prepare(a);
+    return e != cudaSuccess ? e : halves.run(a, pvec, s);
+}
+
 // The smallest TPR * K that holds a row of n vectors.
 template <class T, bool ANY>
 static cudaError_t ring(const LnBackward &a, int64_t n, bool pvec, cudaStream_t s)
@@ -575,7 +612,14 @@ static cudaError_t ring(const LnBackward &a, int64_t n, bool pvec, cudaStream_t 
     if (n <= 256) return go_ring<T, 2, 128, ANY>(a, pvec, s);
     if (n <= 512) return go_ring<T, 2, 256, ANY>(a, pvec, s);
     if (n <= 1024) return go_ring<T, 2, 512, ANY>(a, pvec, s);
-    return go_ring<T, 4, 512, ANY>(a, pvec, s);
+    if constexpr (sizeof(T) == 4) {
+        if (n <= 2048) return go_ring<T, 4, 512, ANY>(a, pvec, s);
+        if constexpr (!ANY)
+            if (n <= 3072) return go_halves<T, 3, ANY>(a, pvec, s);
+        return go_halves<T, 4, ANY>(a, pvec, s);
+    } else {
+        return go_halves<T, 2, ANY>(a, pvec, s);
+    }
 }
 
 template <class T>
@@ -611,7 +655,7 @@ cudaError_t ln_backward(const LnBackward &a, cudaStream_t s)
     if (vectors && n <= 16) return go<T, V, 1, 16, 128>(a, pvec, s);
     if (!vectors && c <= 32) return go<T, 1, 1, 32, 128>(a, pvec, s);
     if (!vectors && c <= 128) return go<T, 1, 4, 32, 128>(a, pvec, s);
-    if (n > 2048) return wide_rows<T>(a, s);
+    if (n > (sizeof(T) == 4 ? 4096 : 2048)) return wide_rows<T>(a, s);
     return vectors ? ring<T, false>(a, n, pvec, s) : ring<T, true>(a, n, pvec, s);
 }
 

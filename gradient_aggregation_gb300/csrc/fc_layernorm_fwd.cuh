@@ -482,7 +482,7 @@ template <class T, int K, int TPR, int RW>
 static cudaError_t go_rows(const LnForward &a, cudaStream_t s)
 {
     // one block an SM where the parameters of a row take much of its memory
-    constexpr int BLOCK = TPR == 256 ? 512 : 256;
+    constexpr int BLOCK = TPR >= 256 ? 512 : 256;
     const auto kernel = k_ln_fwd_rows<T, K, TPR, RW, BLOCK>;
     const size_t smem = 2 * sizeof(float) * (size_t)a.cols;
     if (smem > 40 * 1024) {
@@ -529,6 +529,10 @@ static cudaError_t many_rows(const LnForward &a, int64_t n, cudaStream_t s)
     if (n <= 768) return go_rows<T, 6, 128, 1>(a, s);
     if (n <= 1024) return go_rows<T, 8, 128, 1>(a, s);
     if (n <= 1536) return go_rows<T, 6, 256, 1>(a, s);
+    if constexpr (sizeof(T) == 4) {
+        if (n > 3072) return go_rows<T, 8, 512, 1>(a, s);
+        if (n > 2048) return go_rows<T, 6, 512, 1>(a, s);
+    }
     return go_rows<T, 8, 256, 1>(a, s);
 }
 
@@ -573,7 +577,7 @@ cudaError_t ln_forward(const LnForward &a, cudaStream_t s)
     const int64_t c = a.cols, n = (c + V - 1) / V;
     const bool vectors = c % V == 0 && on16(a.x, a.ldx) && on16(a.y, a.ldy);
     const bool few = few_rows<T>(a.rows, n, vectors);
-    if (n > 2048) {
+    if (n > (vectors && sizeof(T) == 4 ? 4096 : 2048)) {
         const auto wide = k_ln_fwd_wide<T>;
         const int grid = grid_for((const void *)wide, FC_LN_WIDE_BLOCK, 0, a.rows);
         return launch_after_prior(wide, (unsigned)grid, FC_LN_WIDE_BLOCK, 0, s, a);

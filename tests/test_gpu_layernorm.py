@@ -140,6 +140,27 @@ def test_shifted_rows_read_nothing_outside_the_matrix():
                 assert bool(t.isfinite().all())
 
 
+# the backward pass's rows in halves: fewer rows than pairs of blocks, and several rounds
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,cols,pad", [(1, 12296, 0), (2, 16384, 0), (75, 12304, 0),
+                                           (77, 16376, 8), (301, 12290, 0), (301, 16384, 0),
+                                           (160, 8196, 0), (3, 12289, 0), (161, 16383, 1)])
+def test_rows_in_halves(rows, cols, pad, dtype):
+    x, w, b, y, mu, rs, dy, dx, dw, db, ws = check(rows, cols, dtype, pad)
+    dx2, dw2, db2 = torch.empty_like(dx), torch.empty_like(dw), torch.empty_like(db)
+    fc.fc_layernorm_backward(dy, x, w, mu, rs, dx2, dw2, db2, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2) and torch.equal(db, db2)
+
+
+# few narrow rows, whose sums are joined in the same launch, up to where that ends
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows", [1, 2, 3, 7, 9, 33, 64, 127, 128, 129])
+@pytest.mark.parametrize("cols", [5, 40, 64, 100, 128, 130, 200, 256, 512])
+def test_few_rows(rows, cols, dtype):
+    check(rows, cols, dtype, gtype=dtype)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 3, 5, 17, 255, 1000, 5003])
 @pytest.mark.parametrize("cols", [64, 257, 1024])
 def test_row_counts(rows, cols):
