@@ -152,22 +152,39 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_ln_fwd_rows(const LnForw
     const int first = (t >> 5) * (32 * K) + lane;  // this lane's first vector
     int buf = 0;
     const int64_t stride = (int64_t)gridDim.x * G * RW;
-    for (int64_t row0 = ((int64_t)blockIdx.x * G + g) * RW; row0 < a.rows; row0 += stride) {
-        uint32_t v[RW][4 * K];
+    int64_t row0 = ((int64_t)blockIdx.x * G + g) * RW;
+    auto load = [&](int64_t r0, uint32_t (&v)[RW][4 * K]) {
 #pragma unroll
         for (int r = 0; r < RW; ++r)
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int j = first + 32 * k;
                 const uint4 q =
-                    j < nvec && row0 + r < a.rows
-                        ? __ldcs(reinterpret_cast<const uint4 *>(x + (row0 + r) * a.ldx) + j)
+                    j < nvec && r0 + r < a.rows
+                        ? __ldcs(reinterpret_cast<const uint4 *>(x + (r0 + r) * a.ldx) + j)
                         : make_uint4(0, 0, 0, 0);
                 v[r][4 * k] = q.x;
                 v[r][4 * k + 1] = q.y;
                 v[r][4 * k + 2] = q.z;
                 v[r][4 * k + 3] = q.w;
             }
+    };
+    // a block that works on one row alone loads the next meanwhile (16384 fp32
+    // columns 121 us without, 95 with; where other blocks share the SM it gains
+    // nothing: 4096 bf16 columns 87 and 98)
+    constexpr bool AHEAD = TPR == 512;
+    uint32_t v[RW][4 * K], next[AHEAD ? RW : 1][4 * K];
+    if constexpr (AHEAD) load(row0, next);
+    for (; row0 < a.rows; row0 += stride) {
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int r = 0; r < RW; ++r)
+#pragma unroll
+                for (int i = 0; i < 4 * K; ++i) v[r][i] = next[r][i];
+            load(row0 + stride, next);
+        } else {
+            load(row0, v);
+        }
         auto get = [&](int r, int p) { return pair_of<T>(v[r], p); };
         auto inside = [&](int k) { return first + 32 * k < nvec ? 1 : 0; };
         float mean[RW], rstd[RW];
@@ -202,8 +219,12 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_ln_fwd_rows(const LnForw
     }
 }
 
+// Blocks of 256 on an SM: three where a lane holds two vectors (67M elements of
+// bf16 in rows of 333: 87 us, with two 98), else two (rows of 129: 135 us with two,
+// three or four; rows of 1001 and four vectors a lane: 59 us, with three 61).
 template <class T, int K, int TPR, int BLOCK, int D>
-__global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_ln_fwd_any(const LnForward a)
+__global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 2 ? 3 : 2)
+    k_ln_fwd_any(const LnForward a)
 {
     constexpr int VEC = 16 / (int)sizeof(T), NP = K * VEC / 2;
     constexpr int G = BLOCK / TPR, WARPS = TPR / 32, STEP = pair_step<T>();
