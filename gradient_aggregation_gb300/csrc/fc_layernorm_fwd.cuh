@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 2 ? 3 : 2)
     wait_for_prior_grid();
     allow_dependent_launch();
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR, lane = threadIdx.x & 31;
-    constexpr int B = NP < 4 ? NP : 4;  // pairs a block
+    constexpr int B = NP % 4 ? 2 : 4;  // pairs a block
     const int cols = (int)a.cols, room = (cols + 64 * B - 1) / (64 * B) * (64 * B);
     const int base = (t >> 5) * (64 * NP);
     const uint4 *const mine = ring + (threadIdx.x >> 5) * SLOTS;
@@ -557,15 +557,23 @@ static cudaError_t many_rows(const LnForward &a, int64_t n, cudaStream_t s)
     return go_rows<T, 8, 256, 1>(a, s);
 }
 
+// Classes half as wide again as the last (K = 3) and twice as wide: 67M elements
+// of bf16 in rows of 517 / 1101 / 2051 / 4101 columns took 96 / 99 / 108 / 104 us
+// in classes of twice the width alone, 82 / 86 / 93 / 94 with both.
 template <class T>
 static cudaError_t many_rows_any(const LnForward &a, int64_t n, cudaStream_t s)
 {
     if (n <= 32) return go_any<T, 1, 32>(a, s);
     if (n <= 64) return go_any<T, 2, 32>(a, s);
+    if (n <= 96) return go_any<T, 3, 32>(a, s);
     if (n <= 128) return go_any<T, 4, 32>(a, s);
+    if (n <= 192) return go_any<T, 3, 64>(a, s);
     if (n <= 256) return go_any<T, 4, 64>(a, s);
+    if (n <= 384) return go_any<T, 3, 128>(a, s);
     if (n <= 512) return go_any<T, 4, 128>(a, s);
+    if (n <= 768) return go_any<T, 3, 256>(a, s);
     if (n <= 1024) return go_any<T, 4, 256>(a, s);
+    if (n <= 1536) return go_any<T, 3, 512>(a, s);
     return go_any<T, 4, 512>(a, s);
 }
 
