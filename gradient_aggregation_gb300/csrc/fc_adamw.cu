@@ -32,6 +32,7 @@
 
 #include "fc_bulk.cuh"
 #include "fc_opt.h"
+#include "fc_pairs.cuh"
 
 namespace fc {
 
@@ -41,8 +42,8 @@ namespace fc {
 // of 20 units is copied in pieces of 20 KB; with 8 KB pieces the 62M-element
 // step with fp32 moments took 320 us, with 16 KB 286, with 20 KB 279.  With
 // 8-bit moments the update itself needs the warps: 24 of them took 159 us, 23
-// 163, 20 189, 27 161.  Where gradients are shifted, 24 warps with 72 registers
-// are worse than 23 with 80: 27.8 and 26.3 us for 7M elements.
+// 161, 20 163, 27 161.  Where gradients are shifted, 24 warps with 72 registers
+// are worse than 23 with 80: 26.8 and 25.2 us for 7M elements.
 #define FC_ADAM_CW32 20
 #define FC_ADAM_S32 3
 #define FC_ADAM_CW8 24
@@ -342,12 +343,15 @@ __device__ __forceinline__ float fast_rcp_ftz(float x)
 // sqrt(x) for x = 0 or in [2^-126, 2^127]: the approximate reciprocal root, and
 // one Newton step on the root's remainder, after which all but about one root
 // in a million is the nearest fp32 number.
-__device__ __forceinline__ float newton_sqrt(float x)
+__device__ __forceinline__ F2 newton_sqrt2(F2 x)
 {
-    float y;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 0x1p-126f)));
-    const float s = x * y;
-    return fmaf(fmaf(-s, s, x), 0.5f * y, s);
+    const float2 u = un2(x);
+    float2 y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(u.x, 0x1p-126f)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(u.y, 0x1p-126f)));
+    const F2 y2 = f2(y.x, y.y), s = mul2(x, y2), half = mul2(f2(-0.5f, -0.5f), y2);
+    // s - (s^2 - x) y / 2
+    return fma2(fma2(s, s, f2(-u.x, -u.y)), half, s);
 }
 
 // One element with fp32 moments.  The quotient is the fast division (2 units
@@ -360,6 +364,14 @@ __device__ __forceinline__ void adam1(float graw, float decay, const AdamHyper &
     v = fmaf(h.b2, v, h.omb2 * g * g);
     const float step = __fdividef(sc.lrc * m, fmaf(fast_sqrt(v), sc.rc2, h.eps));
     w = fmaf(-h.lrwd * decay, w, w) - step;
+}
+
+// a + b, one by one: the compiler joins a packed sum (one rounding) with a packed
+// product before it.
+__device__ __forceinline__ F2 add_once(F2 a, F2 b)
+{
+    const float2 x = un2(a), y = un2(b);
+    return f2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
 }
 
 __device__ __forceinline__ float max3_nan(float a, float b, float c)
@@ -379,6 +391,10 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c)
 // would turn some code in a million into its neighbour, 6 % away, and the
 // next step's block maximum with it.  The weights take the fast quotient.
 //
+// The unit is bound by the issue of its instructions where it is not by HBM, so
+// two elements share one wherever they can (7M elements in odd layers 25.2 us,
+// one by one 26.2).
+//
 // Rounding r by chance: y = r * 448 / top lies in [0, 448].  Scaled by 2^-120
 // an e4m3 number is the top of an fp32 number's bits: e4m3's smallest normal
 // 2^-6 falls on fp32's 2^-126, so that below it both formats are linear, and
@@ -390,8 +406,12 @@ __device__ __forceinline__ void adam8_unit(const float *graw, const float *d, co
                                            const StepScalars &sc, int64_t i0, float *w,
                                            uint32_t *mq, uint32_t *rq, float &ms, float &rs)
 {
-    float m[8], r[8];
+    F2 m[4], r[4];
     const float ma = ms * FC_ADAM8_UNIT, ra = rs * FC_ADAM8_UNIT;
+    const F2 ma2 = f2(ma, ma), ra2 = f2(ra, ra), s2 = f2(sc.s, sc.s);
+    const F2 b12 = f2(h.b1, h.b1), b22 = f2(h.b2, h.b2);
+    const F2 omb12 = f2(h.omb1, h.omb1), omb22 = f2(h.omb2, h.omb2);
+    const F2 rc22 = f2(sc.rc2, sc.rc2), eps2 = f2(h.eps, h.eps), lrc2 = f2(-sc.lrc, -sc.lrc);
     const float wd0 = -h.lrwd * d[0];
     float mtop = 0.f, rtop = 0.f;
 #pragma unroll
@@ -400,22 +420,21 @@ __device__ __forceinline__ void adam8_unit(const float *graw, const float *d, co
             (__nv_fp8x2_storage_t)(mq[p >> 1] >> (16 * (p & 1))), __NV_E4M3)));
         const float2 cr = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
             (__nv_fp8x2_storage_t)(rq[p >> 1] >> (16 * (p & 1))), __NV_E4M3)));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int j = 2 * p + e;
-            const float g = __fmul_rn(graw[j], sc.s);
-            const float r0 = __fmul_rn(e ? cr.y : cr.x, ra);
-            m[j] = __fadd_rn(__fmul_rn(__fmul_rn(e ? cm.y : cm.x, ma), h.b1),
-                             __fmul_rn(g, h.omb1));
-            const float v = __fadd_rn(__fmul_rn(__fmul_rn(r0, r0), h.b2),
-                                      __fmul_rn(__fmul_rn(g, g), h.omb2));
-            r[j] = newton_sqrt(v);
-            const float rden = fast_rcp_ftz(fmaf(r[j], sc.rc2, h.eps));
-            const float kept = fmaf(UNIFORM ? wd0 : -h.lrwd * d[j], w[j], w[j]);
-            w[j] = fmaf(-sc.lrc * m[j], rden, kept);
-        }
-        mtop = max3_nan(mtop, fabsf(m[2 * p]), fabsf(m[2 * p + 1]));
-        rtop = max3_nan(rtop, r[2 * p], r[2 * p + 1]);
+        const F2 g = mul2(f2(graw[2 * p], graw[2 * p + 1]), s2);
+        const F2 r0 = mul2(f2(cr.x, cr.y), ra2);
+        m[p] = add_once(mul2(mul2(f2(cm.x, cm.y), ma2), b12), mul2(g, omb12));
+        const F2 v = add_once(mul2(mul2(r0, r0), b22), mul2(mul2(g, g), omb22));
+        r[p] = newton_sqrt2(v);
+        const float2 den = un2(fma2(r[p], rc22, eps2));
+        const F2 rden = f2(fast_rcp_ftz(den.x), fast_rcp_ftz(den.y));
+        const F2 w2 = f2(w[2 * p], w[2 * p + 1]);
+        const F2 wd = UNIFORM ? f2(wd0, wd0) : f2(-h.lrwd * d[2 * p], -h.lrwd * d[2 * p + 1]);
+        const float2 wn = un2(fma2(mul2(lrc2, m[p]), rden, fma2(wd, w2, w2)));
+        w[2 * p] = wn.x;
+        w[2 * p + 1] = wn.y;
+        const float2 mu = un2(m[p]), ru = un2(r[p]);
+        mtop = max3_nan(mtop, fabsf(mu.x), fabsf(mu.y));
+        rtop = max3_nan(rtop, ru.x, ru.y);
     }
     // magnitudes compare as their bits; a NaN is above all numbers
     mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
@@ -429,16 +448,16 @@ __device__ __forceinline__ void adam8_unit(const float *graw, const float *d, co
     const float q448 = 448.f * __frcp_rn((threadIdx.x & 1) ? rtop : mtop);
     const float mto = mdead ? 0.f : __shfl_sync(0xffffffffu, q448, 0);
     const float rto = rdead ? 0.f : __shfl_sync(0xffffffffu, q448, 1);
+    const F2 mto2 = f2(mto, mto), rto2 = f2(rto, rto);
     const float least = rdead ? 0.f : 0x1p-129f;  // e4m3's 2^-9
     const uint64_t pair = (uint64_t)i0 >> 1;
     const uint32_t x = (uint32_t)pair + sc.key + (uint32_t)(pair >> 32) * 0x9E3779B9u;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const float *mm = m + 4 * q;
-        mq[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(mm[0] * mto, mm[1] * mto),
-                                                   __NV_SATFINITE, __NV_E4M3) |
-                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(mm[2] * mto, mm[3] * mto),
-                                                   __NV_SATFINITE, __NV_E4M3)
+        mq[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(un2(mul2(m[2 * q], mto2)), __NV_SATFINITE,
+                                                   __NV_E4M3) |
+                (uint32_t)__nv_cvt_float2_to_fp8x2(un2(mul2(m[2 * q + 1], mto2)), __NV_SATFINITE,
+                                                   __NV_E4M3)
                     << 16;
         uint32_t u[4];
 #pragma unroll
@@ -447,10 +466,11 @@ __device__ __forceinline__ void adam8_unit(const float *graw, const float *d, co
             // 24 bits: the 16 drawn, then 0x80
             const uint32_t lo = __byte_perm(bits, 0x80u, 0x5104);
             const uint32_t hi = __byte_perm(bits, 0x80u, 0x5324);
-            const float ra0 = r[4 * q + 2 * e], ra1 = r[4 * q + 2 * e + 1];
+            const float2 ru = un2(r[2 * q + e]);
+            const float2 y = un2(mul2(mul2(r[2 * q + e], rto2), f2(0x1p-120f, 0x1p-120f)));
             // r > 0 is at least 2^-63 here
-            const float y0 = fmaxf(ra0 * rto * 0x1p-120f, fminf(ra0, least));
-            const float y1 = fmaxf(ra1 * rto * 0x1p-120f, fminf(ra1, least));
+            const float y0 = fmaxf(y.x, fminf(ru.x, least));
+            const float y1 = fmaxf(y.y, fminf(ru.y, least));
             u[2 * e] = (__float_as_uint(y0) << 4) + lo;
             u[2 * e + 1] = (__float_as_uint(y1) << 4) + hi;
         }
@@ -927,9 +947,8 @@ static cudaError_t launch_typed(const Tab &tab, const AdamState &st, cudaStream_
     const void *direct = (const void *)k_adamw_direct<GT, BITS, Tab>;
     const int resident = grid_for(direct, FC_ADAM_BLOCK, 0, INT64_MAX);
     // The direct kernel serves what its resident CTAs take in one round (0.93M
-    // elements with fp32 moments, 1.2M with 8-bit ones).  Measured, direct
-    // against ring: 4.8 and 6.0 us at 0.8M elements, 7.7 and 6.4 us at 1.1M
-    // (fp32); 5.4 and 6.2 us at 1.1M, 9.3 and 6.4 us at 1.6M (8-bit).
+    // elements).  Measured, direct against ring: fp32 4.8 and 6.0 us at 0.8M
+    // elements, 7.9 and 6.3 us at 1.1M; 8-bit 4.3 and 5.4 us, 7.0 and 6.5 us.
     if (ctas <= resident)
         return launch_table(direct, (unsigned)ctas, FC_ADAM_BLOCK, 0, s, tab, st);
     if (any_shifted<GT>(tab)) return launch_ring<GT, BITS, true>(tab, st, s);
