@@ -586,11 +586,14 @@ static cudaError_t many_rows_any(const LnForward &a, int64_t n, cudaStream_t s)
 // (bf16); of 2048 columns 2 MB 2.49 and 2.89 and 4 MB 3.75 and 2.99 (fp32), 4
 // MB 4.29 and 4.40 (bf16).  Rows word by word, 523 of 1001 columns 3.91 and 3.78
 // (bf16), 3.48 and 3.35 (fp32); 1047 rows 4.93 and 3.84, 4.45 and 4.01; 524 of
-// 2001 columns 4.79 and 4.91, 4.37 and 4.80.
+// 2001 columns 4.79 and 4.91, 4.37 and 4.80; bf16, 512 of 8001 columns 8.1 and
+// 9.9, but of 12001 columns, whose rows take an SM each, 20.3 and 15.3 (128 rows:
+// 6.7 and 9.1).  fp32 rows of 8193 to 16384 columns have only the three passes
+// beside it: 512 of 12001 columns 22 and 29.
 template <class T>
 static bool few_rows(int64_t rows, int64_t n, bool vectors)
 {
-    if (!vectors) return rows <= 512;
+    if (!vectors) return rows <= (sizeof(T) == 2 && n > 1024 ? 152 : 512);
     const int shift = sizeof(T) == 2 ? (n > 64 ? 18 : 16) : (n > 256 ? 17 : 16);
     return rows * n <= (int64_t)1 << shift;
 }
@@ -606,7 +609,9 @@ cudaError_t ln_forward(const LnForward &a, cudaStream_t s)
     const int64_t c = a.cols, n = (c + V - 1) / V;
     const bool vectors = c % V == 0 && on16(a.x, a.ldx) && on16(a.y, a.ldy);
     const bool few = few_rows<T>(a.rows, n, vectors);
-    if (n > (vectors && sizeof(T) == 4 ? 4096 : 2048)) {
+    const bool one_pass = vectors ? n <= (sizeof(T) == 4 ? 4096 : 2048)
+                                  : n <= 2048 || (few && c <= 16384);
+    if (!one_pass) {
         const auto wide = k_ln_fwd_wide<T>;
         const int grid = grid_for((const void *)wide, FC_LN_WIDE_BLOCK, 0, a.rows);
         return launch_after_prior(wide, (unsigned)grid, FC_LN_WIDE_BLOCK, 0, s, a);
@@ -620,6 +625,7 @@ cudaError_t ln_forward(const LnForward &a, cudaStream_t s)
         if (n <= 256) return go<T, V, 1, 256, 256>(a, pvec, s);
         if (n <= 512) return go<T, V, 1, 512, 512>(a, pvec, s);
         if (n <= 1024) return go<T, V, 1, 1024, 1024>(a, pvec, s);
+        if (n <= 2048) return go<T, V, 2, 1024, 1024>(a, pvec, s);
         return many_rows<T>(a, n, s);
     }
     if (c <= 32) return go<T, 1, 1, 32, 128>(a, pvec, s);
@@ -629,7 +635,8 @@ cudaError_t ln_forward(const LnForward &a, cudaStream_t s)
     if (c <= 1024) return go<T, 1, 4, 256, 256>(a, pvec, s);
     if (c <= 2048) return go<T, 1, 4, 512, 512>(a, pvec, s);
     if (c <= 4096) return go<T, 1, 4, 1024, 1024>(a, pvec, s);
-    return many_rows_any<T>(a, n, s);
+    if (c <= 8192) return go<T, 1, 8, 1024, 1024>(a, pvec, s);
+    return go<T, 1, 16, 1024, 1024>(a, pvec, s);
 }
 
 }  // namespace fc

@@ -153,6 +153,16 @@ def test_rows_in_halves(rows, cols, pad, dtype):
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2) and torch.equal(db, db2)
 
 
+# few wide rows, and the last number of rows that counts as few
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,cols,pad", [(1, 16384, 0), (3, 12296, 0), (64, 16376, 0),
+                                           (1, 5001, 0), (2, 8191, 0), (1, 16383, 0),
+                                           (152, 9001, 0), (153, 9001, 0), (152, 12287, 2),
+                                           (5, 16384, 3)])
+def test_few_wide_rows(rows, cols, pad, dtype):
+    check(rows, cols, dtype, pad, ptype=dtype)
+
+
 # few narrow rows, whose sums are joined in the same launch, up to where that ends
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("rows", [1, 2, 3, 7, 9, 33, 64, 127, 128, 129])
