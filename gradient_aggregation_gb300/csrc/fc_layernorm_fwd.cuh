@@ -11,7 +11,7 @@
 //   M2 = sum_w [ M2_w + n_w (mean_w - mean)^2 ]
 // which needs one exchange through shared memory and one barrier a row.
 //
-// Two kernels: k_ln_fwd_rows for matrices of many rows, and k_ln_fwd, which
+// Kernels: k_ln_fwd_rows and k_ln_fwd_any for many rows, and k_ln_fwd, which
 // spreads each row over as many threads as it has vectors, for few rows and
 // for narrow ones.
 #pragma once
@@ -578,8 +578,9 @@ static cudaError_t many_rows_any(const LnForward &a, int64_t n, cudaStream_t s)
 }
 
 // Few rows: what counts is the latency of a row, so a row is spread over as many
-// threads as it has vectors (or four elements a thread), and no ring and no
-// copy of the parameters is set up first.  Where that ends is measured, few
+// threads as it has vectors, to 1024 (or four elements a thread, more above 4096
+// columns), and no ring and no copy of the parameters is set up first.  Where that
+// ends is measured, few
 // against many in us: rows of vectors, 1 MB of 256 columns 1.85 and 2.44
 // (bf16), 2.50 and 2.47 (fp32), and 2 MB 3.02 and 2.49, 3.12 and 2.48; of 1024
 // columns 2 MB 2.93 and 3.49 (bf16), 3.04 and 2.51 (fp32), 4 MB 3.65 and 3.58
