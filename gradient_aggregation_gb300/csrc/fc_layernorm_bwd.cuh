@@ -191,8 +191,11 @@ __global__ void __launch_bounds__(BLOCK)
 // width; a warp copies the 32 K + 1 aligned granules around its columns and
 // reads its pairs out of them word by word (see fc_pairs.cuh).
 //
-// dx is formed as rstd q - (rstd^2 s2) x - rstd (s1 - mean rstd s2), with s1 and
-// s2 the means of q and q h: one multiplication and two multiply-adds, no h.
+// h is (x - mean) * rstd, the difference first: a row far from zero has its mean's
+// digits cancelled exactly there (as x * rstd - mean * rstd the rounding of the
+// product, |mean| rstd 2^-24, is an error that the whole row's h has in common).
+// dx is rstd ((q - s1) - (rstd s2) (x - mean)), with s1 and s2 the means of q and
+// q h: no h, and rstd is never squared (it may be 1e19 where eps is 0).
 //
 // Measured at 134M elements of bf16 (805 MB), 768 / 1024 / 2048 / 4096 columns:
 // 127 / 130 / 131 / 134 us, 0.9 of the copy rate; with the rows loaded one ahead
@@ -205,6 +208,11 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
     constexpr int G = BLOCK / TPR, WARPS = TPR / 32, STEP = pair_step<T>();
     constexpr int SLOTS = warp_slots<K, ANY>();  // of one row of one matrix
     constexpr int ROW = BLOCK / 32 * 2 * SLOTS;
+    // three vectors of a 16-bit type do not fit beside their sums: the row is read
+    // from its slots again for dx (67M bf16 elements in rows of 1536 / 3000 / 6144 /
+    // 12288 columns: 66 / 69 / 70 / 80 us; held in registers and spilled in part 83 /
+    // 94 / 71 / 96)
+    constexpr bool AGAIN = !ANY && K == 3 && sizeof(T) == 2;
     extern __shared__ __align__(16) uint4 ring[];  // [D][warps][2][SLOTS]
     static_assert(CL == 1 || (G == 1 && CL * WARPS == 32), "a cluster's sums are one a lane");
     __shared__ float2 part[2][CL == 1 ? G : CL][WARPS];
@@ -284,12 +292,15 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
         cp_async_wait<D - 1>();
         if constexpr (ANY) __syncwarp();
         uint32_t vx[4 * K], vy[4 * K];
-        take_row<T, K, ANY>(mine + d * ROW, ANY ? past16(x + row * a.ldx) : 0, cols, base, vx);
-        take_row<T, K, ANY>(mine + d * ROW + SLOTS, ANY ? past16(dy + row * a.lddy) : 0, cols,
-                            base, vy);
+        const uint4 *const held = mine + d * ROW;
+        auto take = [&]() {
+            take_row<T, K, ANY>(held, ANY ? past16(x + row * a.ldx) : 0, cols, base, vx);
+            take_row<T, K, ANY>(held + SLOTS, ANY ? past16(dy + row * a.lddy) : 0, cols, base, vy);
+        };
+        take();
         if (++d == D) d = 0;
-        const float nm = -mean * rstd;
-        const F2 rr = f2(rstd, rstd), nn = f2(nm, nm);
+        const F2 rr = f2(rstd, rstd), mm = f2(-mean, -mean);
+        auto centred = [&](int p) { return add2(pair_of<T>(vx, p), mm); };
         F2 a1 = f2(0.f, 0.f), a2 = f2(0.f, 0.f);
         // in blocks of a vector's pairs, each behind a branch of its own: without
         // it the compiler works on all of them at once and runs out of registers
@@ -299,7 +310,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
 #pragma unroll
             for (int p = k * (VEC / 2); p < (k + 1) * (VEC / 2); ++p) {
                 const F2 fy = pair_of<T>(vy, p);
-                const F2 h = fma2(pair_of<T>(vx, p), rr, nn);
+                const F2 h = mul2(centred(p), rr);
                 const F2 q = mul2(fy, pw[p]);
                 a1 = add2(a1, q);
                 a2 = fma2(q, h, a2);
@@ -329,13 +340,17 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
             s2 = lanes_sum<WARPS>(p.y);
             buf ^= 1;
         }
+        if constexpr (AGAIN) {
+            asm volatile("" ::: "memory");
+            take();
+        }
         s1 *= inv_n;
         s2 *= inv_n;
-        const float cx = -rstd * rstd * s2, c0 = -rstd * fmaf(nm, s2, s1);
-        const F2 cx2 = f2(cx, cx), c02 = f2(c0, c0);
+        const float c = -rstd * s2;
+        const F2 c2 = f2(c, c), c1 = f2(-s1, -s1);
         T *const out = dx + row * a.lddx;
         auto grad = [&](int p) {
-            return fma2(mul2(pair_of<T>(vy, p), pw[p]), rr, fma2(pair_of<T>(vx, p), cx2, c02));
+            return mul2(fma2(centred(p), c2, fma2(pair_of<T>(vy, p), pw[p], c1)), rr);
         };
         if constexpr (ANY) {
             F2 f[NP];

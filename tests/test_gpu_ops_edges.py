@@ -1,0 +1,93 @@
+"""Training-step operators where their arithmetic or their launches could give way:
+rows far from zero, extreme gradients and factors, several host threads."""
+
+import pytest
+import torch
+
+from gradient_aggregation_gb300 import fc
+from tests import ops_ref
+from tests.ops_ref import U, assert_within, rounded
+from tests.test_gpu_layernorm import matrix, params
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+ids = lambda t: str(t).replace("torch.", "")  # noqa: E731
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(fc_lib):
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield
+
+
+# ---- layer norm backward ---------------------------------------------------------
+
+def backward_with_own_bounds(dy, x, weight, mean, rstd, run=64):
+    """The backward pass in 64 bits and bounds for fp32 arithmetic that follows the
+    definition's order: x - mean is rounded once, and h = (x - mean) * rstd once
+    more, so h is known to 3U of itself however far the row lies from zero."""
+    dy, x = dy.double(), x.double()
+    mean, rstd = mean.double()[:, None], rstd.double()[:, None]
+    w = weight.double()
+    h = (x - mean) * rstd
+    q = dy * w
+    s1, s2 = q.mean(1, keepdim=True), (q * h).mean(1, keepdim=True)
+    dx = rstd * (q - s1 - h * s2)
+    eh = 3 * U * h.abs()
+    # sums of at most 2^14 terms: 32 in a row, the rest in a tree
+    e1 = 45 * U * q.abs().mean(1, keepdim=True)
+    e2 = 45 * U * (q * h).abs().mean(1, keepdim=True) + (q.abs() * eh).mean(1, keepdim=True)
+    edx = rstd * (3 * U * (q.abs() + s1.abs() + (h * s2).abs()) + e1 + h.abs() * e2
+                  + eh * s2.abs()) + 2 * U * dx.abs()
+    add = (run + 24) * U
+    edw = add * (dy * h).abs().sum(0) + (dy.abs() * eh).sum(0)
+    return (dx, (dy * h).sum(0), dy.sum(0)), (edx, edw, add * dy.abs().sum(0))
+
+
+def check_backward(x, dy, cols, eps):
+    rows = x.shape[0]
+    w, b = params(cols, F32, 3)
+    y, dx = torch.empty(rows, cols, dtype=x.dtype, device="cuda"), torch.empty(
+        rows, cols, dtype=x.dtype, device="cuda")
+    mu, rs = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    ws = torch.empty(fc.fc_layernorm_backward_workspace_size(rows, cols), dtype=torch.uint8,
+                     device="cuda")
+    fc.fc_layernorm_forward(x, w, b, eps, y, mu, rs)
+    fc.fc_layernorm_backward(dy, x, w, mu, rs, dx, dw, db, ws)
+    torch.cuda.synchronize()
+    (wdx, wdw, wdb), (edx, edw, edb) = backward_with_own_bounds(dy, x, w, mu, rs)
+    assert_within("dx", dx, wdx, rounded(edx, wdx, x.dtype))
+    assert_within("dweight", dw, wdw, rounded(edw, wdw, F32))
+    assert_within("dbias", db, wdb, rounded(edb, wdb, F32))
+
+
+# one width of each kernel and class: several rows a warp; vectors; rows that start
+# anywhere; halves; more than the registers hold
+@pytest.mark.parametrize("mean", [10.0, 1e3, -3e4])
+@pytest.mark.parametrize("cols,pad", [(64, 0), (100, 1), (128, 0), (256, 0), (1000, 0), (1000, 1),
+                                      (1001, 0), (2048, 0), (4096, 0), (8192, 0), (8190, 3),
+                                      (12288, 0), (12290, 1), (16384, 0), (20001, 0)])
+def test_backward_of_rows_far_from_zero(cols, pad, mean):
+    """The gradients of a row do not depend on its distance from zero."""
+    x, _ = matrix(40, cols, F32, pad, 0, 1, 1.0, mean)
+    dy, _ = matrix(40, cols, F32, pad, 0, 5, 0.5)
+    check_backward(x, dy, cols, 1e-5)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=ids)
+@pytest.mark.parametrize("cols,pad", [(512, 0), (1001, 0), (16384, 0)])
+def test_backward_of_16_bit_rows_far_from_zero(cols, pad, dtype):
+    x, _ = matrix(40, cols, dtype, pad, 0, 1, 30.0, 1000.0)
+    dy, _ = matrix(40, cols, dtype, pad, 0, 5, 0.5)
+    check_backward(x, dy, cols, 1e-5)
+
+
+@pytest.mark.parametrize("cols,pad", [(64, 0), (512, 0), (1001, 0), (16384, 0), (20001, 0)])
+def test_backward_of_rows_of_tiny_variance(cols, pad):
+    """eps = 0 and a spread of 1e-18: rstd is 1e18 and its square times the sum of
+    q h would not fit fp32, the gradient does."""
+    x, _ = matrix(20, cols, F32, pad, 0, 1, 1e-18)
+    dy, _ = matrix(20, cols, F32, pad, 0, 5, 1e4)
+    check_backward(x, dy, cols, 0.0)
