@@ -50,6 +50,8 @@ namespace fc {
 #define FC_ADAM_CW8_SHIFTED 23
 #define FC_ADAM_S8 4
 
+#define FC_ADAM_WAIT_NS 2000000000ull
+
 struct AdamState {
     int64_t N;
     AdamHyper h;
@@ -77,8 +79,10 @@ struct StepScalars {
 // eps are multiplied by 2^20 (exact, and folded into factors that are there
 // anyway), so that g^2 stays a normal fp32 number down to |g| = 1e-24, well
 // below the smallest moments that the blocks can hold relative to each other
-// (fp32 moments end at |g| = 1e-19).
+// (fp32 moments end at |g| = 1e-19).  A unit of 256 elements with a v that is then
+// too large for fp32 (|g| from 1.8e13 on) is done again in units of 2^20.
 #define FC_ADAM8_UNIT 0x1p20f
+#define FC_ADAM8_LARGE 0x1p-20f
 
 // 32-bit mixing by multiplications and xor-shifts (a bijection of 32 bits).
 __device__ __forceinline__ unsigned mix32(unsigned x)
@@ -381,6 +385,12 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c)
     return y;
 }
 
+// x, or the limit with x's sign beyond it; an infinity and a NaN stay.
+__device__ __forceinline__ float finite_at_most(float x, float limit)
+{
+    return fabsf(x) < INFINITY ? fminf(fmaxf(x, -limit), limit) : x;
+}
+
 // A lane's eight elements of a unit with 8-bit moments.  w: updated; mq, rq:
 // e4m3 codes in and out; ms, rs: block scales in and out.  UNIFORM: d[0] is
 // the decay of all eight.
@@ -401,17 +411,25 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c)
 // the code is the bits above bit 20 everywhere.  Adding 20 random bits (16
 // drawn, centred) below the code and cutting rounds up with the probability
 // of what is cut off.  A code of 0 for r > 0 becomes 1.
-template <bool UNIFORM>
-__device__ __forceinline__ void adam8_unit(const float *graw, const float *d, const AdamHyper &h,
+//
+// False, for the whole warp: some v is not finite.  The codes and scales are then
+// untouched and w is lost; marked_units does the step with LARGE.  That always
+// succeeds, and a finite gradient beyond 2^83 (9.7e24) counts as 2^83 there, so that
+// it leaves finite moments and weights; an infinity or a NaN goes through.
+template <bool UNIFORM, bool LARGE = false>
+__device__ __forceinline__ bool adam8_unit(const float *graw, const float *d, const AdamHyper &h,
                                            const StepScalars &sc, int64_t i0, float *w,
                                            uint32_t *mq, uint32_t *rq, float &ms, float &rs)
 {
     F2 m[4], r[4];
-    const float ma = ms * FC_ADAM8_UNIT, ra = rs * FC_ADAM8_UNIT;
-    const F2 ma2 = f2(ma, ma), ra2 = f2(ra, ra), s2 = f2(sc.s, sc.s);
+    constexpr float UNIT = LARGE ? FC_ADAM8_LARGE : FC_ADAM8_UNIT;
+    constexpr float FROM = LARGE ? FC_ADAM8_LARGE / FC_ADAM8_UNIT : 1.f;  // the caller's units
+    const float ma = ms * UNIT, ra = rs * UNIT, s = sc.s * FROM;
+    const float eps = LARGE ? fmaxf(h.eps * FROM, 0x1p-126f) : h.eps;
+    const F2 ma2 = f2(ma, ma), ra2 = f2(ra, ra), s2 = f2(s, s);
     const F2 b12 = f2(h.b1, h.b1), b22 = f2(h.b2, h.b2);
     const F2 omb12 = f2(h.omb1, h.omb1), omb22 = f2(h.omb2, h.omb2);
-    const F2 rc22 = f2(sc.rc2, sc.rc2), eps2 = f2(h.eps, h.eps), lrc2 = f2(-sc.lrc, -sc.lrc);
+    const F2 rc22 = f2(sc.rc2, sc.rc2), eps2 = f2(eps, eps), lrc2 = f2(-sc.lrc, -sc.lrc);
     const float wd0 = -h.lrwd * d[0];
     float mtop = 0.f, rtop = 0.f;
 #pragma unroll
@@ -420,7 +438,11 @@ __device__ __forceinline__ void adam8_unit(const float *graw, const float *d, co
             (__nv_fp8x2_storage_t)(mq[p >> 1] >> (16 * (p & 1))), __NV_E4M3)));
         const float2 cr = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
             (__nv_fp8x2_storage_t)(rq[p >> 1] >> (16 * (p & 1))), __NV_E4M3)));
-        const F2 g = mul2(f2(graw[2 * p], graw[2 * p + 1]), s2);
+        F2 g = mul2(f2(graw[2 * p], graw[2 * p + 1]), s2);
+        if constexpr (LARGE) {
+            const float2 u = un2(g);
+            g = f2(finite_at_most(u.x, 0x1p63f), finite_at_most(u.y, 0x1p63f));
+        }
         const F2 r0 = mul2(f2(cr.x, cr.y), ra2);
         m[p] = add_once(mul2(mul2(f2(cm.x, cm.y), ma2), b12), mul2(g, omb12));
         const F2 v = add_once(mul2(mul2(r0, r0), b22), mul2(mul2(g, g), omb22));
@@ -439,11 +461,14 @@ __device__ __forceinline__ void adam8_unit(const float *graw, const float *d, co
     // magnitudes compare as their bits; a NaN is above all numbers
     mtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mtop)));
     rtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rtop)));
+    // the root of an infinite v is NaN
+    if constexpr (!LARGE)
+        if (!(rtop < INFINITY)) return false;
     // a block below 2^-110 holds zeros; a NaN or an infinity goes into the scale
-    const bool mdead = mtop < 0x1p-110f * FC_ADAM8_UNIT;
-    const bool rdead = rtop < 0x1p-110f * FC_ADAM8_UNIT;
-    ms = mdead ? 0.f : mtop * (1.f / 448.f / FC_ADAM8_UNIT);
-    rs = rdead ? 0.f : rtop * (1.f / 448.f / FC_ADAM8_UNIT);
+    const bool mdead = mtop < 0x1p-110f * UNIT;
+    const bool rdead = rtop < 0x1p-110f * UNIT;
+    ms = mdead ? 0.f : mtop * (1.f / 448.f / UNIT);
+    rs = rdead ? 0.f : rtop * (1.f / 448.f / UNIT);
     // even lanes divide for m, odd ones for r
     const float q448 = 448.f * __frcp_rn((threadIdx.x & 1) ? rtop : mtop);
     const float mto = mdead ? 0.f : __shfl_sync(0xffffffffu, q448, 0);
@@ -477,6 +502,7 @@ __device__ __forceinline__ void adam8_unit(const float *graw, const float *d, co
         rq[q] = __byte_perm(__byte_perm(u[0], u[1], 0x0073), __byte_perm(u[2], u[3], 0x0073),
                             0x5410);
     }
+    return true;
 }
 
 __device__ __forceinline__ void store_low4(void *low, int ltype, int64_t i, const float *w)
@@ -615,26 +641,19 @@ __device__ __forceinline__ void load_unit(const Tab &tab, const AdamState &st, i
     }
 }
 
+// What update_unit or marked_units has made of a unit; of a skipped one the
+// low-precision copy alone.
 template <int BITS>
-__device__ __forceinline__ void update_unit(const AdamState &st, const StepScalars &sc, int64_t un,
-                                            int lane, UnitRegs<BITS> &u)
+__device__ __forceinline__ void store_unit(const AdamState &st, int skip, int64_t un, int lane,
+                                           const UnitRegs<BITS> &u)
 {
     const int64_t lo = un * FC_STATE_BLOCK;
-    if (!sc.skip) {
-        if constexpr (BITS == 32) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                adam1(u.g[j], u.d[j], st.h, sc, u.m[j], u.v[j], u.w[j]);
-        } else {
-            adam8_unit<false>(u.g, u.d, st.h, sc, lo + 4 * lane, u.w, u.mq, u.rq, u.ms, u.rs);
-        }
-    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t a = lo + 4 * lane + 128 * i;
         const bool whole = a + 4 <= st.N;
         const int have = a < st.N ? (int)(st.N - a) : 0;
-        if (!sc.skip) {
+        if (!skip) {
             put4(st.w + a, u.w + 4 * i, whole, have);
             if constexpr (BITS == 32) {
                 put4(st.m + a, u.m + 4 * i, whole, have);
@@ -655,11 +674,71 @@ __device__ __forceinline__ void update_unit(const AdamState &st, const StepScala
         }
     }
     if constexpr (BITS == 8) {
-        if (lane == 0 && !sc.skip) {
+        if (lane == 0 && !skip) {
             st.m_scale[un] = u.ms;
             st.r_scale[un] = u.rs;
         }
     }
+}
+
+// Leaves a unit whose v does not fit the usual units as it is and marks it by the
+// sign of its r_scale.
+__device__ __forceinline__ void mark_unit(const AdamState &st, int64_t un, int lane, float rs)
+{
+    if (lane == 0) st.r_scale[un] = __int_as_float(__float_as_int(rs) | 0x80000000);
+}
+
+// The marked ones of a warp's units, in global memory, once all else is done: CW
+// units a tile, tile after tile of the CTA, and (the last CTA) those behind the last.
+// `drained`: barrier of the copies out, which write what came in, or 0.  Out of
+// line, called once and with little in its arguments: in the loops, or with their
+// variables alive, it cost the usual path 2 to 40 % by the registers that it took.
+template <class GT, class Tab>
+__device__ __noinline__ void marked_units(const Tab *tab, const AdamState *st,
+                                          const StepScalars *sc, int64_t tiles, int CW,
+                                          uint32_t drained)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncwarp();
+    if (drained && !mbar_wait(drained, 0, FC_ADAM_WAIT_NS)) {
+        if (lane == 0) atomicOr(reinterpret_cast<unsigned *>(st->steps) + 1, 0x80000000u);
+        return;
+    }
+    int64_t t = blockIdx.x < tiles ? blockIdx.x : tiles;
+    while (t <= tiles) {
+        const int64_t un = t * CW + warp;
+        const bool own = t < tiles || blockIdx.x == gridDim.x - 1;
+        if (own && un * FC_STATE_BLOCK < st->N &&
+            __float_as_int(__ldcg(st->r_scale + un)) < 0) {
+            UnitRegs<8> u;
+            load_unit<GT, 8>(*tab, *st, un, lane, u);
+            adam8_unit<false, true>(u.g, u.d, st->h, *sc, un * FC_STATE_BLOCK + 4 * lane, u.w,
+                                    u.mq, u.rq, u.ms, u.rs);
+            store_unit<8>(*st, false, un, lane, u);
+        }
+        // behind the CTA's last tile comes what is left behind all of them
+        t = t < tiles && t + gridDim.x > tiles ? tiles : t + gridDim.x;
+    }
+}
+
+// False: the unit has been marked.
+template <int BITS>
+__device__ __forceinline__ bool update_unit(const AdamState &st, const StepScalars &sc, int64_t un,
+                                            int lane, UnitRegs<BITS> &u)
+{
+    if (!sc.skip) {
+        if constexpr (BITS == 32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                adam1(u.g[j], u.d[j], st.h, sc, u.m[j], u.v[j], u.w[j]);
+        } else if (!adam8_unit<false>(u.g, u.d, st.h, sc, un * FC_STATE_BLOCK + 4 * lane, u.w,
+                                      u.mq, u.rq, u.ms, u.rs)) {
+            mark_unit(st, un, lane, u.rs);
+            return false;
+        }
+    }
+    store_unit<BITS>(st, sc.skip, un, lane, u);
+    return true;
 }
 
 // ---- direct kernel ----------------------------------------------------------------------
@@ -683,12 +762,16 @@ __global__ void __launch_bounds__(FC_ADAM_BLOCK)
     const StepScalars sc = sh;
     unsigned arrived = 0;
     if (threadIdx.x == 0 && !sc.skip) arrived = arrive_step(st.steps);
+    bool done = true;
     while (un < units) {
-        update_unit<BITS>(st, sc, un, lane, u);
+        done &= update_unit<BITS>(st, sc, un, lane, u);
         un += stride;
         if (un < units) load_unit<GT, BITS>(tab, st, un, lane, u);
     }
     if (threadIdx.x == 0 && !sc.skip) count_step(st.steps, arrived, sc.t);
+    if constexpr (BITS == 8)
+        if (!done)
+            marked_units<GT>(&tab, &st, &sh, units / (FC_ADAM_BLOCK / 32), FC_ADAM_BLOCK / 32, 0);
 }
 
 // ---- ring kernel ------------------------------------------------------------------------
@@ -697,11 +780,11 @@ __global__ void __launch_bounds__(FC_ADAM_BLOCK)
 // moments.  One thread copies tiles in (bulk copies counted on the stage's
 // `full` barrier), CW warps update one unit each in place, and the same
 // thread copies the stage out again once all have arrived at its `done`
-// barrier; a stage is refilled when its copy out has read it.  The gradient
+// barrier; a stage is refilled when its copy out has read it.  A unit with 8-bit
+// moments that does not fit the usual units is left as it is, its r_scale's sign
+// marks it, and its warp does it from global memory at the end.  The gradient
 // comes straight from its tensor (any alignment), one tile ahead in
 // registers, and the low-precision copy goes out from registers.
-
-#define FC_ADAM_WAIT_NS 2000000000ull
 
 template <int BITS, int CW>
 struct RingStage {
@@ -719,6 +802,8 @@ __global__ void __launch_bounds__((CW + 1) * 32)
     using St = RingStage<BITS, CW>;
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ uint64_t bars[2 * 32];  // full [S], done [S]
+    __shared__ uint64_t drained;       // all copies out are done
+    __shared__ int large[CW];          // whether a warp has marked units
     __shared__ StepScalars sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -726,8 +811,10 @@ __global__ void __launch_bounds__((CW + 1) * 32)
             mbar_init(smem_u32(&bars[s]), 1);
             mbar_init(smem_u32(&bars[S + s]), CW);
         }
+        mbar_init(smem_u32(&drained), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (threadIdx.x < CW) large[threadIdx.x] = 0;
     __syncthreads();
     wait_for_prior_grid();
     allow_dependent_launch();
@@ -777,6 +864,7 @@ __global__ void __launch_bounds__((CW + 1) * 32)
             }
         }
         bulk_wait_all();
+        mbar_arrive(smem_u32(&drained));
         return;
     }
 
@@ -846,13 +934,21 @@ __global__ void __launch_bounds__((CW + 1) * 32)
                     reinterpret_cast<uint32_t *>(stage + St::WB + St::AB) + at;
                 uint32_t mq[2] = {qm[0], qm[32]}, rq[2] = {qr[0], qr[32]};
                 float g[8];
+                bool fits;
                 if (cur.d >= 0) {
                     cur.unpack(g);
-                    adam8_unit<true>(g, &cur.decay, st.h, sc, lo + 4 * lane, w, mq, rq, ms, rs);
+                    fits = adam8_unit<true>(g, &cur.decay, st.h, sc, lo + 4 * lane, w, mq, rq, ms,
+                                            rs);
                 } else {
                     float d[8];
                     gather_unit<GT>(tab, st.N, lo, lane, cur.sg, g, d);
-                    adam8_unit<false>(g, d, st.h, sc, lo + 4 * lane, w, mq, rq, ms, rs);
+                    fits = adam8_unit<false>(g, d, st.h, sc, lo + 4 * lane, w, mq, rq, ms, rs);
+                }
+                if (!fits) {
+                    // the stage goes out as it came; the mark is taken up at the end
+                    mark_unit(st, un, lane, rs);
+                    if (lane == 0) large[warp] = 1;
+                    goto done;
                 }
                 qm[0] = mq[0];
                 qm[32] = mq[1];
@@ -870,6 +966,7 @@ __global__ void __launch_bounds__((CW + 1) * 32)
             store_low4(st.low, st.ltype, lo + 4 * lane, w);
             store_low4(st.low, st.ltype, lo + 4 * lane + 128, w + 4);
         }
+    done:
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars[S + s]));
@@ -883,10 +980,14 @@ __global__ void __launch_bounds__((CW + 1) * 32)
         for (int64_t un = tiles * CW + warp; un * FC_STATE_BLOCK < st.N; un += CW) {
             UnitRegs<BITS> u;
             load_unit<GT, BITS>(tab, st, un, lane, u);
-            update_unit<BITS>(st, sc, un, lane, u);
+            if (!update_unit<BITS>(st, sc, un, lane, u) && lane == 0) large[warp] = 1;
         }
     }
     if (threadIdx.x == 0 && !sc.skip) count_step(st.steps, arrived, sc.t);
+    if constexpr (BITS == 8) {
+        __syncwarp();
+        if (large[warp]) marked_units<GT>(&tab, &st, &sh, tiles, CW, smem_u32(&drained));
+    }
 }
 
 // ---- launches ---------------------------------------------------------------------------

@@ -549,8 +549,9 @@ FC_API fc_status fc_adamw_step(const void *const *grads, int32_t grad_type, int3
  * v moves by 1 - beta2 of itself in a step, far less than half an e4m3 step,
  * so rounding to nearest would leave it where it is.  The random bits are a
  * hash of (seed, t, i / 2): the same arguments give the same bits.  The fp32
- * arithmetic is scaled by 2^20, so that squares hold for |g| from 1e-24 to
- * 1e13; above that v is infinite.
+ * arithmetic is scaled by 2^20, so that squares hold for |g| from 1e-24 on; a
+ * block with a v above 1e26 is scaled by 2^-20 instead, where they hold from
+ * 1e-12 up to 9.7e24, and a larger finite g counts as 9.7e24.
  *  exp_avg_q, exp_rms_q  device e4m3 [N], 16-byte aligned, updated in place.
  *  exp_avg_scale, exp_rms_scale  device fp32 [ceil(N / FC_STATE_BLOCK)].
  * All zero at the start of training.  Everything else as fc_adamw_step. */

@@ -8,6 +8,7 @@ from gradient_aggregation_gb300 import fc
 from tests import ops_ref
 from tests.ops_ref import U, assert_within, rounded
 from tests.test_gpu_layernorm import matrix, params
+from tests.test_gpu_optim import HYPER, State, check_codes, check_step, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,65 @@ def test_backward_of_rows_of_tiny_variance(cols, pad):
     x, _ = matrix(20, cols, F32, pad, 0, 1, 1e-18)
     dy, _ = matrix(20, cols, F32, pad, 0, 5, 1e4)
     check_backward(x, dy, cols, 0.0)
+
+
+# ---- AdamW with 8-bit moments: gradients whose squares do not fit ----------------------
+
+# below 0.9M elements the step's registers hold a unit, above they are streamed
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=ids)
+@pytest.mark.parametrize("sizes", [[256 * 5 + 77], [1 << 20, 151111, 256 + 33]], ids=len)
+@pytest.mark.parametrize("size", [1e12, 2e13, 1e15, 1e18])
+def test_adamw8_large_gradients(size, sizes, dtype):
+    """|g| up to the square root of what fp32 holds, in blocks of their own, in blocks
+    of ordinary ones and in the last block: weights, codes and scales as defined."""
+    grads = [rnd(n, 3 + l) for l, n in enumerate(sizes)]
+    grads[0][:256] *= size
+    if len(grads) > 1:
+        grads[-1][:256] *= size
+    grads[0][700:703] *= size
+    grads[-1][-5:] *= size
+    st = check_step([g.to(dtype) for g in grads], sizes, 8, F16, 0, HYPER, scale=None, fresh=True)
+    assert bool((st.rs >= 0).all())
+
+
+def test_adamw8_goes_on_after_large_gradients():
+    """The blocks come back to ordinary gradients by their averages, and the state
+    stays that of the definition, step after step."""
+    n = 1 << 20
+    st = State(n, 8, None, fresh=True)
+    big, small = rnd(n, 1, 1e3), rnd(n, 2)
+    big[::3000] *= 1e14
+    h = dict(HYPER, b1=0.5, b2=0.5)
+    for k, g in enumerate((big, small, small, small)):
+        m0, v0 = st.moments()
+        w0 = st.w.clone()
+        st.step(fc.LayerGrads([g]), None, h)
+        torch.cuda.synchronize()
+        (w, m, v), (ew, em, ev) = ops_ref.adamw(w0, m0, v0, g, torch.ones_like(w0), k + 1, **h)
+        em, ev = em + U * m0.abs(), ev + 3 * U * v0
+        ew = ew + (h["lr"] / (1 - h["b1"] ** (k + 1))) * U * m0.abs() / (
+            torch.sqrt(v / (1 - h["b2"] ** (k + 1))) + h["eps"]) + 0.1 * ew
+        assert_within("w", st.w, w, ew)
+        check_codes(st.m8, st.ms, m, em, None)
+
+
+@pytest.mark.parametrize("n", [1000, 1 << 20])
+def test_adamw8_finite_gradients_leave_a_finite_state(n):
+    """Up to the largest fp32 number: beyond 9.7e24 a gradient counts as that."""
+    g = rnd(n, 5)
+    g[100], g[400], g[900] = 3e38, -3e38, 1e30
+    st = State(n, 8, F16, fresh=True)
+    for _ in range(3):
+        st.step(fc.LayerGrads([g]), None)
+        torch.cuda.synchronize()
+        for t in (st.w, st.ms, st.rs, st.m8.float(), st.r8.float()):
+            assert bool(t.isfinite().all())
+        assert bool((st.rs >= 0).all())
+    assert float(st.m8[100]) * float(st.ms[0]) > 1e24
+    # an element of its own block moves as one of an ordinary size does
+    assert abs(float(st.w[900] - State(n, 8, F16, fresh=True).w[900])) < 4 * HYPER["lr"]
+    # and one that is not finite still shows
+    g[100] = float("inf")
+    st.step(fc.LayerGrads([g]), None)
+    torch.cuda.synchronize()
+    assert not bool(st.w[100].isfinite())
