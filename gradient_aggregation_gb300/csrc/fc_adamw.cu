@@ -24,11 +24,14 @@
 // Two kernels hold the same arithmetic: k_adamw_ring streams weights and
 // moments through shared memory with bulk copies in both directions;
 // k_adamw_direct loads and stores them from registers, which starts faster and
-// serves what is resident at once.  Measured (ring): 279 us for 62.4M elements
-// with fp32 moments, fp32 gradients and an fp16 copy (1.87 GB, 6.7 TB/s); 159
+// serves what is resident at once.  Measured (ring): 278 us for 62.4M elements
+// with fp32 moments, fp32 gradients and an fp16 copy (1.87 GB, 6.7 TB/s); 160
 // us with 8-bit moments and fp16 gradients (1.0 GB, 6.3 TB/s); direct: 3.9 us
 // for 133k elements.
 #include <cuda_fp8.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "fc_bulk.cuh"
 #include "fc_opt.h"
@@ -39,15 +42,16 @@ namespace fc {
 #define FC_ADAM_BLOCK 256
 
 // Consumer warps of the ring kernel (so units a tile) and its stages.  A tile
-// of 20 units is copied in pieces of 20 KB; with 8 KB pieces the 62M-element
-// step with fp32 moments took 320 us, with 16 KB 286, with 20 KB 279.  With
-// 8-bit moments the update itself needs the warps: 24 of them took 159 us, 23
-// 161, 20 163, 27 161.  Where gradients are shifted, 24 warps with 72 registers
-// are worse than 23 with 80: 26.8 and 25.2 us for 7M elements.
-#define FC_ADAM_CW32 20
+// of 19 units is copied in pieces of 19 KB; with 8 KB pieces the 62M-element
+// step with fp32 moments took 320 us, with 16 KB 286, with 19 and 20 KB 278 and 280
+// (fp32 gradients in 600 layers, 20M elements: 96 and 103 us: 20 warps and the copying
+// one have 80 registers each, 19 have 96).  With 8-bit moments the update itself
+// needs the warps: 23 of them have 80 registers, 24 or more have 72.  62M elements of
+// fp16 / bf16 / fp32 160 / 160 / 176 us (24: 173 / 176 / 185, 27: 159 / 159 / 176), 7M
+// in odd layers 24.1 / 24.2 / 29.4 (24: 28.4 / 28.4 / 29.7).
+#define FC_ADAM_CW32 19
 #define FC_ADAM_S32 3
-#define FC_ADAM_CW8 24
-#define FC_ADAM_CW8_SHIFTED 23
+#define FC_ADAM_CW8 23
 #define FC_ADAM_S8 4
 
 #define FC_ADAM_WAIT_NS 2000000000ull
@@ -64,6 +68,8 @@ struct AdamState {
     float *m_scale, *r_scale;
     int32_t *steps;
     uint64_t seed;
+    uint64_t limit_ns;  // of a wait for a copy or for the consumers
+    int64_t drop;       // tile that is not copied in (test hook), -1: none
 };
 
 struct StepScalars {
@@ -71,7 +77,6 @@ struct StepScalars {
     float lrc;   // lr / c1
     float rc2;   // 1 / sqrt(c2)
     unsigned key;
-    int32_t t;
     int skip;
 };
 
@@ -107,7 +112,6 @@ __device__ __forceinline__ void load_scalars(StepScalars &sh, const AdamState &s
     if (lane == 0) {
         sh.lrc = __fdividef(st.h.lr, c);
         sh.s = BITS == 8 ? s * FC_ADAM8_UNIT : s;
-        sh.t = t;
         sh.skip = !isfinite(s);
         sh.key = mix32((unsigned)st.seed ^ mix32((unsigned)(st.seed >> 32) ^ mix32((unsigned)t)));
     } else if (lane == 1) {
@@ -118,6 +122,14 @@ __device__ __forceinline__ void load_scalars(StepScalars &sh, const AdamState &s
 // Each CTA arrives at steps[1] once it has read steps[0], and the last to
 // arrive counts the step, so no CTA can read the new count.  The arrival is
 // issued early and its answer only looked at when the CTA's work is done.
+//
+// Bit 31 of steps[1] says that a wait has run out, in this launch or an earlier one
+// (FC_ADAM_LOST), and no such step is counted.  It may be set before the last CTA
+// arrives, which sees it then, or later: then the step is counted, or will be,
+// and whoever sets the bit takes the count back.  Additions on both sides, so
+// their order does not matter, and nothing that is waited for.
+#define FC_ADAM_LOST 0x80000000u
+
 __device__ __forceinline__ unsigned arrive_step(int32_t *steps)
 {
     unsigned old;
@@ -128,12 +140,22 @@ __device__ __forceinline__ unsigned arrive_step(int32_t *steps)
     return old;
 }
 
-__device__ __forceinline__ void count_step(int32_t *steps, unsigned arrived, int32_t t)
+__device__ __forceinline__ void count_step(int32_t *steps, unsigned arrived)
 {
-    if (arrived == gridDim.x - 1) {
-        steps[0] = t;
-        steps[1] = 0;
+    if ((arrived & ~FC_ADAM_LOST) == gridDim.x - 1) {
+        if (!(arrived & FC_ADAM_LOST)) atomicAdd(steps, 1);
+        atomicSub(reinterpret_cast<unsigned *>(steps) + 1, gridDim.x);
     }
+}
+
+// A wait has run out in a CTA that has arrived (skip: none does).
+__device__ __forceinline__ void step_lost(int32_t *steps, int skip)
+{
+    const unsigned old = atomicOr(reinterpret_cast<unsigned *>(steps) + 1, FC_ADAM_LOST);
+    const unsigned arrived = old & ~FC_ADAM_LOST;
+    // all have arrived, or that is over
+    if (!(old & FC_ADAM_LOST) && !skip && (arrived == gridDim.x || arrived == 0))
+        atomicSub(steps, 1);
 }
 
 __device__ __forceinline__ float as_f32(float x) { return x; }
@@ -700,8 +722,8 @@ __device__ __noinline__ void marked_units(const Tab *tab, const AdamState *st,
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __syncwarp();
-    if (drained && !mbar_wait(drained, 0, FC_ADAM_WAIT_NS)) {
-        if (lane == 0) atomicOr(reinterpret_cast<unsigned *>(st->steps) + 1, 0x80000000u);
+    if (drained && !mbar_wait(drained, 0, st->limit_ns)) {
+        if (lane == 0) step_lost(st->steps, 0);
         return;
     }
     int64_t t = blockIdx.x < tiles ? blockIdx.x : tiles;
@@ -768,7 +790,7 @@ __global__ void __launch_bounds__(FC_ADAM_BLOCK)
         un += stride;
         if (un < units) load_unit<GT, BITS>(tab, st, un, lane, u);
     }
-    if (threadIdx.x == 0 && !sc.skip) count_step(st.steps, arrived, sc.t);
+    if (threadIdx.x == 0 && !sc.skip) count_step(st.steps, arrived);
     if constexpr (BITS == 8)
         if (!done)
             marked_units<GT>(&tab, &st, &sh, units / (FC_ADAM_BLOCK / 32), FC_ADAM_BLOCK / 32, 0);
@@ -780,11 +802,12 @@ __global__ void __launch_bounds__(FC_ADAM_BLOCK)
 // moments.  One thread copies tiles in (bulk copies counted on the stage's
 // `full` barrier), CW warps update one unit each in place, and the same
 // thread copies the stage out again once all have arrived at its `done`
-// barrier; a stage is refilled when its copy out has read it.  A unit with 8-bit
-// moments that does not fit the usual units is left as it is, its r_scale's sign
-// marks it, and its warp does it from global memory at the end.  The gradient
+// barrier; a stage is refilled when its copy out has read it.  That thread also
+// counts the step: the warps have no registers to spare.  The gradient
 // comes straight from its tensor (any alignment), one tile ahead in
-// registers, and the low-precision copy goes out from registers.
+// registers, and the low-precision copy goes out from registers.  A unit with
+// 8-bit moments that does not fit the usual units is left as it is, its r_scale's
+// sign marks it, and its warp does it from global memory at the end.
 
 template <int BITS, int CW>
 struct RingStage {
@@ -832,24 +855,34 @@ __global__ void __launch_bounds__((CW + 1) * 32)
             const int64_t t = blockIdx.x + it * gridDim.x;
             const uint32_t full = smem_u32(&bars[s]);
             const uint32_t to = smem_u32(stages) + (uint32_t)s * St::BYTES;
+            if (t == st.drop) return;
             mbar_expect_tx(full, St::BYTES);
             bulk_g2s(to, gw + t * St::WB, St::WB, full);
             bulk_g2s(to + St::WB, ga + t * St::AB, St::AB, full);
             bulk_g2s(to + St::WB + St::AB, gb + t * St::AB, St::AB, full);
         };
         int64_t filled = 0;
+        unsigned arrived = 0;
+        int skip = 0;
         for (; filled < n && filled < S; ++filled) fill(filled);
         for (int64_t it = 0; it < n; ++it) {
             const int s = (int)(it % S);
-            if (!mbar_wait(smem_u32(&bars[S + s]), (uint32_t)(it / S) & 1, FC_ADAM_WAIT_NS)) {
+            const bool done = mbar_wait(smem_u32(&bars[S + s]), (uint32_t)(it / S) & 1, st.limit_ns);
+            if (it == 0) {
+                // the consumers have read the step's scalars (long ago, if one of
+                // them has given up)
+                skip = *(volatile int *)&sh.skip;
+                if (!skip) arrived = arrive_step(st.steps);
+            }
+            if (!done) {
                 // not expected: no more copies out; those coming in must have
                 // landed before the shared memory may go
-                atomicOr(reinterpret_cast<unsigned *>(st.steps) + 1, 0x80000000u);
+                step_lost(st.steps, skip);
                 for (int64_t j = it; j < filled; ++j)
-                    mbar_wait(smem_u32(&bars[j % S]), (uint32_t)(j / S) & 1, FC_ADAM_WAIT_NS);
+                    mbar_wait(smem_u32(&bars[j % S]), (uint32_t)(j / S) & 1, st.limit_ns);
                 break;
             }
-            if (!sh.skip) {
+            if (!skip) {
                 const int64_t t = blockIdx.x + it * gridDim.x;
                 const uint32_t from = smem_u32(stages) + (uint32_t)s * St::BYTES;
                 bulk_s2g(const_cast<char *>(gw) + t * St::WB, from, St::WB);
@@ -865,6 +898,7 @@ __global__ void __launch_bounds__((CW + 1) * 32)
         }
         bulk_wait_all();
         mbar_arrive(smem_u32(&drained));
+        if (!skip) count_step(st.steps, arrived);
         return;
     }
 
@@ -884,16 +918,12 @@ __global__ void __launch_bounds__((CW + 1) * 32)
     if (warp == 0) load_scalars<BITS>(sh, st);
     asm volatile("bar.sync 1, %0;" ::"n"(CW * 32) : "memory");
     const StepScalars sc = sh;
-    unsigned arrived = 0;
-    if (threadIdx.x == 0 && !sc.skip) arrived = arrive_step(st.steps);
     int s = 0;
     uint32_t phase = 0;
     for (int64_t it = 0; it < n; ++it) {
         unsigned char *const stage = stages + (size_t)s * St::BYTES;
-        if (!mbar_wait(smem_u32(&bars[s]), phase, FC_ADAM_WAIT_NS)) {
-            if (lane == 0) atomicOr(reinterpret_cast<unsigned *>(st.steps) + 1, 0x80000000u);
-            return;
-        }
+        // given up, it is missed at the stage's `done` barrier
+        if (!mbar_wait(smem_u32(&bars[s]), phase, st.limit_ns)) return;
         const int64_t un = unit(it);
         const int64_t lo = un * FC_STATE_BLOCK;
         const UnitGrad<GT, SHIFTED> cur = next;
@@ -983,7 +1013,6 @@ __global__ void __launch_bounds__((CW + 1) * 32)
             if (!update_unit<BITS>(st, sc, un, lane, u) && lane == 0) large[warp] = 1;
         }
     }
-    if (threadIdx.x == 0 && !sc.skip) count_step(st.steps, arrived, sc.t);
     if constexpr (BITS == 8) {
         __syncwarp();
         if (large[warp]) marked_units<GT>(&tab, &st, &sh, tiles, CW, smem_u32(&drained));
@@ -1023,15 +1052,25 @@ static bool any_shifted(const Tab &tab)
     return false;
 }
 
+// Test hook (fc_test_adamw_loss): a tile that the next streamed launch does not copy
+// in, and the limit of that launch's waits.
+static std::atomic<int64_t> g_drop_tile{-1};
+static std::atomic<uint64_t> g_drop_limit_ns{0};
+
 template <class GT, int BITS, bool SHIFTED, class Tab>
-static cudaError_t launch_ring(const Tab &tab, const AdamState &st, cudaStream_t s)
+static cudaError_t launch_ring(const Tab &tab, AdamState st, cudaStream_t s)
 {
-    constexpr int CW = BITS == 32 ? FC_ADAM_CW32 : SHIFTED ? FC_ADAM_CW8_SHIFTED : FC_ADAM_CW8;
+    constexpr int CW = BITS == 32 ? FC_ADAM_CW32 : FC_ADAM_CW8;
     constexpr int S = BITS == 32 ? FC_ADAM_S32 : FC_ADAM_S8;
     static_assert(S >= 2 && S <= 32, "a stage is refilled while the next one is worked on");
     using St = RingStage<BITS, CW>;
     const size_t smem = (size_t)S * St::BYTES;
     const int64_t tiles = st.N / St::T;
+    st.drop = g_drop_tile.exchange(-1);
+    if (st.drop >= 0) {
+        st.drop = std::min(st.drop, tiles - 1);
+        st.limit_ns = g_drop_limit_ns.load();
+    }
     const void *ring = (const void *)k_adamw_ring<GT, BITS, CW, SHIFTED, Tab>;
     cudaError_t e =
         cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -1079,6 +1118,8 @@ cudaError_t launch_adamw(const Tab &tab, int gtype, int64_t N, const AdamHyper &
     st.m = m;
     st.v = v;
     st.steps = steps;
+    st.limit_ns = FC_ADAM_WAIT_NS;
+    st.drop = -1;
     return launch_bits<32>(tab, gtype, st, s);
 }
 
@@ -1102,6 +1143,8 @@ cudaError_t launch_adamw8(const Tab &tab, int gtype, int64_t N, const AdamHyper 
     st.r_scale = r_scale;
     st.steps = steps;
     st.seed = seed;
+    st.limit_ns = FC_ADAM_WAIT_NS;
+    st.drop = -1;
     return launch_bits<8>(tab, gtype, st, s);
 }
 
@@ -1117,3 +1160,12 @@ FC_INST(OptTableS)
 FC_INST(OptTableL)
 
 }  // namespace fc
+
+extern "C" fc_status fc_test_adamw_loss(int64_t tile, uint64_t wait_limit_ns)
+{
+    if (tile >= 0 && (wait_limit_ns < 1000000ull || wait_limit_ns > 2000000000ull))
+        return fc::set_error(FC_ERR_INVALID_ARG, "wait_limit_ns must be in [1 ms, 2 s]");
+    fc::g_drop_limit_ns.store(wait_limit_ns);
+    fc::g_drop_tile.store(tile < 0 ? -1 : tile);
+    return FC_OK;
+}

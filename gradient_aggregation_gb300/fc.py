@@ -69,6 +69,7 @@ _SIGS = {
     "fc_test_stage_loss": (ctypes.c_int, [_I64, ctypes.c_uint64]),
     "fc_test_one_launch_kind": (ctypes.c_int, [_I32]),
     "fc_test_barrier_loss": (ctypes.c_int, [_I32, ctypes.c_uint64]),
+    "fc_test_adamw_loss": (ctypes.c_int, [_I64, ctypes.c_uint64]),
     "fc_step_reduce": (ctypes.c_int, [_P, _I32, _I32, _P, _F32, _I64, _P, _P, _P, _SZ, _P]),
     "fc_step_select": (ctypes.c_int, [_I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "fc_step_update": (ctypes.c_int, [_P, _I64, _I64, _F32, _F32, _P, _P, _P, _P, _P, _P, _P,
@@ -233,6 +234,12 @@ def fc_test_barrier_loss(cta: int, wait_limit_ns: int = 20_000_000) -> None:
     grid barrier and the others wait at most wait_limit_ns (see
     include/fc.h)."""
     _check(lib().fc_test_barrier_loss(int(cta), int(wait_limit_ns)))
+
+
+def fc_test_adamw_loss(tile: int, wait_limit_ns: int = 20_000_000) -> None:
+    """Test hook: the next streamed AdamW step copies in nothing for `tile` and
+    bounds its waits by wait_limit_ns (see include/fc.h)."""
+    _check(lib().fc_test_adamw_loss(int(tile), int(wait_limit_ns)))
 
 
 # ---- the five calls ---------------------------------------------------------------
@@ -744,7 +751,15 @@ class AdamWEngine:
             fc_adamw8_step(*head, self.exp_avg_q, self.exp_avg_scale, self.exp_rms_q,
                            self.exp_rms_scale, self.steps, self.seed, stream)
 
+    def status(self) -> int:
+        """FC_OK, or FC_ERR_TIMEOUT once a bounded wait inside a step has run out: the
+        state is then updated in part, and load_state_dict brings a whole one back.
+        Waits for the GPU."""
+        return FC_ERR_TIMEOUT if int(self.steps[1]) < 0 else FC_OK
+
     def state_dict(self) -> dict:
+        if self.status() != FC_OK:
+            raise FcError(FC_ERR_TIMEOUT, "a step was applied in part: no state to save")
         return {k: getattr(self, k).clone()
                 for k in ("weights", "steps") + self.STATE[self.bits]}
 

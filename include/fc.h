@@ -520,7 +520,9 @@ FC_API fc_status fc_grad_norm(const void *const *grads, int32_t grad_type, int32
  *               steps[0] counts the steps applied, steps[1] belongs to the
  *               kernel (zero between calls).  steps[1] < 0 after a call says
  *               that a bounded wait of the kernel ran out (not expected): the
- *               state is updated in part and no further step is counted.
+ *               state is updated in part, the step is not counted, and no
+ *               later one is until both words are set again, beside a state
+ *               that is whole.
  * lr, weight_decay finite and >= 0; 0 <= beta1, beta2 < 1; eps > 0 in fp32.
  * The moments, weights and gradients must not overlap one another. */
 FC_API fc_status fc_adamw_step(const void *const *grads, int32_t grad_type, int32_t L,
@@ -638,6 +640,15 @@ FC_API fc_status fc_test_one_launch_kind(int32_t kind);
  * step.  cta < 0 disarms.  Host only; the next such launch from any thread
  * consumes it. */
 FC_API fc_status fc_test_barrier_loss(int32_t cta, uint64_t wait_limit_ns);
+
+/* Exercises the failure path of the AdamW steps that stream their state through
+ * shared memory (those of more than about 0.9M elements).  Arms the next such
+ * launch to copy in nothing for its tile `tile` (clamped to the last; 4864
+ * elements, 5888 with 8-bit moments), with its waits bounded by
+ * wait_limit_ns (1 ms .. 2 s) instead of 2 s: they run out, and steps[1] says so.
+ * tile < 0 disarms the hook.  Host only; the next such launch from any thread
+ * consumes it. */
+FC_API fc_status fc_test_adamw_loss(int64_t tile, uint64_t wait_limit_ns);
 
 #ifdef __cplusplus
 }

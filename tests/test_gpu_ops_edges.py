@@ -154,3 +154,67 @@ def test_adamw8_finite_gradients_leave_a_finite_state(n):
     st.step(fc.LayerGrads([g]), None)
     torch.cuda.synchronize()
     assert not bool(st.w[100].isfinite())
+
+
+# ---- AdamW: a wait that runs out ------------------------------------------------------
+
+@pytest.mark.parametrize("skip", [False, True])
+@pytest.mark.parametrize("tile", [0, 1, 100, 1 << 40])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_wait_that_runs_out(bits, tile, skip):
+    """The failure path of the streamed step, without any fault: a tile that is not
+    copied in.  The record stays whichever block finishes last, neither that step
+    nor a later one is counted, and the tile keeps its weights; from a whole
+    state the steps go on as if nothing had been."""
+    n, done = 1_300_001, 7
+    g = rnd(n, 1)
+    table = fc.LayerGrads([g])
+    scale = torch.tensor([float("nan") if skip else 1.0], device="cuda")
+    st, ref = State(n, bits, BF16, done), State(n, bits, BF16, done)
+    whole = st.copies()
+    ref.step(table, None)
+    fc.fc_test_adamw_loss(tile)
+    st.step(table, scale)
+    torch.cuda.synchronize()
+    st.check_guards()
+    assert int(st.steps[0]) == done and int(st.steps[1]) == -(1 << 31)
+    same = st.w == whole["w"]
+    assert bool(((st.w == ref.w) | same).all())
+    # a tile, and what its block had still to do, or nothing at all
+    assert bool(same.all()) if skip else 4608 <= int(same.sum()) <= 30000
+    st.step(table, None)
+    torch.cuda.synchronize()
+    assert int(st.steps[0]) == done and int(st.steps[1]) == -(1 << 31)
+    for k, v in whole.items():
+        getattr(st, k).copy_(v)
+    st.step(table, None)
+    torch.cuda.synchronize()
+    want = ref.copies()
+    for k, v in st.copies().items():
+        assert torch.equal(v.view(torch.uint8), want[k].view(torch.uint8)), k
+    assert st.steps.tolist() == [done + 1, 0]
+
+
+def test_engine_tells_of_a_wait_that_ran_out():
+    sizes, W = [1_200_000], 2
+    grads = [[rnd(sizes[0], w, 1.0, F16)] for w in range(W)]
+    eng = fc.AdamWEngine(sizes, W, rnd(sizes[0], 9), lr=1e-3, loss_scale=64.0)
+    eng.step(grads)
+    assert eng.status() == fc.FC_OK
+    saved = eng.state_dict()
+    fc.fc_test_adamw_loss(3)
+    eng.step(grads)
+    assert eng.status() == fc.FC_ERR_TIMEOUT
+    with pytest.raises(fc.FcError) as e:
+        eng.state_dict()
+    assert e.value.status == fc.FC_ERR_TIMEOUT
+    eng.load_state_dict(saved)
+    eng.step(grads)
+    assert eng.status() == fc.FC_OK and eng.steps.tolist() == [2, 0]
+
+
+def test_adamw_loss_hook_refusals():
+    for limit in (0, 999_999, 2_000_000_001):
+        with pytest.raises(fc.FcError):
+            fc.fc_test_adamw_loss(0, limit)
+    fc.fc_test_adamw_loss(-1, 0)
