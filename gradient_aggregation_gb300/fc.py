@@ -739,6 +739,11 @@ class AdamWEngine:
         self._norm_ws = torch.zeros(fc_grad_norm_workspace_size(), dtype=torch.uint8, device=dev)
 
     def step(self, grads, stream=None) -> None:
+        grads = _table(grads)
+        # the reduction writes as many elements as the gradients have
+        if grads.W != self.W or grads.sizes != self.sizes:
+            raise ValueError("the gradients must be %d workers' layers of the engine's sizes"
+                             % self.W)
         fc_step_reduce_ordered(grads, self.loss_scale, self._chunk, None, self.a, self.order,
                                self._reduce_ws, stream)
         # the mean is unscaled already

@@ -218,3 +218,21 @@ def test_adamw_loss_hook_refusals():
         with pytest.raises(fc.FcError):
             fc.fc_test_adamw_loss(0, limit)
     fc.fc_test_adamw_loss(-1, 0)
+
+
+# ---- calls whose tensors do not fit: refused before anything is launched ---------------
+
+def test_engine_refuses_gradients_of_another_layout():
+    """The buffers of the engine hold its own sizes, no others."""
+    sizes, W = [300, 77], 2
+    eng = fc.AdamWEngine(sizes, W, rnd(377, 9), lr=1e-3, loss_scale=1.0)
+    half = lambda *ns: [torch.zeros(n, device="cuda", dtype=F16) for n in ns]  # noqa: E731
+    for grads in ([half(300, 77)], [half(300, 77)] * 3, [half(77, 300)] * 2,
+                  [half(300, 77, 4000)] * 2, [half(4000, 77)] * 2, [half(300)] * 2):
+        with pytest.raises(ValueError):
+            eng.step(grads)
+        with pytest.raises(ValueError):
+            eng.step(fc.PtrTable(grads))
+    eng.step([half(300, 77)] * 2)
+    torch.cuda.synchronize()
+    assert eng.steps.tolist() == [1, 0]
