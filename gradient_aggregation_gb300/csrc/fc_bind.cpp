@@ -110,6 +110,14 @@ void *matrix(const at::Tensor &t, const at::Tensor &x, const char *name, int dev
     return t.data_ptr();
 }
 
+// Scratch of any type: its bytes are its elements', one after another.
+void *scratch(const at::Tensor &t, int dev)
+{
+    on_gpu(t, dev, "workspace");
+    if (!t.is_contiguous()) refuse("workspace must be contiguous");
+    return t.data_ptr();
+}
+
 int64_t integer(PyObject *o)
 {
     const long long v = PyLong_AsLongLong(o);
@@ -179,10 +187,10 @@ PyObject *grad_norm(PyObject *, PyObject *const *args, Py_ssize_t n)
     return call(args, n, 7, [](PyObject *const *a) {
         const Layers l(a[0]);
         const at::Tensor &ws = needed(a[5], "workspace");
-        on_gpu(ws, l.dev, "workspace");
+        void *const p = scratch(ws, l.dev);
         return p_grad_norm(l.grads, l.type, l.L, l.sizes, (float)number(a[1]),
                            (float)number(a[2]), flat32(a[3], 1, "norm", l.dev),
-                           flat32(a[4], 1, "scale", l.dev), ws.data_ptr(), ws.nbytes(),
+                           flat32(a[4], 1, "scale", l.dev), p, ws.nbytes(),
                            stream(a[6], l.dev));
     });
 }
@@ -305,12 +313,11 @@ PyObject *layernorm_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
             gtype = kind;
         }
         const at::Tensor *ws = tensor(a[8], "workspace");
-        if (ws) on_gpu(*ws, x.dev, "workspace");
+        void *const p = ws ? scratch(*ws, x.dev) : nullptr;
         return p_layernorm_backward(dy, lddy, x.p, x.ld, x.type, w, ptype,
                                     flat32(a[3], x.rows, "mean", x.dev),
                                     flat32(a[4], x.rows, "rstd", x.dev), x.rows, x.cols, dx,
-                                    lddx, dw, db, gtype, ws ? ws->data_ptr() : nullptr,
-                                    ws ? ws->nbytes() : 0, stream(a[9], x.dev));
+                                    lddx, dw, db, gtype, p, ws ? ws->nbytes() : 0, stream(a[9], x.dev));
     });
 }
 

@@ -236,3 +236,19 @@ def test_engine_refuses_gradients_of_another_layout():
     eng.step([half(300, 77)] * 2)
     torch.cuda.synchronize()
     assert eng.steps.tolist() == [1, 0]
+
+
+def test_workspaces_have_the_bytes_that_they_name():
+    """An expanded or strided tensor has more elements than memory, or gaps."""
+    g = torch.zeros(400, device="cuda")
+    norm, scale = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")
+    need = fc.fc_grad_norm_workspace_size()
+    x = torch.zeros(8, 400, device="cuda")
+    dx, w, st = torch.empty_like(x), torch.ones(400, device="cuda"), torch.zeros(8, device="cuda")
+    most = max(need, fc.fc_layernorm_backward_workspace_size(8, 400))
+    for ws in (torch.zeros(1, dtype=torch.uint8, device="cuda").expand(most),
+               torch.zeros(2 * most, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            fc.fc_grad_norm(fc.LayerGrads([g]), 1.0, 0.0, norm, scale, ws)
+        with pytest.raises(ValueError):
+            fc.fc_layernorm_backward(x, x, w, st, st, dx, w.clone(), w.clone(), ws)
