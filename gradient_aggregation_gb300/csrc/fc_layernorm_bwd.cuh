@@ -543,9 +543,11 @@ struct RingLaunch {
     cudaError_t prepare(const LnBackward &a)
     {
         const void *k = (const void *)kernel;
-        smem = std::max<size_t>((size_t)D * (BLOCK / 32) * 2 * warp_slots<K, ANY>() * 16,
-                                2 * sizeof(float) * (size_t)G *
-                                    (CL == 1 ? ln_padded(a.cols) : TPR * K * (16 / sizeof(T))));
+        // the same for every width: the ring has room for the sums of the widest row
+        smem = (size_t)D * (BLOCK / 32) * 2 * warp_slots<K, ANY>() * 16;
+        static_assert((size_t)D * (BLOCK / 32) * 2 * 32 * K * 16 >=
+                          2 * sizeof(float) * (size_t)G * TPR * K * (16 / sizeof(T)),
+                      "the sums lie where the ring was");
         ctas = (a.rows + G - 1) / G;
         cudaError_t e =
             cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

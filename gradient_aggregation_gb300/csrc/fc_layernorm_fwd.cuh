@@ -506,9 +506,12 @@ static cudaError_t go_rows(const LnForward &a, cudaStream_t s)
     constexpr int BLOCK = TPR >= 256 ? 512 : 256;
     const auto kernel = k_ln_fwd_rows<T, K, TPR, RW, BLOCK>;
     const size_t smem = 2 * sizeof(float) * (size_t)a.cols;
-    if (smem > 40 * 1024) {
+    // what the widest row of the class needs: the limit belongs to the kernel, and
+    // calls of other widths on other host threads must not lower it before this launch
+    constexpr size_t most = 2 * sizeof(float) * (size_t)(K * TPR * (16 / (int)sizeof(T)));
+    if (most > 40 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(
-            (const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            (const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
     }
     const int64_t per = BLOCK / TPR * RW;
@@ -524,10 +527,15 @@ static cudaError_t go_any(const LnForward &a, cudaStream_t s)
 {
     constexpr int BLOCK = TPR >= 256 ? 512 : 256, D = 3;
     const auto kernel = k_ln_fwd_any<T, K, TPR, BLOCK, D>;
-    const size_t smem = (size_t)D * (BLOCK / 32) * warp_slots<K, true>() * 16 +
-                        2 * sizeof(float) * (size_t)((a.cols + 255) & ~(int64_t)255);
+    constexpr size_t slots = (size_t)D * (BLOCK / 32) * warp_slots<K, true>() * 16;
+    const size_t smem =
+        slots + 2 * sizeof(float) * (size_t)((a.cols + 255) & ~(int64_t)255);
+    // as in go_rows: the widest row's
+    constexpr size_t most =
+        slots + 2 * sizeof(float) * (size_t)((K * TPR * (16 / (int)sizeof(T)) + 255) & ~255);
+    static_assert(most + 256 <= 227 * 1024, "a block's shared memory");
     cudaError_t e = cudaFuncSetAttribute((const void *)kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
     const int grid =

@@ -1,6 +1,8 @@
 """Training-step operators where their arithmetic or their launches could give way:
 rows far from zero, extreme gradients and factors, several host threads."""
 
+import threading
+
 import pytest
 import torch
 
@@ -252,3 +254,37 @@ def test_workspaces_have_the_bytes_that_they_name():
             fc.fc_grad_norm(fc.LayerGrads([g]), 1.0, 0.0, norm, scale, ws)
         with pytest.raises(ValueError):
             fc.fc_layernorm_backward(x, x, w, st, st, dx, w.clone(), w.clone(), ws)
+
+
+# ---- calls on several host threads -----------------------------------------------------
+
+@pytest.mark.parametrize("pair", [(12291, 16383), (6152, 8192), (8200, 12288), (1537, 2047)])
+def test_layernorm_widths_of_one_kernel_on_several_host_threads(pair):
+    """Two widths that one kernel serves, called through the C ABI (which, unlike the
+    binding, lets go of the interpreter) from four host threads on their own streams:
+    no call takes away what another one's launch needs."""
+    L, rows, rounds, failed = fc.lib(), 200, 2000, []
+
+    def run(cols, seed):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            x = rnd(rows * cols, seed, 1.0, BF16).view(rows, cols)
+            y, want = torch.empty_like(x), torch.empty_like(x)
+            fc.fc_layernorm_forward(x, None, None, 1e-5, want)
+            args = (x.data_ptr(), rows, cols, cols, fc.FC_TYPE_BF16, None, None, 0, 1e-5,
+                    y.data_ptr(), cols, None, None, s.cuda_stream)
+            for _ in range(rounds):
+                st = L.fc_layernorm_forward(*args)
+                if st:
+                    failed.append((cols, st, L.fc_last_error()))
+                    return
+            s.synchronize()
+            if not torch.equal(y, want):
+                failed.append((cols, "other values"))
+
+    threads = [threading.Thread(target=run, args=(pair[i % 2], i)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
