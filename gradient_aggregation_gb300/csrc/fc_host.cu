@@ -1,6 +1,9 @@
 // Host-side helpers of the kernels' launchers: the layer table and the
 // launch-size cache.
+#include <atomic>
 #include <mutex>
+#include <new>
+#include <unordered_map>
 
 #include "fc_internal.h"
 
@@ -76,35 +79,53 @@ template bool fill_table<TableL>(TableL &, const void *const *, int32_t,
 // kernel ran 15 % slower.
 // (FC_CARVEOUT in fc_internal.h; -1: no preference.)
 
-// SM count and resident blocks per SM are looked up once per (kernel,
-// device) and cached, so that later calls (for instance while a stream is
-// being captured into a CUDA graph) make no further runtime queries.  The
-// carveout preference is set at the same first lookup.
+namespace {
+
+struct LaunchKey {
+    const void *kernel;
+    int dev, block;
+    size_t smem;
+    bool operator==(const LaunchKey &o) const
+    {
+        return kernel == o.kernel && dev == o.dev && block == o.block && smem == o.smem;
+    }
+};
+
+struct LaunchKeyHash {
+    size_t operator()(const LaunchKey &k) const
+    {
+        return ((size_t)k.kernel >> 4) * 31 + (size_t)k.dev * 7 + (size_t)k.block + k.smem;
+    }
+};
+
+std::atomic<int64_t> g_lookups{0};
+
+}  // namespace
+
+// SM count and resident blocks per SM are looked up once per (kernel, block,
+// shared memory, device) and kept, so that later calls (for instance while a
+// stream is being captured into a CUDA graph) make no further runtime queries.
+// The carveout preference belongs to the kernel and is set at the same first
+// lookup.  A kernel that serves many widths passes the shared memory of its
+// widest, whatever the call needs: one lookup, and one preference, for all.
 int grid_for(const void *kernel, int block, size_t smem, int64_t work, int carveout)
 {
-    struct Entry {
-        const void *kernel;
-        int dev, block, blocks;
-        size_t smem;
-    };
     static std::mutex mu;
-    static Entry cache[256];
-    static int used = 0;
-    int dev = 0;
-    cudaGetDevice(&dev);
+    // never destroyed: calls may come from threads that outlive the statics
+    static auto *const cache =
+        new (std::nothrow) std::unordered_map<LaunchKey, int, LaunchKeyHash>;
+    LaunchKey key{kernel, 0, block, smem};
+    cudaGetDevice(&key.dev);
     int blocks = 0;
-    {
+    if (cache) {
         std::lock_guard<std::mutex> lock(mu);
-        for (int i = 0; i < used; ++i)
-            if (cache[i].kernel == kernel && cache[i].dev == dev &&
-                cache[i].block == block && cache[i].smem == smem) {
-                blocks = cache[i].blocks;
-                break;
-            }
+        const auto it = cache->find(key);
+        if (it != cache->end()) blocks = it->second;
     }
     if (blocks == 0) {
+        g_lookups.fetch_add(1);
         int sms = 0, per_sm = 0;
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, key.dev);
         if (carveout >= 0)
             cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                  carveout);
@@ -115,7 +136,10 @@ int grid_for(const void *kernel, int block, size_t smem, int64_t work, int carve
         if (sms < 1) sms = 1;
         blocks = sms * per_sm;
         std::lock_guard<std::mutex> lock(mu);
-        if (used < 256) cache[used++] = Entry{kernel, dev, block, blocks, smem};
+        try {
+            if (cache) cache->emplace(key, blocks);
+        } catch (const std::bad_alloc &) {  // looked up again next time
+        }
     }
     int64_t g = blocks;
     if (work < g) g = work;
@@ -123,3 +147,5 @@ int grid_for(const void *kernel, int block, size_t smem, int64_t work, int carve
 }
 
 }  // namespace fc
+
+extern "C" int64_t fc_test_launch_lookups(void) { return fc::g_lookups.load(); }

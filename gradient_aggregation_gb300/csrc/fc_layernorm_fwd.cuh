@@ -516,9 +516,10 @@ static cudaError_t go_rows(const LnForward &a, cudaStream_t s)
     }
     const int64_t per = BLOCK / TPR * RW;
     // All of the shared memory only where the parameters need it: at 2048
-    // columns it took 97 us in place of 84.
-    const int grid = grid_for((const void *)kernel, BLOCK, smem, (a.rows + per - 1) / per,
-                              smem > 50 * 1024 ? cudaSharedmemCarveoutMaxShared : FC_CARVEOUT);
+    // columns it took 97 us in place of 84.  The choice is the kernel's, not the
+    // width's, or it would depend on the widths called before.
+    const int grid = grid_for((const void *)kernel, BLOCK, most, (a.rows + per - 1) / per,
+                              most > 50 * 1024 ? cudaSharedmemCarveoutMaxShared : FC_CARVEOUT);
     return launch_after_prior(kernel, (unsigned)grid, BLOCK, smem, s, a);
 }
 
@@ -539,7 +540,7 @@ static cudaError_t go_any(const LnForward &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int64_t ctas = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
     const int grid =
-        grid_for((const void *)kernel, BLOCK, smem, ctas, cudaSharedmemCarveoutMaxShared);
+        grid_for((const void *)kernel, BLOCK, most, ctas, cudaSharedmemCarveoutMaxShared);
     return launch_after_prior(kernel, (unsigned)grid, BLOCK, smem, s, a);
 }
 

@@ -70,6 +70,7 @@ _SIGS = {
     "fc_test_one_launch_kind": (ctypes.c_int, [_I32]),
     "fc_test_barrier_loss": (ctypes.c_int, [_I32, ctypes.c_uint64]),
     "fc_test_adamw_loss": (ctypes.c_int, [_I64, ctypes.c_uint64]),
+    "fc_test_launch_lookups": (_I64, []),
     "fc_step_reduce": (ctypes.c_int, [_P, _I32, _I32, _P, _F32, _I64, _P, _P, _P, _SZ, _P]),
     "fc_step_select": (ctypes.c_int, [_I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "fc_step_update": (ctypes.c_int, [_P, _I64, _I64, _F32, _F32, _P, _P, _P, _P, _P, _P, _P,

@@ -650,6 +650,10 @@ FC_API fc_status fc_test_barrier_loss(int32_t cta, uint64_t wait_limit_ns);
  * consumes it. */
 FC_API fc_status fc_test_adamw_loss(int64_t tile, uint64_t wait_limit_ns);
 
+/* How often a launch has looked up a kernel's resident blocks, in this process: once
+ * a kernel and device, whatever sizes it is called with.  Host only. */
+FC_API int64_t fc_test_launch_lookups(void);
+
 #ifdef __cplusplus
 }
 #endif
