@@ -1132,7 +1132,9 @@ cudaError_t launch_adamw8(const Tab &tab, int gtype, int64_t N, const AdamHyper 
     AdamState st = {};
     st.N = N;
     st.h = h;
-    st.h.eps *= FC_ADAM8_UNIT;
+    // a normal number: the quotient's reciprocal takes a subnormal one for zero, and
+    // an element that never had a gradient would divide 0 by 0
+    st.h.eps = std::max(h.eps * FC_ADAM8_UNIT, 0x1p-126f);
     st.scale = scale;
     st.w = w;
     st.low = low;

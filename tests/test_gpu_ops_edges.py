@@ -115,6 +115,22 @@ def test_adamw8_large_gradients(size, sizes, dtype):
     assert bool((st.rs >= 0).all())
 
 
+def step_and_check_weights(st, g, k, h):
+    """Step k + 1 from the moments that the state holds, 8-bit ones as they are held;
+    the new moments in 64 bits and the bound on m."""
+    m0, v0 = st.moments()
+    w0 = st.w.clone()
+    st.step(fc.LayerGrads([g]), None, h)
+    torch.cuda.synchronize()
+    (w, m, v), (ew, em, ev) = ops_ref.adamw(w0, m0, v0, g, torch.ones_like(w0), k + 1, **h)
+    if st.bits == 8:
+        em = em + U * m0.abs()
+        ew = ew + (h["lr"] / (1 - h["b1"] ** (k + 1))) * U * m0.abs() / (
+            torch.sqrt(v / (1 - h["b2"] ** (k + 1))) + h["eps"]) + 0.1 * ew
+    assert_within("w", st.w, w, ew)
+    return m, em
+
+
 def test_adamw8_goes_on_after_large_gradients():
     """The blocks come back to ordinary gradients by their averages, and the state
     stays that of the definition, step after step."""
@@ -122,17 +138,8 @@ def test_adamw8_goes_on_after_large_gradients():
     st = State(n, 8, None, fresh=True)
     big, small = rnd(n, 1, 1e3), rnd(n, 2)
     big[::3000] *= 1e14
-    h = dict(HYPER, b1=0.5, b2=0.5)
     for k, g in enumerate((big, small, small, small)):
-        m0, v0 = st.moments()
-        w0 = st.w.clone()
-        st.step(fc.LayerGrads([g]), None, h)
-        torch.cuda.synchronize()
-        (w, m, v), (ew, em, ev) = ops_ref.adamw(w0, m0, v0, g, torch.ones_like(w0), k + 1, **h)
-        em, ev = em + U * m0.abs(), ev + 3 * U * v0
-        ew = ew + (h["lr"] / (1 - h["b1"] ** (k + 1))) * U * m0.abs() / (
-            torch.sqrt(v / (1 - h["b2"] ** (k + 1))) + h["eps"]) + 0.1 * ew
-        assert_within("w", st.w, w, ew)
+        m, em = step_and_check_weights(st, g, k, dict(HYPER, b1=0.5, b2=0.5))
         check_codes(st.m8, st.ms, m, em, None)
 
 
@@ -316,3 +323,18 @@ def test_launch_sizes_are_looked_up_once_a_kernel(dtype):
     # kernels of one element type: 13 and 12 forward, 26 backward
     assert first - before <= 60
     assert lookups() == first
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-30, 1e-38, 1e-40, 2e-45])
+def test_adamw_tiny_eps(bits, eps):
+    """Down to the smallest fp32 number: no NaN where a gradient is and always was 0."""
+    for n in (1000, 1 << 20):
+        st = State(n, bits, None, fresh=True)
+        w0 = st.w.clone()
+        g = rnd(n, 3)
+        g[:300] = 0
+        g[::7] = 0
+        for k in range(2):
+            step_and_check_weights(st, g, k, dict(HYPER, eps=eps, wd=0.0))
+        assert torch.equal(st.w[g == 0], w0[g == 0])
