@@ -41,11 +41,18 @@ __global__ void __launch_bounds__(32 * FC_LN_JOIN)
     }
 }
 
-// At most 1024 blocks, and no more than rows.
+// As many sets as blocks leave, and no more than rows.  Several blocks an SM up to
+// 256 columns; one above (a GB300 has 152 to 160 SMs), and two to a row where rows
+// go in halves whatever their type; beyond 16384 columns as many as make 4096 blocks
+// of 128 columns.
 int64_t ln_max_parts(int64_t rows, int64_t cols)
 {
-    (void)cols;
-    return rows < 1024 ? rows : 1024;
+    const int64_t strips = (cols + 127) / 128;
+    const int64_t most = cols <= 256     ? 1024
+                         : cols <= 12288 ? 160
+                         : cols <= 16384 ? 80
+                                         : std::max<int64_t>(1, 4096 / strips);
+    return std::min(rows, most);
 }
 
 cudaError_t ln_join(const LnBackward &a, int parts, cudaStream_t s)

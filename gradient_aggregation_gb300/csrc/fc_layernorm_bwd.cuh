@@ -647,8 +647,7 @@ static cudaError_t wide_rows(const LnBackward &a, cudaStream_t s)
     cudaError_t e = launch_after_prior(wide, (unsigned)grid, FC_LN_WIDE_BLOCK, 0, s, a);
     if (e != cudaSuccess || !a.partials) return e;
     const int64_t strips = (a.cols + 127) / 128;
-    int64_t parts = ln_max_parts(a.rows, a.cols);
-    if (strips * parts > 4096) parts = 4096 / strips < 1 ? 1 : 4096 / strips;
+    const int64_t parts = ln_max_parts(a.rows, a.cols);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)strips, (unsigned)parts);
     cfg.blockDim = dim3(128);

@@ -338,3 +338,29 @@ def test_adamw_tiny_eps(bits, eps):
         for k in range(2):
             step_and_check_weights(st, g, k, dict(HYPER, eps=eps, wd=0.0))
         assert torch.equal(st.w[g == 0], w0[g == 0])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=ids)
+@pytest.mark.parametrize("rows,cols,pad", [
+    (200000, 64, 0), (200000, 61, 0), (100000, 256, 0), (60000, 257, 1), (20000, 1024, 0),
+    (9000, 3000, 0), (4000, 8192, 0), (3000, 12288, 0), (3000, 12289, 0), (2000, 16384, 0),
+    (2000, 16383, 1), (900, 16392, 0), (300, 70000, 0), (5, 600000, 0)])
+def test_backward_keeps_to_its_scratch(rows, cols, pad, dtype):
+    """Many rows of every class, with exactly the bytes asked for and a guard behind."""
+    x, _ = matrix(rows, cols, dtype, pad)
+    dy, _ = matrix(rows, cols, dtype, pad, seed=2)
+    mu, rs = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    need = fc.fc_layernorm_backward_workspace_size(rows, cols)
+    buf = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    fc.fc_layernorm_backward(dy, x, None, mu, rs, torch.empty_like(x), dw, db, buf[:need])
+    torch.cuda.synchronize()
+    assert bool((buf[need:] == 0xA5).all())
+    for got, terms in ((dw, lambda s: dy[s].double() * x[s].double()), (db, lambda s: dy[s].double())):
+        want, size = (torch.zeros(cols, dtype=torch.float64, device="cuda") for _ in range(2))
+        for a in range(0, rows, 8192):
+            t = terms(slice(a, a + 8192))
+            want += t.sum(0)
+            size += t.abs().sum(0)
+        # at worst one thread adds all rows of its block one after another
+        assert_within("sums", got, want, (rows + 24) * U * size)
