@@ -4,9 +4,10 @@ Every ``csrc/*.cu`` file is compiled for sm_103a in parallel with nvcc and
 linked into one shared library with the CUDA runtime linked statically (the
 library then needs only the driver at run time).  No CMake, no setuptools.
 
-Beside them ``csrc/fc_bind.cpp``, the tensor checks of the training-step
-operators' Python binding, becomes a Python module for the torch that is
-installed (``BIND_PATH``).  The library does not need it.
+``csrc/fc_bind.cpp``, the tensor checks of the training-step operators' Python
+binding, becomes a Python module for the torch that is installed
+(``build_binding``).  The library needs neither it nor torch, g++'s Python headers
+or Python: ``build_library`` builds it alone, ``build_all`` both side by side.
 """
 
 from __future__ import annotations
@@ -19,8 +20,6 @@ import subprocess
 import sys
 import sysconfig
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
@@ -29,9 +28,6 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libfc.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 BIND_SRC = os.path.join(CSRC, "fc_bind.cpp")
-# one for each Python and torch: the module is of no use to another
-BIND_PATH = os.path.join(OUT_DIR, "_fcbind.%s.torch-%s.so" % (
-    sys.implementation.cache_tag, torch.__version__.replace("+", "-")))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -65,8 +61,17 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def bind_path() -> str:
+    """Where the Python module is: one for each Python and torch, it is of no use to
+    another."""
+    import torch
+    return os.path.join(OUT_DIR, "_fcbind.%s.torch-%s.so" % (
+        sys.implementation.cache_tag, torch.__version__.replace("+", "-")))
+
+
 def _bind_command(target: str):
     """The compiler call that makes the Python module."""
+    import torch
     cxx = shutil.which("g++") or shutil.which("c++")
     if not cxx:
         raise RuntimeError("a C++ compiler is required to build the Python binding")
@@ -81,29 +86,35 @@ def _bind_command(target: str):
             "-lc10"]
 
 
-def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if needed) the library and the Python module beside it; returns
-    the path of libfc.so."""
+def build_binding(force: bool = False) -> str:
+    """Compile (if needed) the Python module for the installed torch and return its
+    path."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    bind = None
-    if force or _stale(BIND_PATH, [BIND_SRC, os.path.join(INCLUDE, "fc.h"), __file__]):
-        part = BIND_PATH + ".tmp.%d" % os.getpid()
-        bind = subprocess.Popen(_bind_command(part), stdout=subprocess.PIPE,
-                                stderr=subprocess.STDOUT, text=True)
-    try:
-        _build_cuda(force, verbose)
-    finally:
-        if bind is not None:
-            out = bind.communicate()[0]
-    if bind is not None:
-        if bind.returncode != 0:
-            sys.stderr.write(out)
+    path = bind_path()
+    if force or _stale(path, [BIND_SRC, os.path.join(INCLUDE, "fc.h"), __file__]):
+        part = path + ".tmp.%d" % os.getpid()
+        p = subprocess.run(_bind_command(part), stdout=subprocess.PIPE,
+                           stderr=subprocess.STDOUT, text=True)
+        if p.returncode != 0:
+            sys.stderr.write(p.stdout)
             raise RuntimeError("building the Python binding failed")
-        os.replace(part, BIND_PATH)
-    return LIB_PATH
+        os.replace(part, path)
+    return path
 
 
-def _build_cuda(force: bool, verbose: bool) -> str:
+def build_all(force: bool = False, verbose: bool = False) -> str:
+    """The library and the Python module, side by side; returns the path of libfc.so.
+    If the module cannot be built, the library is there all the same."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        bind = ex.submit(build_binding, force)
+        path = build_library(force, verbose)
+        bind.result()
+    return path
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile (if needed) and return the path of libfc.so."""
+    os.makedirs(OUT_DIR, exist_ok=True)
     srcs = _sources()
     hdrs = _headers()
     if not force and not _stale(LIB_PATH, srcs + hdrs + [__file__]):
@@ -143,4 +154,5 @@ def _build_cuda(force: bool, verbose: bool) -> str:
 
 
 if __name__ == "__main__":
-    print(build_library(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    make = build_library if "--library" in sys.argv else build_all
+    print(make(force="--force" in sys.argv, verbose="-v" in sys.argv))

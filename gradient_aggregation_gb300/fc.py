@@ -452,11 +452,9 @@ def _load_bind():
     from . import build
     with _lock:
         if _bind is None:
-            if not os.path.exists(build.BIND_PATH):
-                raise RuntimeError("the Python binding is not built for this torch (%s); run "
-                                   "`python -m gradient_aggregation_gb300.build`"
-                                   % build.BIND_PATH)
-            spec = importlib.util.spec_from_file_location("_fcbind", build.BIND_PATH)
+            # built here if the library was built alone
+            path = build.build_binding()
+            spec = importlib.util.spec_from_file_location("_fcbind", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             module.connect(*[ctypes.cast(getattr(handle, name), _P).value for name in (
