@@ -288,9 +288,13 @@ class ClockSampler:
 
 # ---- GPU arm ---------------------------------------------------------------------------
 
+# The reduction's device code: both kernels, and the device headers that they include.
+PHASE1_SOURCES = ("fc_reduce.cu", "fc_reduce_tma.cu", "fc_common.cuh", "fc_bulk.cuh")
+
+
 def kernel_source_hash():
     h = hashlib.sha256()
-    for name in ("fc_reduce.cu", "fc_reduce_tma.cu", "fc_common.cuh"):
+    for name in PHASE1_SOURCES:
         with open(os.path.join(ROOT, "gradient_aggregation_gb300", "csrc", name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
