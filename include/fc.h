@@ -549,10 +549,22 @@ FC_API fc_status fc_adamw_step(const void *const *grads, int32_t grad_type, int3
  *     y = sqrt(v) * (448 / R), above with the probability (to 16 bits) of how
  *     far y lies towards it; a value above 0 never becomes 0.
  * v moves by 1 - beta2 of itself in a step, far less than half an e4m3 step,
- * so rounding to nearest would leave it where it is.  The random bits are a
+ * so rounding to nearest would leave it where it is.  Two properties of the
+ * 8 bits, for gradients drawn at random in each step:
+ *  - sqrt(v) is rounded without bias, so v itself settles above its average by
+ *    the rounding's variance: by 2.6 % at beta2 = 0.95, 4.8 % at 0.99, 5.6 % at
+ *    0.999, 5.8 % at 0.9999 (steps 1.3 to 2.9 % short).
+ *  - m is rounded to nearest and stands still once (1 - beta1) * |g - m| is below
+ *    half an e4m3 step of m, 3 to 6 % of it.  Where a gradient's spread from step
+ *    to step is at least 0.3 of its mean, m's average in time is as good as fp32's
+ *    for beta1 up to 0.95 (median error 1 to 2 % more).  Where it hardly
+ *    changes, m stays off a new mean by a median of 14 % at beta1 = 0.8,
+ *    26 % at 0.9, 42 % at 0.95; at beta1 = 0.99 by 32 % even with a spread as
+ *    large as the mean.  A larger beta1 than 0.95 wants fp32 moments.
+ * The random bits are a
  * hash of (seed, t, i / 2): the same arguments give the same bits.  The fp32
  * arithmetic is scaled by 2^20, so that squares hold for |g| from 1e-24 on; a
- * block with a v above 1e26 is scaled by 2^-20 instead, where they hold from
+ * block with a v above 3e26 is scaled by 2^-20 instead, where they hold from
  * 1e-12 up to 9.7e24, and a larger finite g counts as 9.7e24.
  *  exp_avg_q, exp_rms_q  device e4m3 [N], 16-byte aligned, updated in place.
  *  exp_avg_scale, exp_rms_scale  device fp32 [ceil(N / FC_STATE_BLOCK)].
