@@ -211,8 +211,9 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
     // three vectors of a 16-bit type do not fit beside their sums: the row is read
     // from its slots again for dx (67M bf16 elements in rows of 1536 / 3000 / 6144 /
     // 12288 columns: 66 / 69 / 70 / 80 us; held in registers and spilled in part 83 /
-    // 94 / 71 / 96)
-    constexpr bool AGAIN = !ANY && K == 3 && sizeof(T) == 2;
+    // 94 / 71 / 96), and where the block has one row it is read vector by vector
+    // for the sums, too (12288 columns 75 us, but 3000 columns 71.5)
+    constexpr bool AGAIN = !ANY && K == 3 && sizeof(T) == 2, BY_VECTOR = AGAIN && TPR == 512;
     extern __shared__ __align__(16) uint4 ring[];  // [D][warps][2][SLOTS]
     static_assert(CL == 1 || (G == 1 && CL * WARPS == 32), "a cluster's sums are one a lane");
     __shared__ float2 part[2][CL == 1 ? G : CL][WARPS];
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
             take_row<T, K, ANY>(held, ANY ? past16(x + row * a.ldx) : 0, cols, base, vx);
             take_row<T, K, ANY>(held + SLOTS, ANY ? past16(dy + row * a.lddy) : 0, cols, base, vy);
         };
-        take();
+        if constexpr (!BY_VECTOR) take();
         if (++d == D) d = 0;
         const F2 rr = f2(rstd, rstd), mm = f2(-mean, -mean);
         auto centred = [&](int p) { return add2(pair_of<T>(vx, p), mm); };
@@ -307,6 +308,11 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (column(k * (VEC / 2)) >= cols) continue;
+            if constexpr (BY_VECTOR) {
+                const uint4 qx = held[lane + 32 * k], qy = held[SLOTS + lane + 32 * k];
+                vx[4 * k] = qx.x; vx[4 * k + 1] = qx.y; vx[4 * k + 2] = qx.z; vx[4 * k + 3] = qx.w;
+                vy[4 * k] = qy.x; vy[4 * k + 1] = qy.y; vy[4 * k + 2] = qy.z; vy[4 * k + 3] = qy.w;
+            }
 #pragma unroll
             for (int p = k * (VEC / 2); p < (k + 1) * (VEC / 2); ++p) {
                 const F2 fy = pair_of<T>(vy, p);
