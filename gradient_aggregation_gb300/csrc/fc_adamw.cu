@@ -25,7 +25,7 @@
 // moments through shared memory with bulk copies in both directions;
 // k_adamw_direct loads and stores them from registers, which starts faster and
 // serves what is resident at once.  Measured (ring): 278 us for 62.4M elements
-// with fp32 moments, fp32 gradients and an fp16 copy (1.87 GB, 6.7 TB/s); 160
+// with fp32 moments, fp32 gradients and an fp16 copy (1.87 GB, 6.7 TB/s); 159
 // us with 8-bit moments and fp16 gradients (1.0 GB, 6.3 TB/s); direct: 3.9 us
 // for 133k elements.
 #include <cuda_fp8.h>
@@ -46,12 +46,14 @@ namespace fc {
 // step with fp32 moments took 320 us, with 16 KB 286, with 19 and 20 KB 278 and 280
 // (fp32 gradients in 600 layers, 20M elements: 96 and 103 us: 20 warps and the copying
 // one have 80 registers each, 19 have 96).  With 8-bit moments the update itself
-// needs the warps: 23 of them have 80 registers, 24 or more have 72.  62M elements of
-// fp16 / bf16 / fp32 160 / 160 / 176 us (24: 173 / 176 / 185, 27: 159 / 159 / 176), 7M
-// in odd layers 24.1 / 24.2 / 29.4 (24: 28.4 / 28.4 / 29.7).
+// needs the warps: 23 of them have 80 registers, 24 to 27 have 72.  62M elements of
+// fp16 / bf16 / fp32 159 / 159 / 176 us with 27 (23: 160 / 160 / 176, 24: 173 / 176 /
+// 185); where gradients are shifted the selecting needs the registers, 7M elements in
+// odd layers 24.1 / 24.2 / 29.6 with 23 (24: 28.4 / 28.4 / 29.7, 27: bf16 27.2).
 #define FC_ADAM_CW32 19
 #define FC_ADAM_S32 3
-#define FC_ADAM_CW8 23
+#define FC_ADAM_CW8 27
+#define FC_ADAM_CW8_SHIFTED 23
 #define FC_ADAM_S8 4
 
 #define FC_ADAM_WAIT_NS 2000000000ull
@@ -424,8 +426,8 @@ __device__ __forceinline__ float finite_at_most(float x, float limit)
 // next step's block maximum with it.  The weights take the fast quotient.
 //
 // The unit is bound by the issue of its instructions where it is not by HBM, so
-// two elements share one wherever they can (7M elements in odd layers 25.2 us,
-// one by one 26.2).
+// two elements share one wherever they can (7M elements in odd layers 25.2 us
+// so, one by one 26.2, with the loads as they then were).
 //
 // Rounding r by chance: y = r * 448 / top lies in [0, 448].  Scaled by 2^-120
 // an e4m3 number is the top of an fp32 number's bits: e4m3's smallest normal
@@ -896,9 +898,10 @@ __global__ void __launch_bounds__((CW + 1) * 32)
                 fill(filled++);
             }
         }
+        // while the last copies out are on their way
+        if (!skip) count_step(st.steps, arrived);
         bulk_wait_all();
         mbar_arrive(smem_u32(&drained));
-        if (!skip) count_step(st.steps, arrived);
         return;
     }
 
@@ -1060,7 +1063,7 @@ static std::atomic<uint64_t> g_drop_limit_ns{0};
 template <class GT, int BITS, bool SHIFTED, class Tab>
 static cudaError_t launch_ring(const Tab &tab, AdamState st, cudaStream_t s)
 {
-    constexpr int CW = BITS == 32 ? FC_ADAM_CW32 : FC_ADAM_CW8;
+    constexpr int CW = BITS == 32 ? FC_ADAM_CW32 : SHIFTED ? FC_ADAM_CW8_SHIFTED : FC_ADAM_CW8;
     constexpr int S = BITS == 32 ? FC_ADAM_S32 : FC_ADAM_S8;
     static_assert(S >= 2 && S <= 32, "a stage is refilled while the next one is worked on");
     using St = RingStage<BITS, CW>;

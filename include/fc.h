@@ -656,7 +656,7 @@ FC_API fc_status fc_test_barrier_loss(int32_t cta, uint64_t wait_limit_ns);
 /* Exercises the failure path of the AdamW steps that stream their state through
  * shared memory (those of more than about 0.9M elements).  Arms the next such
  * launch to copy in nothing for its tile `tile` (clamped to the last; 4864
- * elements, 5888 with 8-bit moments), with its waits bounded by
+ * to 6912 elements, by the kernel's variant), with its waits bounded by
  * wait_limit_ns (1 ms .. 2 s) instead of 2 s: they run out, and steps[1] says so.
  * tile < 0 disarms the hook.  Host only; the next such launch from any thread
  * consumes it. */
