@@ -91,7 +91,9 @@ struct StepScalars {
 #define FC_ADAM8_UNIT 0x1p20f
 #define FC_ADAM8_LARGE 0x1p-20f
 
-// 32-bit mixing by multiplications and xor-shifts (a bijection of 32 bits).
+// 32-bit mixing by multiplications and xor-shifts (a bijection of 32 bits), with a
+// pair of multipliers from Chris Wellons' published search for mixers of this form
+// (2018), chosen for the low bias of each output bit.
 __device__ __forceinline__ unsigned mix32(unsigned x)
 {
     x ^= x >> 16;

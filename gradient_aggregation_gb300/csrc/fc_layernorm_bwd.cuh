@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(BLOCK)
 // q h: no h, and rstd is never squared (it may be 1e19 where eps is 0).
 //
 // Measured at 134M elements of bf16 (805 MB), 768 / 1024 / 2048 / 4096 columns:
-// 127 / 130 / 131 / 134 us, 0.9 of the copy rate; with the rows loaded one ahead
+// 123 / 130 / 131 / 131 us, 0.9 of the copy rate; with the rows loaded one ahead
 // into registers 197 / 161 / 178 / 200 us.
 template <class T, int K, int TPR, int BLOCK, int D, bool ANY, int CL>
 __global__ void __launch_bounds__(BLOCK, BLOCK == 512 ? 1 : K == 1 ? 4 : 2)
@@ -607,8 +607,8 @@ static cudaError_t go_ring(const LnBackward &a, bool pvec, cudaStream_t s)
 
 // Rows wider than one CTA's registers hold with their sums: half a row in each
 // of two CTAs, which exchange the sums of their warps.  Measured at 805 MB: 16384
-// bf16 columns 209 us (one CTA of four vectors a thread, which spills: 234), 12288
-// and 16384 fp32 columns 171 and 152 us (two passes over the row: 360 and 387).  A
+// bf16 columns 214 us (one CTA of four vectors a thread, which spills: 234), 12288
+// and 16384 fp32 columns 170 and 151 us (two passes over the row: 360 and 387).  A
 // quarter of a row in each of four CTAs, two to an SM: 311, 241 and 211 us.
 template <class T, int K, bool ANY>
 static cudaError_t go_halves(const LnBackward &a, bool pvec, cudaStream_t s)
