@@ -22,6 +22,10 @@ decltype(&fc_adamw_step) p_adamw_step;
 decltype(&fc_adamw8_step) p_adamw8_step;
 decltype(&fc_layernorm_forward) p_layernorm_forward;
 decltype(&fc_layernorm_backward) p_layernorm_backward;
+decltype(&fc_groupnorm_forward) p_groupnorm_forward;
+decltype(&fc_groupnorm_backward) p_groupnorm_backward;
+decltype(&fc_router_forward) p_router_forward;
+decltype(&fc_router_backward) p_router_backward;
 
 // Thrown with a Python error set.
 struct Refused {};
@@ -321,15 +325,208 @@ PyObject *layernorm_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
     });
 }
 
-// The addresses of the five C entry points, in the order of the pointers above.
+// One type for two tensors that may be missing: FC_TYPE_F32 without either.
+int shared_type(PyObject *a, PyObject *b, const char *names)
+{
+    int kind = FC_TYPE_F32;
+    if (a != Py_None) kind = type_of(THPVariable_Unpack(a).scalar_type());
+    if (b != Py_None) {
+        const int other = type_of(THPVariable_Unpack(b).scalar_type());
+        if (a != Py_None && other != kind) refuse("%s must have one type", names);
+        kind = other;
+    }
+    return kind;
+}
+
+int truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{};
+    return v;
+}
+
+// Images like x, [samples, positions, channels] with the channels next to one another.
+struct Images {
+    void *p;
+    int64_t ld, ss;
+
+    Images(const at::Tensor &t, const at::Tensor &x, const char *name, int dev)
+    {
+        on_gpu(t, dev, name);
+        if (t.dim() != 3 || t.scalar_type() != x.scalar_type() || t.sizes() != x.sizes())
+            refuse("%s must be of three dimensions, of the shape and type of x", name);
+        if (t.size(2) > 1 && t.stride(2) != 1)
+            refuse("the channels of %s must lie next to one another", name);
+        // the stride of what there is one of says nothing
+        ld = t.size(1) > 1 ? t.stride(1) : t.size(2);
+        ss = t.size(0) > 1 ? t.stride(0) : (t.size(1) - 1) * ld + t.size(2);
+        p = t.data_ptr();
+    }
+};
+
+// The images x: their GPU, shape and type.
+struct Maps {
+    const at::Tensor &x;
+    int dev, type;
+    int64_t samples, positions, channels;
+
+    explicit Maps(PyObject *o) : x(needed(o, "x"))
+    {
+        if (x.dim() != 3) refuse("x must have three dimensions, not %d", (int)x.dim());
+        type = type_of(x, "x");
+        if (!x.is_cuda()) refuse("x must be on a GPU, not on %s", x.device().str().c_str());
+        dev = (int)x.get_device();
+        samples = x.size(0);
+        positions = x.size(1);
+        channels = x.size(2);
+    }
+};
+
+int64_t groups_of(PyObject *o)
+{
+    const int64_t g = integer(o);
+    if (g < 1) refuse("groups must be 1 or more");
+    return g;
+}
+
+// x, groups, weight, bias, eps, act, y, mean, rstd, workspace, stream
+PyObject *groupnorm_forward(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call(args, n, 11, [](PyObject *const *a) {
+        const Maps m(a[0]);
+        const int64_t groups = groups_of(a[1]);
+        const Images x(m.x, m.x, "x", m.dev), y(needed(a[6], "y"), m.x, "y", m.dev);
+        const at::ScalarType own = m.x.scalar_type();
+        const void *w = flat(a[2], m.channels, "weight", m.dev, at::kFloat, own);
+        const void *b = flat(a[3], m.channels, "bias", m.dev, at::kFloat, own);
+        const at::Tensor &ws = needed(a[9], "workspace");
+        void *const p = scratch(ws, m.dev);
+        return p_groupnorm_forward(x.p, m.samples, m.positions, m.channels, x.ld, x.ss, m.type,
+                                   groups, w, b, shared_type(a[2], a[3], "weight and bias"),
+                                   (float)number(a[4]), (int32_t)integer(a[5]), y.p, y.ld, y.ss,
+                                   flat32(a[7], m.samples * groups, "mean", m.dev),
+                                   flat32(a[8], m.samples * groups, "rstd", m.dev), p,
+                                   ws.nbytes(), stream(a[10], m.dev));
+    });
+}
+
+// dy, x, groups, weight, bias, act, mean, rstd, dx, dweight, dbias, workspace, stream
+PyObject *groupnorm_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call(args, n, 13, [](PyObject *const *a) {
+        const Maps m(a[1]);
+        const int64_t groups = groups_of(a[2]);
+        const Images dy(needed(a[0], "dy"), m.x, "dy", m.dev), x(m.x, m.x, "x", m.dev),
+            dx(needed(a[8], "dx"), m.x, "dx", m.dev);
+        const at::ScalarType own = m.x.scalar_type();
+        const void *w = flat(a[3], m.channels, "weight", m.dev, at::kFloat, own);
+        const void *b = flat(a[4], m.channels, "bias", m.dev, at::kFloat, own);
+        void *dw = flat(a[9], m.channels, "dweight", m.dev, at::kFloat, at::kHalf, at::kBFloat16);
+        void *db = flat(a[10], m.channels, "dbias", m.dev, at::kFloat, at::kHalf, at::kBFloat16);
+        const at::Tensor &ws = needed(a[11], "workspace");
+        void *const p = scratch(ws, m.dev);
+        return p_groupnorm_backward(dy.p, dy.ld, dy.ss, x.p, x.ld, x.ss, m.type, m.samples,
+                                    m.positions, m.channels, groups, w, b,
+                                    shared_type(a[3], a[4], "weight and bias"),
+                                    (int32_t)integer(a[5]),
+                                    flat32(a[6], m.samples * groups, "mean", m.dev),
+                                    flat32(a[7], m.samples * groups, "rstd", m.dev), dx.p, dx.ld,
+                                    dx.ss, dw, db, shared_type(a[9], a[10], "dweight and dbias"),
+                                    p, ws.nbytes(), stream(a[12], m.dev));
+    });
+}
+
+// The logits [sequences * tokens, experts] and what one row's choice is.
+struct Scores {
+    const at::Tensor &x;
+    int dev, type;
+    int64_t rows, experts, ld, sequences, tokens, groups, k;
+    void *p;
+
+    Scores(PyObject *logits, PyObject *count, PyObject *per_sequence, PyObject *chosen)
+        : x(needed(logits, "logits"))
+    {
+        if (x.dim() != 2) refuse("logits must have two dimensions, not %d", (int)x.dim());
+        type = type_of(x, "logits");
+        if (!x.is_cuda()) refuse("logits must be on a GPU, not on %s", x.device().str().c_str());
+        dev = (int)x.get_device();
+        rows = x.size(0);
+        experts = x.size(1);
+        p = matrix(x, x, "logits", dev, &ld);
+        sequences = integer(count);
+        if (sequences < 0 || (sequences == 0 && rows != 0) || (sequences && rows % sequences))
+            refuse("%lld rows of logits are not whole sequences, %lld of them", (long long)rows,
+                   (long long)sequences);
+        tokens = sequences ? rows / sequences : 0;
+        groups = truth(per_sequence) ? sequences : 1;
+        const at::Tensor &c = needed(chosen, "chosen");
+        if (c.dim() != 2 || c.size(0) != rows) refuse("chosen must be [rows, k]");
+        k = c.size(1);
+        if (k < 1 || k > experts) refuse("chosen must have 1 to %lld columns", (long long)experts);
+    }
+};
+
+int32_t *flat_int(PyObject *o, int64_t n, const char *name, int dev)
+{
+    return static_cast<int32_t *>(flat(o, n, name, dev, at::kInt));
+}
+
+// logits, sequences, lengths, normalise, per_sequence, chosen, weights, lse, counts,
+// routed, probs, loss, workspace, stream
+PyObject *router_forward(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call(args, n, 14, [](PyObject *const *a) {
+        const Scores s(a[0], a[1], a[4], a[5]);
+        const int32_t *lengths = flat_int(a[2], s.sequences, "lengths", s.dev);
+        int32_t *const chosen = flat_int(a[5], s.rows * s.k, "chosen", s.dev);
+        float *const w = flat32(a[6], s.rows * s.k, "weights", s.dev);
+        const at::Tensor &ws = needed(a[12], "workspace");
+        void *const p = scratch(ws, s.dev);
+        return p_router_forward(s.p, s.sequences, s.tokens, s.experts, s.ld, s.type, lengths,
+                                (int32_t)s.k, truth(a[3]), truth(a[4]), chosen, w,
+                                flat32(a[7], s.rows, "lse", s.dev),
+                                flat_int(a[8], s.groups * s.experts, "counts", s.dev),
+                                flat_int(a[9], s.groups, "routed", s.dev),
+                                flat32(a[10], s.groups * s.experts, "probs", s.dev),
+                                flat32(a[11], 2, "loss", s.dev), p, ws.nbytes(),
+                                stream(a[13], s.dev));
+    });
+}
+
+// logits, sequences, normalise, per_sequence, chosen, weights, lse, counts, routed,
+// dweights, dloss, dlogits, stream
+PyObject *router_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return call(args, n, 13, [](PyObject *const *a) {
+        const Scores s(a[0], a[1], a[3], a[4]);
+        int64_t lddl;
+        void *const dl = matrix(needed(a[11], "dlogits"), s.x, "dlogits", s.dev, &lddl);
+        const int32_t *const chosen = flat_int(a[4], s.rows * s.k, "chosen", s.dev);
+        const float *const w = flat32(a[5], s.rows * s.k, "weights", s.dev);
+        return p_router_backward(s.p, s.sequences, s.tokens, s.experts, s.ld, s.type, (int32_t)s.k,
+                                 truth(a[2]), truth(a[3]), chosen, w,
+                                 flat32(a[6], s.rows, "lse", s.dev),
+                                 flat_int(a[7], s.groups * s.experts, "counts", s.dev),
+                                 flat_int(a[8], s.groups, "routed", s.dev),
+                                 flat32(a[9], s.rows * s.k, "dweights", s.dev),
+                                 flat32(a[10], 2, "dloss", s.dev), dl, lddl,
+                                 stream(a[12], s.dev));
+    });
+}
+
+// The addresses of the nine C entry points, in the order of the pointers above.
 PyObject *connect(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
-    return call(args, n, 5, [](PyObject *const *a) {
+    return call(args, n, 9, [](PyObject *const *a) {
         p_grad_norm = (decltype(p_grad_norm))(intptr_t)integer(a[0]);
         p_adamw_step = (decltype(p_adamw_step))(intptr_t)integer(a[1]);
         p_adamw8_step = (decltype(p_adamw8_step))(intptr_t)integer(a[2]);
         p_layernorm_forward = (decltype(p_layernorm_forward))(intptr_t)integer(a[3]);
         p_layernorm_backward = (decltype(p_layernorm_backward))(intptr_t)integer(a[4]);
+        p_groupnorm_forward = (decltype(p_groupnorm_forward))(intptr_t)integer(a[5]);
+        p_groupnorm_backward = (decltype(p_groupnorm_backward))(intptr_t)integer(a[6]);
+        p_router_forward = (decltype(p_router_forward))(intptr_t)integer(a[7]);
+        p_router_backward = (decltype(p_router_backward))(intptr_t)integer(a[8]);
         return 0;
     });
 }
@@ -338,6 +535,8 @@ PyObject *connect(PyObject *, PyObject *const *args, Py_ssize_t n)
 PyMethodDef methods[] = {METHOD(connect),           METHOD(grad_norm),
                          METHOD(adamw_step),        METHOD(adamw8_step),
                          METHOD(layernorm_forward), METHOD(layernorm_backward),
+                         METHOD(groupnorm_forward), METHOD(groupnorm_backward),
+                         METHOD(router_forward),    METHOD(router_backward),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef definition = {PyModuleDef_HEAD_INIT, "_fcbind", nullptr, -1, methods,

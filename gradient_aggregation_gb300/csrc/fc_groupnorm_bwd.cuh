@@ -1,0 +1,62 @@
+// Group norm, backward, for one element type T.
+#pragma once
+
+#include "fc_groupnorm.cuh"
+#include "fc_layernorm_bwd.cuh"
+
+namespace fc {
+
+// dweight and dbias from `sets` sets of the channels' sums.
+inline cudaError_t gn_join(const GnBackward &a, int64_t sets, cudaStream_t s)
+{
+    if (!a.dweight && !a.dbias) return cudaSuccess;
+    LnBackward l = {};
+    l.cols = a.n.channels;
+    l.dweight = a.dweight;
+    l.dbias = a.dbias;
+    l.gtype = a.gtype;
+    l.partials = a.ws;
+    return ln_join(l, (int)sets, s);
+}
+
+template <class T, int AB, int ACT>
+cudaError_t gn_backward_streaming(const GnBackward &a, cudaStream_t s)
+{
+    const GnTile t = gn_tile(a.n, Gv<T, AB>::NE);
+    const int64_t sets = gn_sets(a.n), used = a.n.samples * t.parts;
+    const unsigned grid = gn_grid(a.n, t);
+    float *const part = a.ws, *const stat = a.ws + 2 * sets * gn_padded(a.n.channels);
+    cudaError_t e = launch_after_prior(k_gn_sums<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, part,
+                                       used);
+    if (e != cudaSuccess) return e;
+    const int64_t groups = a.n.samples * a.n.groups;
+    if ((int64_t)t.parts * (a.n.channels / a.n.groups) <= 1024)
+        e = launch_after_prior(k_gn_finish_sums<T, 32>, (unsigned)((groups + 7) / 8), 256, 0, s, a,
+                               t.parts, part, used, stat);
+    else
+        e = launch_after_prior(k_gn_finish_sums<T, 256>, (unsigned)groups, 256, 0, s, a, t.parts,
+                               part, used, stat);
+    if (e != cudaSuccess) return e;
+    e = launch_after_prior(k_gn_apply_bwd<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);
+    if (e != cudaSuccess) return e;
+    return gn_join(a, used, s);
+}
+
+template <class T, int AB>
+cudaError_t gn_backward_act(const GnBackward &a, int act, cudaStream_t s)
+{
+    if (act == FC_ACT_RELU) return gn_backward_streaming<T, AB, FC_ACT_RELU>(a, s);
+    if (act == FC_ACT_SILU) return gn_backward_streaming<T, AB, FC_ACT_SILU>(a, s);
+    return gn_backward_streaming<T, AB, FC_ACT_NONE>(a, s);
+}
+
+template <class T>
+cudaError_t gn_backward(const GnBackward &a, int act, cudaStream_t s)
+{
+    const int ab = gn_access<T>(a.n, {&a.x, &a.dy, &a.dx});
+    if (ab == 16) return gn_backward_act<T, 16>(a, act, s);
+    if (sizeof(T) == 2 && ab == 2) return gn_backward_act<T, sizeof(T) == 2 ? 2 : 4>(a, act, s);
+    return gn_backward_act<T, 4>(a, act, s);
+}
+
+}  // namespace fc

@@ -1,0 +1,7 @@
+#include "fc_groupnorm_bwd.cuh"
+
+namespace fc {
+
+template cudaError_t gn_backward<__nv_bfloat16>(const GnBackward &, int, cudaStream_t);
+
+}  // namespace fc

@@ -1,0 +1,46 @@
+// Group norm, forward, for one element type T.
+#pragma once
+
+#include "fc_groupnorm.cuh"
+
+namespace fc {
+
+template <class T, int AB, int ACT>
+cudaError_t gn_forward_streaming(const GnForward &a, cudaStream_t s)
+{
+    const GnTile t = gn_tile(a.n, Gv<T, AB>::NE);
+    const int64_t sets = gn_sets(a.n);
+    const unsigned grid = gn_grid(a.n, t);
+    float *const part = a.ws, *const stat = a.ws + 2 * sets * gn_padded(a.n.channels);
+    cudaError_t e = launch_after_prior(k_gn_stats<T, AB>, grid, FC_GN_BLOCK, 0, s, a.x, a.n, t, part,
+                                       sets);
+    if (e != cudaSuccess) return e;
+    const int64_t groups = a.n.samples * a.n.groups;
+    if ((int64_t)t.parts * (a.n.channels / a.n.groups) <= 1024)
+        e = launch_after_prior(k_gn_finish<32>, (unsigned)((groups + 7) / 8), 256, 0, s, a.n, t.parts,
+                               t.rows, part, sets, a.eps, stat, a.mean, a.rstd);
+    else
+        e = launch_after_prior(k_gn_finish<256>, (unsigned)groups, 256, 0, s, a.n, t.parts, t.rows,
+                               part, sets, a.eps, stat, a.mean, a.rstd);
+    if (e != cudaSuccess) return e;
+    return launch_after_prior(k_gn_apply<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);
+}
+
+template <class T, int AB>
+cudaError_t gn_forward_act(const GnForward &a, int act, cudaStream_t s)
+{
+    if (act == FC_ACT_RELU) return gn_forward_streaming<T, AB, FC_ACT_RELU>(a, s);
+    if (act == FC_ACT_SILU) return gn_forward_streaming<T, AB, FC_ACT_SILU>(a, s);
+    return gn_forward_streaming<T, AB, FC_ACT_NONE>(a, s);
+}
+
+template <class T>
+cudaError_t gn_forward(const GnForward &a, int act, cudaStream_t s)
+{
+    const int ab = gn_access<T>(a.n, {&a.x, &a.y});
+    if (ab == 16) return gn_forward_act<T, 16>(a, act, s);
+    if (sizeof(T) == 2 && ab == 2) return gn_forward_act<T, sizeof(T) == 2 ? 2 : 4>(a, act, s);
+    return gn_forward_act<T, 4>(a, act, s);
+}
+
+}  // namespace fc

@@ -1,5 +1,6 @@
-// C entry points of the training-step operators: gradient norm, AdamW and
-// layer norm.  Argument checks and launches; contracts in include/fc.h.
+// C entry points of the training-step operators: gradient norm, AdamW, layer
+// norm, group norm and the router.  Argument checks and launches; contracts in
+// include/fc.h.
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -7,8 +8,10 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "fc.h"
+#include "fc_groupnorm.h"
 #include "fc_layernorm.h"
 #include "fc_opt.h"
+#include "fc_router.h"
 
 using namespace fc;
 
@@ -398,6 +401,224 @@ fc_status fc_layernorm_backward(const void *dy, int64_t lddy, const void *x, int
     const LnBackward a = {dy,   lddy, x,       ldx,   weight,    param_type, mean, rstd, rows, cols,
                           dx,   lddx, dweight, dbias, grad_type, sums ? (float *)workspace : nullptr};
     return launched(launch_ln_backward(a, type, (cudaStream_t)stream), "layernorm launch");
+}
+
+static fc_status check_workspace(const void *workspace, size_t have, size_t need)
+{
+    if (!workspace || have < need)
+        return fail(FC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed",
+                    workspace ? have : (size_t)0, need);
+    return check_ptr(workspace, "workspace", 256, false);
+}
+
+static bool groupnorm_shape(int64_t samples, int64_t positions, int64_t channels, int64_t groups)
+{
+    return samples >= 0 && samples <= (1 << 24) && positions >= 1 &&
+           positions <= ((int64_t)1 << 40) && channels >= 1 && channels <= (1 << 20) &&
+           groups >= 1 && groups <= channels && channels % groups == 0 &&
+           samples * groups <= ((int64_t)1 << 30) &&
+           positions <= ((int64_t)1 << 40) / channels / (samples ? samples : 1);
+}
+
+static fc_status check_groupnorm(int32_t type, int32_t param_type, int32_t act, int64_t samples,
+                                 int64_t positions, int64_t channels, int64_t groups)
+{
+    TRY(check_type(type, "type"));
+    if (param_type != FC_TYPE_F32 && param_type != type)
+        return fail(FC_ERR_INVALID_ARG, "param_type = %d must be FC_TYPE_F32 or the type of x",
+                    param_type);
+    if (act < FC_ACT_NONE || act > FC_ACT_SILU)
+        return fail(FC_ERR_INVALID_ARG, "act = %d is not an FC_ACT_* value", act);
+    if (channels >= 1 && groups >= 1 && channels % groups != 0)
+        return fail(FC_ERR_INVALID_ARG, "channels = %lld must be a multiple of groups = %lld",
+                    (long long)channels, (long long)groups);
+    if (!groupnorm_shape(samples, positions, channels, groups))
+        return fail(FC_ERR_INVALID_ARG,
+                    "%lld samples of %lld positions, %lld channels and %lld groups: out of range",
+                    (long long)samples, (long long)positions, (long long)channels,
+                    (long long)groups);
+    return FC_OK;
+}
+
+// Images whose elements all lie apart: samples one after another, or positions.
+static fc_status check_images(const void *p, const char *name, int32_t type, int64_t samples,
+                              int64_t positions, int64_t channels, int64_t ld, int64_t ss)
+{
+    if (samples == 0) return FC_OK;
+    TRY(check_ptr(p, name, (uintptr_t)type_size(type), false));
+    const int64_t most = (int64_t)1 << 60;
+    if (ld < 0 || ss < 0 || ld > ((int64_t)1 << 40) || ss > ((int64_t)1 << 40) ||
+        ld > most / positions || ss > most / samples)
+        return fail(FC_ERR_INVALID_ARG, "%s: the strides are out of range", name);
+    const bool by_sample = (positions == 1 || ld >= channels) &&
+                           (samples == 1 || ss >= (positions - 1) * ld + channels);
+    const bool by_position = (samples == 1 || ss >= channels) &&
+                             (positions == 1 || ld >= (samples - 1) * ss + channels);
+    if (!by_sample && !by_position)
+        return fail(FC_ERR_INVALID_ARG,
+                    "%s: positions %lld and samples %lld elements apart overlap", name,
+                    (long long)ld, (long long)ss);
+    return FC_OK;
+}
+
+size_t fc_groupnorm_workspace_size(int64_t samples, int64_t positions, int64_t channels,
+                                   int64_t groups)
+{
+    if (!groupnorm_shape(samples, positions, channels, groups)) return 0;
+    const GnShape n = {samples, positions, (int)channels, (int)groups};
+    const size_t floats = 2 * (size_t)(gn_sets(n) * gn_padded(n.channels)) +
+                          2 * (size_t)(samples * groups);
+    return (floats * sizeof(float) + 511) / 256 * 256;
+}
+
+fc_status fc_groupnorm_forward(const void *x, int64_t samples, int64_t positions, int64_t channels,
+                               int64_t ldx, int64_t sx, int32_t type, int64_t groups,
+                               const void *weight, const void *bias, int32_t param_type, float eps,
+                               int32_t act, void *y, int64_t ldy, int64_t sy, float *mean,
+                               float *rstd, void *workspace, size_t workspace_bytes, void *stream)
+{
+    TraceRange trace("fc_groupnorm_forward");
+    TRY(check_groupnorm(type, param_type, act, samples, positions, channels, groups));
+    TRY(check_images(x, "x", type, samples, positions, channels, ldx, sx));
+    TRY(check_images(y, "y", type, samples, positions, channels, ldy, sy));
+    TRY(check_ptr(weight, "weight", (uintptr_t)type_size(param_type), true));
+    TRY(check_ptr(bias, "bias", (uintptr_t)type_size(param_type), true));
+    if (!(eps >= 0.f) || !isfinite(eps))
+        return fail(FC_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!mean != !rstd)
+        return fail(FC_ERR_INVALID_ARG, "mean and rstd must both be given or both be NULL");
+    TRY(check_ptr(mean, "mean", 4, true));
+    TRY(check_ptr(rstd, "rstd", 4, true));
+    TRY(check_workspace(workspace, workspace_bytes,
+                        fc_groupnorm_workspace_size(samples, positions, channels, groups)));
+    if (samples == 0) return ok();
+    DeviceScope scope;
+    TRY(scope.bind(y));
+    const GnForward a = {{x, ldx, sx}, {samples, positions, (int)channels, (int)groups}, weight, bias,
+                         param_type, eps, {y, ldy, sy}, mean, rstd, (float *)workspace};
+    return launched(launch_gn_forward(a, type, act, (cudaStream_t)stream), "groupnorm launch");
+}
+
+fc_status fc_groupnorm_backward(const void *dy, int64_t lddy, int64_t sdy, const void *x,
+                                int64_t ldx, int64_t sx, int32_t type, int64_t samples,
+                                int64_t positions, int64_t channels, int64_t groups,
+                                const void *weight, const void *bias, int32_t param_type,
+                                int32_t act, const float *mean, const float *rstd, void *dx,
+                                int64_t lddx, int64_t sdx, void *dweight, void *dbias,
+                                int32_t grad_type, void *workspace, size_t workspace_bytes,
+                                void *stream)
+{
+    TraceRange trace("fc_groupnorm_backward");
+    TRY(check_groupnorm(type, param_type, act, samples, positions, channels, groups));
+    TRY(check_type(grad_type, "grad_type"));
+    TRY(check_images(dy, "dy", type, samples, positions, channels, lddy, sdy));
+    TRY(check_images(x, "x", type, samples, positions, channels, ldx, sx));
+    TRY(check_images(dx, "dx", type, samples, positions, channels, lddx, sdx));
+    TRY(check_ptr(weight, "weight", (uintptr_t)type_size(param_type), true));
+    TRY(check_ptr(bias, "bias", (uintptr_t)type_size(param_type), true));
+    TRY(check_ptr(mean, "mean", 4, samples == 0));
+    TRY(check_ptr(rstd, "rstd", 4, samples == 0));
+    TRY(check_ptr(dweight, "dweight", (uintptr_t)type_size(grad_type), true));
+    TRY(check_ptr(dbias, "dbias", (uintptr_t)type_size(grad_type), true));
+    TRY(check_workspace(workspace, workspace_bytes,
+                        fc_groupnorm_workspace_size(samples, positions, channels, groups)));
+    if (samples == 0 && !dweight && !dbias) return ok();
+    DeviceScope scope;
+    TRY(scope.bind(samples ? dx : dweight ? dweight : dbias));
+    const GnBackward a = {{dy, lddy, sdy}, {x, ldx, sx},
+                          {samples, positions, (int)channels, (int)groups},
+                          weight, bias, param_type, mean, rstd, {dx, lddx, sdx},
+                          dweight, dbias, grad_type, (float *)workspace};
+    return launched(launch_gn_backward(a, type, act, (cudaStream_t)stream), "groupnorm launch");
+}
+
+static bool router_shape(int64_t sequences, int64_t tokens, int64_t experts)
+{
+    return sequences >= 0 && tokens >= 0 && sequences <= INT32_MAX && tokens <= INT32_MAX &&
+           sequences * tokens <= INT32_MAX && experts >= 1 && experts <= FC_MAX_EXPERTS &&
+           sequences * ((experts + 31) / 32) <= INT32_MAX;
+}
+
+static fc_status check_router(int32_t type, int64_t sequences, int64_t tokens, int64_t experts,
+                              int32_t k)
+{
+    TRY(check_type(type, "type"));
+    if (experts > FC_MAX_EXPERTS)
+        return fail(FC_ERR_LIMIT, "experts = %lld exceeds FC_MAX_EXPERTS = %d", (long long)experts,
+                    FC_MAX_EXPERTS);
+    if (k > FC_MAX_CHOSEN)
+        return fail(FC_ERR_LIMIT, "k = %d exceeds FC_MAX_CHOSEN = %d", k, FC_MAX_CHOSEN);
+    if (!router_shape(sequences, tokens, experts))
+        return fail(FC_ERR_INVALID_ARG, "%lld sequences of %lld tokens over %lld experts: out of range",
+                    (long long)sequences, (long long)tokens, (long long)experts);
+    if (k < 1 || k > experts)
+        return fail(FC_ERR_INVALID_ARG, "k = %d out of [1, experts = %lld]", k, (long long)experts);
+    return FC_OK;
+}
+
+size_t fc_router_workspace_size(int64_t sequences, int64_t tokens, int64_t experts,
+                                int32_t per_sequence)
+{
+    if (!router_shape(sequences, tokens, experts)) return 0;
+    return router_workspace(sequences, tokens, experts, per_sequence ? sequences : 1);
+}
+
+fc_status fc_router_forward(const void *logits, int64_t sequences, int64_t tokens, int64_t experts,
+                            int64_t ld, int32_t type, const int32_t *lengths, int32_t k,
+                            int32_t normalise, int32_t per_sequence, int32_t *chosen, float *weights,
+                            float *lse, int32_t *counts, int32_t *routed, float *probs, float *loss,
+                            void *workspace, size_t workspace_bytes, void *stream)
+{
+    TraceRange trace("fc_router_forward");
+    TRY(check_router(type, sequences, tokens, experts, k));
+    const int64_t rows = sequences * tokens, groups = per_sequence ? sequences : 1;
+    TRY(check_matrix(logits, "logits", type, rows, experts, ld));
+    TRY(check_ptr(lengths, "lengths", 4, true));
+    TRY(check_ptr(chosen, "chosen", 4, rows == 0));
+    TRY(check_ptr(weights, "weights", 4, rows == 0));
+    TRY(check_ptr(lse, "lse", 4, rows == 0));
+    TRY(check_ptr(counts, "counts", 4, groups == 0));
+    TRY(check_ptr(routed, "routed", 4, groups == 0));
+    TRY(check_ptr(probs, "probs", 4, groups == 0));
+    TRY(check_ptr(loss, "loss", 4, false));
+    TRY(check_workspace(workspace, workspace_bytes,
+                        router_workspace(sequences, tokens, experts, groups)));
+    DeviceScope scope;
+    TRY(scope.bind(loss));
+    if (groups == 0)
+        return launched(cudaMemsetAsync(loss, 0, 2 * sizeof(float), (cudaStream_t)stream),
+                        "router launch");
+    const RouterForward a = {logits, ld, {sequences, tokens, (int)experts, k, groups, normalise != 0},
+                             lengths, chosen, weights, lse, counts, routed, probs, loss, workspace};
+    return launched(launch_router_forward(a, type, (cudaStream_t)stream), "router launch");
+}
+
+fc_status fc_router_backward(const void *logits, int64_t sequences, int64_t tokens, int64_t experts,
+                             int64_t ld, int32_t type, int32_t k, int32_t normalise,
+                             int32_t per_sequence, const int32_t *chosen, const float *weights,
+                             const float *lse, const int32_t *counts, const int32_t *routed,
+                             const float *dweights, const float *dloss, void *dlogits, int64_t lddl,
+                             void *stream)
+{
+    TraceRange trace("fc_router_backward");
+    TRY(check_router(type, sequences, tokens, experts, k));
+    const int64_t rows = sequences * tokens, groups = per_sequence ? sequences : 1;
+    TRY(check_matrix(logits, "logits", type, rows, experts, ld));
+    TRY(check_matrix(dlogits, "dlogits", type, rows, experts, lddl));
+    const bool none = rows == 0;
+    TRY(check_ptr(chosen, "chosen", 4, none || !dweights));
+    TRY(check_ptr(weights, "weights", 4, none || !dweights));
+    TRY(check_ptr(lse, "lse", 4, none));
+    TRY(check_ptr(counts, "counts", 4, none || !dloss));
+    TRY(check_ptr(routed, "routed", 4, none || !dloss));
+    TRY(check_ptr(dweights, "dweights", 4, true));
+    TRY(check_ptr(dloss, "dloss", 4, true));
+    if (none) return ok();
+    DeviceScope scope;
+    TRY(scope.bind(dlogits));
+    const RouterBackward a = {logits, ld, {sequences, tokens, (int)experts, k, groups, normalise != 0},
+                              chosen, weights, lse, counts, routed, dweights, dloss, dlogits, lddl};
+    return launched(launch_router_backward(a, type, (cudaStream_t)stream), "router launch");
 }
 
 }  // extern "C"

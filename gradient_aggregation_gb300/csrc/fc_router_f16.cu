@@ -1,0 +1,8 @@
+#include "fc_router.cuh"
+
+namespace fc {
+
+template cudaError_t router_forward<__half>(const RouterForward &, int, cudaStream_t);
+template cudaError_t router_backward<__half>(const RouterBackward &, int, cudaStream_t);
+
+}  // namespace fc

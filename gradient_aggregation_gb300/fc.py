@@ -36,6 +36,9 @@ FC_STEP_THREE_KERNELS, FC_STEP_ONE_LAUNCH, FC_STEP_ONE_CLUSTER = 0, 1, 2
 FC_TYPE_F32, FC_TYPE_F16, FC_TYPE_BF16 = 0, 1, 2
 FC_MAX_OPT_LAYERS = 1536
 FC_STATE_BLOCK = 256
+FC_ACT_NONE, FC_ACT_RELU, FC_ACT_SILU = 0, 1, 2
+FC_MAX_EXPERTS = 1024
+FC_MAX_CHOSEN = 32
 
 _lock = threading.Lock()
 _lib = None
@@ -90,6 +93,18 @@ _SIGS = {
     "fc_layernorm_backward_workspace_size": (_SZ, [_I64, _I64]),
     "fc_layernorm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _P, _I32, _P, _P, _I64,
                                              _I64, _P, _I64, _P, _P, _I32, _P, _SZ, _P]),
+    "fc_groupnorm_workspace_size": (_SZ, [_I64, _I64, _I64, _I64]),
+    "fc_groupnorm_forward": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I64, _I32, _I64, _P, _P,
+                                            _I32, _F32, _I32, _P, _I64, _I64, _P, _P, _P, _SZ,
+                                            _P]),
+    "fc_groupnorm_backward": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _I32, _I64, _I64,
+                                             _I64, _I64, _P, _P, _I32, _I32, _P, _P, _P, _I64,
+                                             _I64, _P, _P, _I32, _P, _SZ, _P]),
+    "fc_router_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
+    "fc_router_forward": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I32, _P, _I32, _I32, _I32,
+                                         _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "fc_router_backward": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P,
+                                          _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
 }
 
 
@@ -459,7 +474,8 @@ def _load_bind():
             spec.loader.exec_module(module)
             module.connect(*[ctypes.cast(getattr(handle, name), _P).value for name in (
                 "fc_grad_norm", "fc_adamw_step", "fc_adamw8_step", "fc_layernorm_forward",
-                "fc_layernorm_backward")])
+                "fc_layernorm_backward", "fc_groupnorm_forward", "fc_groupnorm_backward",
+                "fc_router_forward", "fc_router_backward")])
             _bind = module
     return _bind
 
@@ -573,6 +589,75 @@ def fc_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[to
     over the rows (any of the three types, one for both; None: not wanted)."""
     st = (_bind or _load_bind()).layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias,
                                                     workspace, _raw(stream))
+    if st:
+        _check(st)
+
+
+def fc_groupnorm_workspace_size(samples: int, positions: int, channels: int, groups: int) -> int:
+    return int(lib().fc_groupnorm_workspace_size(int(samples), int(positions), int(channels),
+                                                 int(groups)))
+
+
+def fc_groupnorm_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor],
+                         bias: Optional[torch.Tensor], eps: float, act: int, y: torch.Tensor,
+                         mean: Optional[torch.Tensor], rstd: Optional[torch.Tensor],
+                         workspace: torch.Tensor, stream=None) -> None:
+    """Group norm and an activation (FC_ACT_*) over channels-last images x [samples,
+    positions, channels]; mean and rstd (fp32 [samples, groups]) are what the backward
+    pass needs.  A channels_last tensor t of [N, C, H, W] is
+    t.permute(0, 2, 3, 1).flatten(1, 2), without a copy.  weight and bias have one type:
+    fp32 or that of x."""
+    st = (_bind or _load_bind()).groupnorm_forward(x, groups, weight, bias, eps, act, y, mean,
+                                                   rstd, workspace, _raw(stream))
+    if st:
+        _check(st)
+
+
+def fc_groupnorm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int,
+                          weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], act: int,
+                          mean: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                          dweight: Optional[torch.Tensor], dbias: Optional[torch.Tensor],
+                          workspace: torch.Tensor, stream=None) -> None:
+    """Gradients of fc_groupnorm_forward: dx, and the sums dweight and dbias over samples
+    and positions (any of the three types, one for both; None: not wanted)."""
+    st = (_bind or _load_bind()).groupnorm_backward(dy, x, groups, weight, bias, act, mean, rstd,
+                                                    dx, dweight, dbias, workspace, _raw(stream))
+    if st:
+        _check(st)
+
+
+def fc_router_workspace_size(sequences: int, tokens: int, experts: int,
+                             per_sequence: bool = False) -> int:
+    return int(lib().fc_router_workspace_size(int(sequences), int(tokens), int(experts),
+                                              int(bool(per_sequence))))
+
+
+def fc_router_forward(logits: torch.Tensor, sequences: int, lengths: Optional[torch.Tensor],
+                      normalise: bool, per_sequence: bool, chosen: torch.Tensor,
+                      weights: torch.Tensor, lse: torch.Tensor, counts: torch.Tensor,
+                      routed: torch.Tensor, probs: torch.Tensor, loss: torch.Tensor,
+                      workspace: torch.Tensor, stream=None) -> None:
+    """Chooses k experts for each row of logits [sequences * tokens, experts], k being
+    the width of chosen (int32 [rows, k]), and forms what keeps them balanced: weights
+    [rows, k], lse [rows], counts (int32) and probs [B, experts], routed (int32 [B]) and
+    loss [2], B being sequences with per_sequence and 1 without."""
+    st = (_bind or _load_bind()).router_forward(logits, sequences, lengths, normalise,
+                                                per_sequence, chosen, weights, lse, counts,
+                                                routed, probs, loss, workspace, _raw(stream))
+    if st:
+        _check(st)
+
+
+def fc_router_backward(logits: torch.Tensor, sequences: int, normalise: bool, per_sequence: bool,
+                       chosen: torch.Tensor, weights: torch.Tensor, lse: torch.Tensor,
+                       counts: torch.Tensor, routed: torch.Tensor,
+                       dweights: Optional[torch.Tensor], dloss: Optional[torch.Tensor],
+                       dlogits: torch.Tensor, stream=None) -> None:
+    """Gradients of fc_router_forward by the logits, for dweights [rows, k] by the
+    weights and dloss [2] by the two losses (None: 0)."""
+    st = (_bind or _load_bind()).router_backward(logits, sequences, normalise, per_sequence,
+                                                 chosen, weights, lse, counts, routed, dweights,
+                                                 dloss, dlogits, _raw(stream))
     if st:
         _check(st)
 

@@ -624,6 +624,143 @@ FC_API fc_status fc_layernorm_backward(const void *dy, int64_t lddy, const void 
                                        int32_t grad_type, void *workspace,
                                        size_t workspace_bytes, void *stream);
 
+/* What follows the norm: nothing, max(z, 0), or z / (1 + e^-z). */
+#define FC_ACT_NONE 0
+#define FC_ACT_RELU 1
+#define FC_ACT_SILU 2
+
+/* Bytes of scratch that both passes of group norm need; 0 on bad arguments.
+ * Needs no filling. */
+FC_API size_t fc_groupnorm_workspace_size(int64_t samples, int64_t positions, int64_t channels,
+                                          int64_t groups);
+
+/* Group norm with an activation over images whose channels lie next to one
+ * another, x [samples, positions, channels] (positions: height * width, or any
+ * other extent).  Channels are cut into `groups` groups of channels / groups;
+ * over the M = positions * channels / groups elements of a sample's group:
+ *   mean = sum x / M,  rstd = 1 / sqrt(sum (x - mean)^2 / M + eps)
+ *   z = (x - mean) * rstd * weight[c] + bias[c],  y = act(z)
+ * in fp32 (the variance from differences, not from a difference of squares),
+ * y rounded once.  Sums run in a fixed order: the same inputs on the same GPU
+ * give the same bits.
+ *  x, y        device images of `type`, positions ldx and ldy and samples sx and
+ *              sy elements apart (samples one after another, or positions: no two
+ *              elements may share a place), aligned to their element; y must not
+ *              overlap x.
+ *  weight, bias  device [channels] of param_type (FC_TYPE_F32, or `type`),
+ *              aligned to their element; either may be NULL (1 and 0).
+ *  act         FC_ACT_*.
+ *  mean, rstd  device fp32 [samples, groups] outputs, 4-byte aligned, or both
+ *              NULL.
+ *  workspace   device, fc_groupnorm_workspace_size() bytes, 256-aligned; not
+ *              shared by calls that may overlap on the GPU.
+ * 0 <= samples <= 2^24 (0: nothing is done); positions >= 1; 1 <= channels <=
+ * 2^20, a multiple of groups; samples * groups <= 2^30; at most 2^40 elements;
+ * eps >= 0 finite. */
+FC_API fc_status fc_groupnorm_forward(const void *x, int64_t samples, int64_t positions,
+                                      int64_t channels, int64_t ldx, int64_t sx, int32_t type,
+                                      int64_t groups, const void *weight, const void *bias,
+                                      int32_t param_type, float eps, int32_t act, void *y,
+                                      int64_t ldy, int64_t sy, float *mean, float *rstd,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of fc_groupnorm_forward.  With h = (x - mean) * rstd, z = h * weight +
+ * bias, dz = dy * act'(z) (for FC_ACT_RELU dy where z > 0, else 0) and q = dz *
+ * weight, over each sample's group:
+ *   dx = rstd * (q - sum(q) / M - h * sum(q * h) / M)
+ * and over samples and positions:
+ *   dweight[c] = sum dz * h,  dbias[c] = sum dz
+ * in fp32, each rounded once, the sums in a fixed order.  Which side of 0 a value
+ * lies on (FC_ACT_RELU) is as in exact arithmetic with the given mean and rstd.
+ *  dy, x, dx   device images of `type` as in the forward pass, each with strides of
+ *              its own; dx must not overlap the inputs.
+ *  weight, bias, act  as in the forward pass.
+ *  mean, rstd  device fp32 [samples, groups] from the forward pass.
+ *  dweight, dbias  device [channels] outputs of grad_type (any FC_TYPE_*), aligned
+ *              to their element; either may be NULL (not wanted).
+ *  workspace   as in the forward pass.
+ * samples = 0 writes zeros to dweight and dbias. */
+FC_API fc_status fc_groupnorm_backward(const void *dy, int64_t lddy, int64_t sdy, const void *x,
+                                       int64_t ldx, int64_t sx, int32_t type, int64_t samples,
+                                       int64_t positions, int64_t channels, int64_t groups,
+                                       const void *weight, const void *bias, int32_t param_type,
+                                       int32_t act, const float *mean, const float *rstd, void *dx,
+                                       int64_t lddx, int64_t sdx, void *dweight, void *dbias,
+                                       int32_t grad_type, void *workspace, size_t workspace_bytes,
+                                       void *stream);
+
+/* Most experts, and most chosen for one token, that the router accepts. */
+#define FC_MAX_EXPERTS 1024
+#define FC_MAX_CHOSEN 32
+
+/* Bytes of scratch that fc_router_forward needs; 0 on bad arguments.  Needs no
+ * filling. */
+FC_API size_t fc_router_workspace_size(int64_t sequences, int64_t tokens, int64_t experts,
+                                       int32_t per_sequence);
+
+/* The router of a mixture of experts, with what keeps its experts balanced.  Row
+ * t of logits [sequences * tokens, experts] scores the experts for one token:
+ *   lse[t] = log sum_e exp(x[e]),  p[e] = exp(x[e]) / sum_j exp(x[j])
+ *   chosen[t, 0..k)   the experts of the k largest x, largest first; of equal ones
+ *                     the lowest
+ *   weights[t, j]     p[chosen[t, j]], or with `normalise` that over the sum of
+ *                     the row's k
+ * An expert whose logit is -infinity is closed to the token: it is not chosen,
+ * and where fewer than k are open the rest of chosen is -1 and of weights 0.  A row
+ * behind its sequence's length, or with every expert closed, is not routed: chosen
+ * -1, weights 0, lse -infinity, and it counts nowhere.  (A NaN among the logits is
+ * never chosen; it makes the row's lse and weights NaN, and so the losses.)
+ * Over the groups b of rows that are balanced by themselves (B = sequences of
+ * them with per_sequence, else B = 1: all rows), n the group's routed rows:
+ *   counts[b, e]  rows that chose e,  routed[b] = n,  probs[b, e] = sum_t p[e] / n
+ *   loss[0] = 1/B sum_b sum_e (counts[b, e] * experts / (k n)) * probs[b, e]
+ *   loss[1] = 1/B sum_b sum_t lse[t]^2 / n
+ * (a group with n = 0 adds nothing).  loss[0] is 1 where every expert is as likely
+ * and as often chosen as every other; loss[1] keeps the logits small.  All in fp32,
+ * sums in a fixed order: the same inputs on the same GPU give the same bits.
+ *  logits     device [sequences * tokens, experts] of `type`, rows ld elements
+ *             apart, aligned to their element.
+ *  lengths    device int32 [sequences], routed tokens at the start of each sequence
+ *             (below 0: none, above tokens: all), or NULL: all tokens.
+ *  chosen     device int32 [rows, k];  weights device fp32 [rows, k];
+ *  lse        device fp32 [rows];  counts device int32 [B, experts];
+ *  routed     device int32 [B];  probs device fp32 [B, experts];
+ *  loss       device fp32 [2]: outputs, 4-byte aligned.
+ *  workspace  device, fc_router_workspace_size() bytes, 256-aligned; not shared by
+ *             calls that may overlap on the GPU.
+ * 1 <= k <= experts, k <= FC_MAX_CHOSEN, experts <= FC_MAX_EXPERTS, fewer than 2^31
+ * rows.  Without rows the sums and the losses are 0. */
+FC_API fc_status fc_router_forward(const void *logits, int64_t sequences, int64_t tokens,
+                                   int64_t experts, int64_t ld, int32_t type,
+                                   const int32_t *lengths, int32_t k, int32_t normalise,
+                                   int32_t per_sequence, int32_t *chosen, float *weights,
+                                   float *lse, int32_t *counts, int32_t *routed, float *probs,
+                                   float *loss, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* Gradients of fc_router_forward by the logits, for dweights by the weights and
+ * dloss by the two losses (the counts are constants: a choice has no derivative).
+ * With c[e] = dloss[0] * counts[b, e] * experts / (k n^2 B):
+ *   dlogits[e] = p[e] * (c[e] - sum_j p[j] c[j] + 2 dloss[1] lse / (B n)) + v[e]
+ * where, w and dw being the row's weights and dweights, i = sum_j w[j] dw[j]:
+ *   normalise:  v[chosen[j]] = w[j] * (dw[j] - i), else 0
+ *   otherwise:  v[e] = -p[e] * i, plus w[j] * dw[j] for e = chosen[j]
+ * in fp32, rounded once.  Rows that were not routed get zeros.
+ *  logits, sequences .. per_sequence, chosen .. routed  as in, or from, the forward
+ *             pass (chosen and weights may be NULL without dweights, counts and
+ *             routed without dloss).
+ *  dweights   device fp32 [rows, k], or NULL: 0.
+ *  dloss      device fp32 [2], or NULL: 0.
+ *  dlogits    device [rows, experts] of `type`, rows lddl elements apart; must not
+ *             overlap the inputs. */
+FC_API fc_status fc_router_backward(const void *logits, int64_t sequences, int64_t tokens,
+                                    int64_t experts, int64_t ld, int32_t type, int32_t k,
+                                    int32_t normalise, int32_t per_sequence,
+                                    const int32_t *chosen, const float *weights, const float *lse,
+                                    const int32_t *counts, const int32_t *routed,
+                                    const float *dweights, const float *dloss, void *dlogits,
+                                    int64_t lddl, void *stream);
+
 /* ---- test hook ------------------------------------------------------------------- */
 
 /* Exercises the failure path of the TMA-staged phase 1 (not part of the
