@@ -32,6 +32,36 @@ __device__ __forceinline__ void cluster_sync()
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of cluster_sync, for work of a CTA's own between them.
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+// An arrival that orders no writes: it says that what the CTA wanted to read it has
+// read.
+__device__ __forceinline__ void cluster_arrive_relaxed()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Loads from the address of `local` (a shared variable) in CTA `rank` of the
+// cluster.
+__device__ __forceinline__ float ld_cluster_f32(const float *local, uint32_t rank)
+{
+    const uint32_t a = (uint32_t)__cvta_generic_to_shared(local);
+    uint32_t r;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+    return v;
+}
+
 // Stores v at the address of `local` (a shared variable) in CTA `rank` of
 // the cluster.
 __device__ __forceinline__ void st_cluster_u32(const void *local, uint32_t rank, uint32_t v)

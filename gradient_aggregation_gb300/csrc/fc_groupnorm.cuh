@@ -24,6 +24,10 @@ struct GnRaw<16> {
     using type = uint4;
 };
 template <>
+struct GnRaw<8> {
+    using type = uint2;
+};
+template <>
 struct GnRaw<4> {
     using type = uint32_t;
 };
@@ -50,6 +54,13 @@ struct Gv {
                 else
                     f[p] = pair_of_word<T>(w[p]);
             }
+        } else if constexpr (AB == 8) {
+            if constexpr (sizeof(T) == 4) {
+                f[0] = f2(__uint_as_float(r.x), __uint_as_float(r.y));
+            } else {
+                f[0] = pair_of_word<T>(r.x);
+                f[1] = pair_of_word<T>(r.y);
+            }
         } else if constexpr (sizeof(T) == 4) {
             f[0] = f2(__uint_as_float(r), 0.f);
         } else {
@@ -59,96 +70,68 @@ struct Gv {
 
     static __device__ __forceinline__ Raw put(const F2 (&f)[NP])
     {
-        if constexpr (AB == 16)
+        if constexpr (AB == 16) {
             return from_pairs<T>(f);
-        else if constexpr (sizeof(T) == 4)
+        } else if constexpr (AB == 8) {
+            if constexpr (sizeof(T) == 4) {
+                const float2 a = un2(f[0]);
+                return make_uint2(__float_as_uint(a.x), __float_as_uint(a.y));
+            } else {
+                return make_uint2(word_of_pair<T>(f[0]), word_of_pair<T>(f[1]));
+            }
+        } else if constexpr (sizeof(T) == 4)
             return __float_as_uint(un2(f[0]).x);
         else
             return (Raw)word_of_pair<T>(f[0]);
     }
 };
 
-__device__ __forceinline__ float gn_param(const void *p, int ptype, int type16, int64_t c, float none)
+template <class T>
+__device__ __forceinline__ float gn_param(const void *p, int ptype, int64_t c, float none)
 {
     if (!p) return none;
-    if (ptype == FC_TYPE_F32) return __ldg(static_cast<const float *>(p) + c);
-    if (type16 == FC_TYPE_F16) return __half2float(static_cast<const __half *>(p)[c]);
-    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[c]);
+    if (sizeof(T) == 4 || ptype == FC_TYPE_F32) return __ldg(static_cast<const float *>(p) + c);
+    if constexpr (__is_same(T, __half))
+        return __half2float(static_cast<const __half *>(p)[c]);
+    else if constexpr (sizeof(T) == 2)
+        return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[c]);
+    return none;
 }
 
-template <class T>
-constexpr int gn_type()
-{
-    return sizeof(T) == 4 ? FC_TYPE_F32 : __is_same(T, __half) ? FC_TYPE_F16 : FC_TYPE_BF16;
-}
-
-// Channels c0.. of a parameter as pairs; those past `end` are 0.
+// Channels c0 (a multiple of NE) and the next of a parameter, as pairs.
 template <class T, int NE>
 __device__ __forceinline__ void gn_params(const void *p, int ptype, int64_t c0, float none,
                                           F2 (&f)[(NE + 1) / 2])
 {
+    constexpr int NP = (NE + 1) / 2;
+    if (!p) {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) f[q] = f2(none, NE > 1 ? none : 0.f);
+        return;
+    }
+    const bool whole = ((uintptr_t)p & 15) == 0;
+    if (NE >= 4 && whole && (sizeof(T) == 4 || ptype == FC_TYPE_F32)) {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c0);
+#pragma unroll
+        for (int i = 0; i < NE / 4; ++i) {
+            const float4 v = __ldg(q + i);
+            f[2 * i] = f2(v.x, v.y);
+            f[2 * i + 1] = f2(v.z, v.w);
+        }
+        return;
+    }
+    if constexpr (NE == 8 && sizeof(T) == 2) {
+        if (whole) {
+            Gv<T, 16>::get(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + c0)), f);
+            return;
+        }
+    }
     float v[NE + 1];
     v[NE] = 0.f;
 #pragma unroll
-    for (int e = 0; e < NE; ++e) v[e] = gn_param(p, ptype, gn_type<T>(), c0 + e, none);
+    for (int e = 0; e < NE; ++e) v[e] = gn_param<T>(p, ptype, c0 + e, none);
 #pragma unroll
-    for (int q = 0; q < (NE + 1) / 2; ++q) f[q] = f2(v[2 * q], v[2 * q + 1]);
-}
-
-// x / (1 + e^-x): the exponential and the quotient are within 2 ulp each, and the
-// exponent's own rounding adds |x| ulp.
-__device__ __forceinline__ float gn_silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
-
-template <int ACT>
-__device__ __forceinline__ float gn_act(float z)
-{
-    if (ACT == FC_ACT_RELU) return z < 0.f ? 0.f : z;  // keeps NaN
-    if (ACT == FC_ACT_SILU) return gn_silu(z);
-    return z;
-}
-
-// Which side of 0 a value lies on that fp32 cannot tell: an error of z's size would be
-// one of the gradient's.  Reached by about one value in a million.
-static __device__ __noinline__ bool gn_positive(float x, float mean, float rstd, float w, float b)
-{
-    return ((double)x - (double)mean) * (double)rstd * (double)w + (double)b > 0.0;
-}
-
-// dy * act'(z), z = h w + b, h = (x - mean) rstd.
-template <int ACT>
-__device__ __forceinline__ float gn_dz(float dy, float x, float mean, float rstd, float h, float w,
-                                       float b)
-{
-    if (ACT == FC_ACT_NONE) return dy;
-    const float z = fmaf(h, w, b);
-    if (ACT == FC_ACT_RELU) {
-        bool on = z > 0.f;
-        // z's error is below 5 roundings of b, where h w nearly cancels it; without b
-        // the sign is exact
-        if (fabsf(z) < fabsf(b) * 0x1p-20f) on = gn_positive(x, mean, rstd, w, b);
-        return on ? dy : 0.f;
-    }
-    // s (1 + z (1 - s))
-    const float s = __fdividef(1.f, 1.f + __expf(-z));
-    return dy * (s * fmaf(z, 1.f - s, 1.f));
-}
-
-template <int ACT, int NP>
-__device__ __forceinline__ void gn_dz_pairs(const F2 (&dy)[NP], const F2 (&x)[NP], const F2 (&mean)[NP],
-                                            const F2 (&rstd)[NP], const F2 (&h)[NP],
-                                            const F2 (&w)[NP], const F2 (&b)[NP], F2 (&dz)[NP])
-{
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        if (ACT == FC_ACT_NONE) {
-            dz[p] = dy[p];
-        } else {
-            const float2 y = un2(dy[p]), u = un2(x[p]), m = un2(mean[p]), r = un2(rstd[p]),
-                         g = un2(h[p]), v = un2(w[p]), c = un2(b[p]);
-            dz[p] = f2(gn_dz<ACT>(y.x, u.x, m.x, r.x, g.x, v.x, c.x),
-                       gn_dz<ACT>(y.y, u.y, m.y, r.y, g.y, v.y, c.y));
-        }
-    }
+    for (int q = 0; q < NP; ++q) f[q] = f2(v[2 * q], v[2 * q + 1]);
 }
 
 __device__ __forceinline__ F2 neg2(F2 a)
@@ -156,6 +139,209 @@ __device__ __forceinline__ F2 neg2(F2 a)
     const float2 v = un2(a);
     return f2(-v.x, -v.y);
 }
+
+__device__ __forceinline__ float gn_ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float gn_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + e^-z) of a vector, off by 10 + 1.5 |z| roundings at most (what is below
+// 2^-126 is flushed).  Two special-function instructions a value; a reciprocal shared
+// by two values spares a quarter of them and costs more issue slots than it gives.
+template <int NP>
+__device__ __forceinline__ void gn_sigmoid(const F2 (&z)[NP], F2 (&s)[NP])
+{
+    constexpr float kL = -1.44269504f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const float2 t = un2(mul2(z[p], f2(kL, kL)));
+        const float2 a = un2(add2(f2(gn_ex2(t.x), gn_ex2(t.y)), f2(1.f, 1.f)));
+        s[p] = f2(gn_rcp(a.x), gn_rcp(a.y));
+    }
+}
+
+template <int ACT, int NP>
+__device__ __forceinline__ void gn_act(F2 (&z)[NP])
+{
+    if constexpr (ACT == FC_ACT_RELU) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const float2 v = un2(z[p]);
+            z[p] = f2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);  // keeps NaN
+        }
+    } else if constexpr (ACT == FC_ACT_SILU) {
+        F2 s[NP];
+        gn_sigmoid<NP>(z, s);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) z[p] = mul2(z[p], s[p]);
+    }
+}
+
+// (x - mean) rstd w + b > 0 where fp32 cannot tell (an error of z's size would be one of
+// the gradient's): every step with its rounding error, good to 2^-44 of b.
+__device__ __forceinline__ bool gn_positive(float x, float mean, float rstd, float w, float b)
+{
+    const float d = __fsub_rn(x, mean), t = __fsub_rn(d, x);
+    const float dl = __fadd_rn(__fsub_rn(x, __fsub_rn(d, t)), __fsub_rn(-mean, t));
+    const float k = __fmul_rn(rstd, w), kl = __fmaf_rn(rstd, w, -k);
+    const float p = __fmul_rn(d, k);
+    const float pl = __fadd_rn(__fmaf_rn(d, k, -p), __fmaf_rn(d, kl, __fmul_rn(dl, k)));
+    const float s = __fadd_rn(p, b), u = __fsub_rn(s, p);
+    const float sl = __fadd_rn(__fsub_rn(p, __fsub_rn(s, u)), __fsub_rn(b, u));
+    return __fadd_rn(s, __fadd_rn(sl, pl)) > 0.f;
+}
+
+// Where a vector's values come from, for a second look at them.
+struct GnSource {
+    const void *x;              // the vector
+    const float *mean, *rstd;   // of its first group, those of the next `stride` further
+    int stride, off, cpg;       // off: of its first channel in the group
+    const void *weight, *bias;
+    int ptype, c;               // c: its first channel
+};
+
+// A bit for each element of a vector: z > 0 as in exact arithmetic.  Out of line: about
+// one vector in 100,000 is looked at again.
+template <class T, int NE>
+static __device__ __noinline__ uint32_t gn_positive_bits(const GnSource s)
+{
+    uint32_t bits = 0;
+#pragma unroll 1
+    for (int e = 0; e < NE; ++e) {
+        const int g = (s.off + e) / s.cpg * s.stride;
+        float x;
+        if constexpr (sizeof(T) == 4)
+            x = static_cast<const float *>(s.x)[e];
+        else if constexpr (__is_same(T, __half))
+            x = __half2float(static_cast<const __half *>(s.x)[e]);
+        else
+            x = __bfloat162float(static_cast<const __nv_bfloat16 *>(s.x)[e]);
+        bits |= (uint32_t)gn_positive(x, s.mean[g], s.rstd[g],
+                                      gn_param<T>(s.weight, s.ptype, s.c + e, 1.f),
+                                      gn_param<T>(s.bias, s.ptype, s.c + e, 0.f)) << e;
+    }
+    return bits;
+}
+
+// dy * act'(z), z = d rw + b with d = x - mean and rw = rstd w; source() says where the
+// vector came from.
+template <class T, int ACT, int NE, class Source>
+__device__ __forceinline__ void gn_dz(const F2 (&dy)[(NE + 1) / 2], const F2 (&d)[(NE + 1) / 2],
+                                      const F2 (&rw)[(NE + 1) / 2], const F2 (&b)[(NE + 1) / 2],
+                                      F2 (&dz)[(NE + 1) / 2], Source source)
+{
+    constexpr int NP = (NE + 1) / 2;
+    if constexpr (ACT == FC_ACT_NONE) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) dz[p] = dy[p];
+    } else if constexpr (ACT == FC_ACT_RELU) {
+        // z's error is below 5 roundings of b where d rw nearly cancels it; without b the
+        // sign is exact
+        float near = INFINITY;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const float2 z = un2(fma2(d[p], rw[p], b[p])), c = un2(b[p]);
+            near = fminf(near, fminf(fmaf(fabsf(c.x), -0x1p-20f, fabsf(z.x)),
+                                     fmaf(fabsf(c.y), -0x1p-20f, fabsf(z.y))));
+            bits |= (z.x > 0.f ? 1u << 2 * p : 0u) | (z.y > 0.f ? 2u << 2 * p : 0u);
+        }
+        if (near < 0.f) bits = gn_positive_bits<T, NE>(source());
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const float2 y = un2(dy[p]);
+            dz[p] = f2(bits & 1u << 2 * p ? y.x : 0.f, bits & 2u << 2 * p ? y.y : 0.f);
+        }
+    } else {
+        F2 z[NP], s[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) z[p] = fma2(d[p], rw[p], b[p]);
+        gn_sigmoid<NP>(z, s);
+        // s (1 + z (1 - s))
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            dz[p] = mul2(mul2(dy[p], s[p]),
+                         fma2(z[p], fma2(s[p], f2(-1.f, -1.f), f2(1.f, 1.f)), f2(1.f, 1.f)));
+    }
+}
+
+// ---- a vector's groups --------------------------------------------------------------------
+//
+// ONE: every vector lies in one group.
+
+// Calls f(j, first, last) for every group j that the vector touches, of which it has the
+// elements [first, last); `off`: its first element's place in its group.
+template <int NE, bool ONE, class F>
+__device__ __forceinline__ void gn_pieces(int off, int cpg, F f)
+{
+    if constexpr (ONE) {
+        f(0, 0, NE);
+    } else {
+        int first = 0, last = min(NE, cpg - off);
+        for (int j = 0; first < NE; ++j) {
+            f(j, first, last);
+            first = last;
+            last = min(NE, last + cpg);
+        }
+    }
+}
+
+template <int NE>
+__device__ __forceinline__ float gn_element(const F2 (&f)[(NE + 1) / 2], int e)
+{
+    const float2 a = un2(f[e / 2]);
+    return e & 1 ? a.y : a.x;
+}
+
+// Adds up elements [first, last) of a vector of values.
+template <int NE, bool ONE>
+__device__ __forceinline__ float gn_add(const F2 (&f)[(NE + 1) / 2], int first, int last)
+{
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+        if (ONE || (e >= first && e < last)) x += gn_element<NE>(f, e);
+    return x;
+}
+
+// A group's value for each pair of the vector (ONE: the same for all).
+template <int NE, bool ONE>
+struct GnOf {
+    static constexpr int NP = (NE + 1) / 2;
+    F2 f[ONE ? 1 : NP];
+
+    __device__ __forceinline__ F2 operator[](int p) const { return f[ONE ? 0 : p]; }
+    template <class L>
+    __device__ __forceinline__ void load(int g0, int off, int cpg, L value)
+    {
+        if constexpr (ONE) {
+            const float v = value(g0);
+            f[0] = f2(v, v);
+        } else {
+            float v[2 * NP] = {};
+            int left = cpg - off, g = g0;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                v[e] = value(g);
+                if (--left == 0 && e < NE - 1) {
+                    ++g;
+                    left = cpg;
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < NP; ++p) f[p] = f2(v[2 * p], v[2 * p + 1]);
+        }
+    }
+};
 
 // ---- streaming: any alignment, groups of any size -----------------------------------------
 //
@@ -384,48 +570,33 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
         F2 f[NP];
         V::get(__ldcs(reinterpret_cast<const typename V::Raw *>(x + row * a.x.ld)), f);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            f[p] = fma2(add2(f[p], m[p]), w[p], b[p]);
-            if (ACT != FC_ACT_NONE) {
-                const float2 z = un2(f[p]);
-                f[p] = f2(gn_act<ACT>(z.x), gn_act<ACT>(z.y));
-            }
-        }
+        for (int p = 0; p < NP; ++p) f[p] = fma2(add2(f[p], m[p]), w[p], b[p]);
+        gn_act<ACT, NP>(f);
         __stcs(reinterpret_cast<typename V::Raw *>(y + row * a.y.ld), V::put(f));
     }
 }
 
-// What a thread of the backward pass holds of its channels.
-template <class T, int NE>
+// What a thread of the backward pass holds of its vector's channels.  With d = x - mean,
+// z = d (rstd w) + bias; sums of dz h are sums of dz d times rstd.
+template <class T, int NE, bool ONE>
 struct GnChannels {
     static constexpr int NP = (NE + 1) / 2;
-    F2 neg[NP], mean[NP], rstd[NP], w[NP], b[NP];
+    F2 b[NP], rw[NP];  // bias, rstd * weight
+    GnOf<NE, ONE> mean, rstd;
 
-    __device__ __forceinline__ void params(const GnBackward &a, int64_t c)
-    {
-        gn_params<T, NE>(a.weight, a.ptype, c, 1.f, w);
-        gn_params<T, NE>(a.bias, a.ptype, c, 0.f, b);
-    }
-    // mean and rstd of the groups that channels c.. of sample n belong to
-    __device__ __forceinline__ void stats(const GnBackward &a, int64_t n, int c, int cpg)
-    {
-        const float *m = a.mean + n * a.n.groups, *r = a.rstd + n * a.n.groups;
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int g0 = (c + 2 * p) / cpg, g1 = NE > 1 ? (c + 2 * p + 1) / cpg : g0;
-            mean[p] = f2(__ldg(m + g0), __ldg(m + g1));
-            rstd[p] = f2(__ldg(r + g0), __ldg(r + g1));
-            neg[p] = neg2(mean[p]);
-        }
-    }
-    // h and dz of a vector
-    template <int ACT>
-    __device__ __forceinline__ void at(const F2 (&x)[NP], const F2 (&dy)[NP], F2 (&h)[NP],
-                                       F2 (&dz)[NP]) const
+    __device__ __forceinline__ void scale(const F2 (&w)[NP])
     {
 #pragma unroll
-        for (int p = 0; p < NP; ++p) h[p] = mul2(add2(x[p], neg[p]), rstd[p]);
-        gn_dz_pairs<ACT, NP>(dy, x, mean, rstd, h, w, b, dz);
+        for (int p = 0; p < NP; ++p) rw[p] = mul2(rstd[p], w[p]);
+    }
+    // d and dz of a vector
+    template <int ACT, class Source>
+    __device__ __forceinline__ void at(const F2 (&x)[NP], const F2 (&dy)[NP], F2 (&d)[NP],
+                                       F2 (&dz)[NP], Source source) const
+    {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) d[p] = add2(x[p], neg2(mean[p]));
+        gn_dz<T, ACT, NE>(dy, d, rw, b, dz, source);
     }
 };
 
@@ -444,9 +615,15 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
 #pragma unroll
     for (int p = 0; p < NP; ++p) sh[p] = s[p] = f2(0.f, 0.f);
     if (q.on) {
-        GnChannels<T, NE> ch;
-        ch.params(a, q.c0);
-        ch.stats(a, q.n, q.c0, a.n.channels / a.n.groups);
+        GnChannels<T, NE, false> ch;
+        const int cpg = a.n.channels / a.n.groups, g0 = q.c0 / cpg;
+        const int64_t at = q.n * a.n.groups;
+        F2 w[NP];
+        gn_params<T, NE>(a.weight, a.ptype, q.c0, 1.f, w);
+        gn_params<T, NE>(a.bias, a.ptype, q.c0, 0.f, ch.b);
+        ch.mean.load(g0, q.c0 - g0 * cpg, cpg, [&](int g) { return __ldg(a.mean + at + g); });
+        ch.rstd.load(g0, q.c0 - g0 * cpg, cpg, [&](int g) { return __ldg(a.rstd + at + g); });
+        ch.scale(w);
         const T *x = static_cast<const T *>(a.x.p) + q.n * a.x.ss + q.c0;
         const T *dy = static_cast<const T *>(a.dy.p) + q.n * a.dy.ss + q.c0;
 #pragma unroll 2
@@ -454,13 +631,18 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
             F2 f[NP], g[NP], h[NP], dz[NP];
             V::get(*reinterpret_cast<const typename V::Raw *>(x + row * a.x.ld), f);
             V::get(*reinterpret_cast<const typename V::Raw *>(dy + row * a.dy.ld), g);
-            ch.template at<ACT>(f, g, h, dz);
+            ch.template at<ACT>(f, g, h, dz, [&] {
+                return GnSource{x + row * a.x.ld, a.mean + at + g0, a.rstd + at + g0, 1,
+                                q.c0 - g0 * cpg, cpg, a.weight, a.bias, a.ptype, q.c0};
+            });
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 sh[p] = fma2(dz[p], h[p], sh[p]);
                 s[p] = add2(s[p], dz[p]);
             }
         }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) sh[p] = mul2(sh[p], ch.rstd[p]);
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const float2 u = un2(sh[e / 2]), v = un2(s[e / 2]);
@@ -504,7 +686,7 @@ __global__ void __launch_bounds__(256)
     for (int64_t i = lane; i < entries; i += TPG) {
         const int64_t p = i / cpg;
         const int c = c0 + (int)(i - p * cpg);
-        const float w = gn_param(a.weight, a.ptype, gn_type<T>(), c, 1.f);
+        const float w = gn_param<T>(a.weight, a.ptype, c, 1.f);
         const int64_t j = (sample * parts + p) * padded + c;
         s2 = fmaf(w, __ldcg(in + j), s2);
         s1 = fmaf(w, __ldcg(in + sets * padded + j), s1);
@@ -517,16 +699,26 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// dx of a vector: rstd (dz w - c1 - h c2).
-template <int NP>
-__device__ __forceinline__ void gn_dx(const F2 (&dz)[NP], const F2 (&h)[NP], const F2 (&w)[NP],
-                                      const F2 (&rstd)[NP], const F2 (&n1)[NP], const F2 (&n2)[NP],
-                                      F2 (&dx)[NP])
-{
+// dx = rstd w dz - rstd c1 - rstd^2 c2 d, c1 and c2 the means of q and of q h.
+template <int NE, bool ONE>
+struct GnSlope {
+    GnOf<NE, ONE> k1, k2;  // -rstd c1, -rstd^2 c2
+    static constexpr int NP = (NE + 1) / 2;
+
+    __device__ __forceinline__ void scale(const GnOf<NE, ONE> &rstd)
+    {
 #pragma unroll
-    for (int p = 0; p < NP; ++p)
-        dx[p] = mul2(fma2(h[p], n2[p], fma2(dz[p], w[p], n1[p])), rstd[p]);
-}
+        for (int p = 0; p < (ONE ? 1 : NP); ++p) {
+            k1.f[p] = mul2(k1.f[p], rstd.f[p]);
+            k2.f[p] = mul2(k2.f[p], mul2(rstd.f[p], rstd.f[p]));
+        }
+    }
+    __device__ __forceinline__ void dx(const F2 (&d)[NP], const F2 (&rw)[NP], F2 (&dz)[NP]) const
+    {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) dz[p] = fma2(dz[p], rw[p], fma2(d[p], k2[p], k1[p]));
+    }
+};
 
 template <class T, int AB, int ACT>
 __global__ void __launch_bounds__(FC_GN_BLOCK)
@@ -538,18 +730,20 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
     allow_dependent_launch();
     const GnPlace q = gn_place<NE>(tile, a.n.positions);
     if (!q.on) return;
-    const int cpg = a.n.channels / a.n.groups;
-    GnChannels<T, NE> ch;
-    ch.params(a, q.c0);
-    ch.stats(a, q.n, q.c0, cpg);
-    F2 n1[NP], n2[NP];
-    const float *st = stat + 2 * q.n * a.n.groups;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        const int g0 = (q.c0 + 2 * p) / cpg, g1 = NE > 1 ? (q.c0 + 2 * p + 1) / cpg : g0;
-        n1[p] = f2(-__ldcg(st + 2 * g0), -__ldcg(st + 2 * g1));
-        n2[p] = f2(-__ldcg(st + 2 * g0 + 1), -__ldcg(st + 2 * g1 + 1));
-    }
+    const int cpg = a.n.channels / a.n.groups, g0 = q.c0 / cpg, off = q.c0 - g0 * cpg;
+    const int64_t at = q.n * a.n.groups;
+    const float *st = stat + 2 * at;
+    GnChannels<T, NE, false> ch;
+    F2 w[NP];
+    gn_params<T, NE>(a.weight, a.ptype, q.c0, 1.f, w);
+    gn_params<T, NE>(a.bias, a.ptype, q.c0, 0.f, ch.b);
+    ch.mean.load(g0, off, cpg, [&](int g) { return __ldg(a.mean + at + g); });
+    ch.rstd.load(g0, off, cpg, [&](int g) { return __ldg(a.rstd + at + g); });
+    ch.scale(w);
+    GnSlope<NE, false> to;
+    to.k1.load(g0, off, cpg, [&](int g) { return -__ldcg(st + 2 * g); });
+    to.k2.load(g0, off, cpg, [&](int g) { return -__ldcg(st + 2 * g + 1); });
+    to.scale(ch.rstd);
     const T *x = static_cast<const T *>(a.x.p) + q.n * a.x.ss + q.c0;
     const T *dy = static_cast<const T *>(a.dy.p) + q.n * a.dy.ss + q.c0;
     T *dx = static_cast<T *>(const_cast<void *>(a.dx.p)) + q.n * a.dx.ss + q.c0;
@@ -558,10 +752,12 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
         F2 f[NP], g[NP], h[NP], dz[NP];
         V::get(__ldcs(reinterpret_cast<const typename V::Raw *>(x + row * a.x.ld)), f);
         V::get(__ldcs(reinterpret_cast<const typename V::Raw *>(dy + row * a.dy.ld)), g);
-        ch.template at<ACT>(f, g, h, dz);
-        F2 o[NP];
-        gn_dx<NP>(dz, h, ch.w, ch.rstd, n1, n2, o);
-        __stcs(reinterpret_cast<typename V::Raw *>(dx + row * a.dx.ld), V::put(o));
+        ch.template at<ACT>(f, g, h, dz, [&] {
+            return GnSource{x + row * a.x.ld, a.mean + at + g0, a.rstd + at + g0, 1, off, cpg,
+                            a.weight, a.bias, a.ptype, q.c0};
+        });
+        to.dx(h, ch.rw, dz);
+        __stcs(reinterpret_cast<typename V::Raw *>(dx + row * a.dx.ld), V::put(dz));
     }
 }
 

@@ -41,10 +41,11 @@ struct GnBackward {
     float *ws;
 };
 
-// The workspace: sets of two values a channel (what blocks leave), then two
-// values a group and sample.
+// The workspace: sets of two values a channel (what blocks leave), then two values a
+// group and sample.
 int64_t gn_parts(const GnShape &n);  // parts of a sample's positions, streaming
 int64_t gn_sets(const GnShape &n);
+bool gn_may_stream(const GnShape &n);  // else the workspace has no room for it
 inline int64_t gn_padded(int channels) { return ((int64_t)channels + 7) & ~(int64_t)7; }
 
 cudaError_t launch_gn_forward(const GnForward &a, int type, int act, cudaStream_t s);

@@ -1,12 +1,12 @@
 // Group norm, backward, for one element type T.
 #pragma once
 
-#include "fc_groupnorm.cuh"
+#include "fc_groupnorm_res.cuh"
 #include "fc_layernorm_bwd.cuh"
 
 namespace fc {
 
-// dweight and dbias from `sets` sets of the channels' sums.
+// dweight and dbias from `sets` sets of the channels' sums, as layer norm joins its own.
 inline cudaError_t gn_join(const GnBackward &a, int64_t sets, cudaStream_t s)
 {
     if (!a.dweight && !a.dbias) return cudaSuccess;
@@ -42,12 +42,39 @@ cudaError_t gn_backward_streaming(const GnBackward &a, cudaStream_t s)
     return gn_join(a, used, s);
 }
 
+template <class T, int AB, int ACT, bool ONE>
+cudaError_t gn_backward_one(const GnBackward &a, cudaStream_t s)
+{
+    GnPlan p;
+    if (!gn_plan(a.n, AB, Gv<T, AB>::NE, 2, (const void *)k_gn_bwd<T, AB, ACT, ONE>, &p)) {
+        if (!gn_may_stream(a.n)) return cudaErrorInvalidConfiguration;
+        return gn_backward_streaming<T, AB, ACT>(a, s);
+    }
+    const cudaError_t e = gn_launch(k_gn_bwd<T, AB, ACT, ONE>, a, p, s);
+    return e == cudaSuccess ? gn_join(a, p.per, s) : e;
+}
+
+// A thread holds five values a channel, and two or four more of each group that its
+// vector touches: vectors that cross groups are halved.
+template <class T, int AB, int ACT>
+cudaError_t gn_backward_groups(const GnBackward &a, cudaStream_t s)
+{
+    constexpr int NE = Gv<T, AB>::NE;
+    const int cpg = a.n.channels / a.n.groups;
+    if (cpg % NE == 0) return gn_backward_one<T, AB, ACT, true>(a, s);
+    if constexpr (AB == 16) {
+        if (cpg % (NE / 2) == 0) return gn_backward_one<T, AB / 2, ACT, true>(a, s);
+        return gn_backward_one<T, AB / 2, ACT, false>(a, s);
+    }
+    return gn_backward_one<T, AB, ACT, NE == 1>(a, s);  // a vector of one lies in one group
+}
+
 template <class T, int AB>
 cudaError_t gn_backward_act(const GnBackward &a, int act, cudaStream_t s)
 {
-    if (act == FC_ACT_RELU) return gn_backward_streaming<T, AB, FC_ACT_RELU>(a, s);
-    if (act == FC_ACT_SILU) return gn_backward_streaming<T, AB, FC_ACT_SILU>(a, s);
-    return gn_backward_streaming<T, AB, FC_ACT_NONE>(a, s);
+    if (act == FC_ACT_RELU) return gn_backward_groups<T, AB, FC_ACT_RELU>(a, s);
+    if (act == FC_ACT_SILU) return gn_backward_groups<T, AB, FC_ACT_SILU>(a, s);
+    return gn_backward_groups<T, AB, FC_ACT_NONE>(a, s);
 }
 
 template <class T>

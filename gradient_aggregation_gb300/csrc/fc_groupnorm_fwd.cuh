@@ -1,7 +1,7 @@
 // Group norm, forward, for one element type T.
 #pragma once
 
-#include "fc_groupnorm.cuh"
+#include "fc_groupnorm_res.cuh"
 
 namespace fc {
 
@@ -26,12 +26,30 @@ cudaError_t gn_forward_streaming(const GnForward &a, cudaStream_t s)
     return launch_after_prior(k_gn_apply<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);
 }
 
+template <class T, int AB, int ACT, bool ONE>
+cudaError_t gn_forward_one(const GnForward &a, cudaStream_t s)
+{
+    GnPlan p;
+    if (gn_plan(a.n, AB, Gv<T, AB>::NE, 1, (const void *)k_gn_fwd<T, AB, ACT, ONE>, &p))
+        return gn_launch(k_gn_fwd<T, AB, ACT, ONE>, a, p, s);
+    if (!gn_may_stream(a.n)) return cudaErrorInvalidConfiguration;
+    return gn_forward_streaming<T, AB, ACT>(a, s);
+}
+
+template <class T, int AB, int ACT>
+cudaError_t gn_forward_groups(const GnForward &a, cudaStream_t s)
+{
+    constexpr int NE = Gv<T, AB>::NE;
+    if (a.n.channels / a.n.groups % NE == 0) return gn_forward_one<T, AB, ACT, true>(a, s);
+    return gn_forward_one<T, AB, ACT, NE == 1>(a, s);  // a vector of one lies in one group
+}
+
 template <class T, int AB>
 cudaError_t gn_forward_act(const GnForward &a, int act, cudaStream_t s)
 {
-    if (act == FC_ACT_RELU) return gn_forward_streaming<T, AB, FC_ACT_RELU>(a, s);
-    if (act == FC_ACT_SILU) return gn_forward_streaming<T, AB, FC_ACT_SILU>(a, s);
-    return gn_forward_streaming<T, AB, FC_ACT_NONE>(a, s);
+    if (act == FC_ACT_RELU) return gn_forward_groups<T, AB, FC_ACT_RELU>(a, s);
+    if (act == FC_ACT_SILU) return gn_forward_groups<T, AB, FC_ACT_SILU>(a, s);
+    return gn_forward_groups<T, AB, FC_ACT_NONE>(a, s);
 }
 
 template <class T>
