@@ -2,17 +2,26 @@
 // choice of the element type.  The kernels over the rows are in fc_router.cuh; each
 // element type is compiled in a file of its own, so that they build side by side.
 #include <algorithm>
+#include <mutex>
+#include <new>
+#include <set>
+#include <utility>
 
 #include "fc_router.cuh"
 
 namespace fc {
 
-extern template cudaError_t router_forward<float>(const RouterForward &, int, cudaStream_t);
-extern template cudaError_t router_forward<__half>(const RouterForward &, int, cudaStream_t);
-extern template cudaError_t router_forward<__nv_bfloat16>(const RouterForward &, int, cudaStream_t);
-extern template cudaError_t router_backward<float>(const RouterBackward &, int, cudaStream_t);
-extern template cudaError_t router_backward<__half>(const RouterBackward &, int, cudaStream_t);
-extern template cudaError_t router_backward<__nv_bfloat16>(const RouterBackward &, int, cudaStream_t);
+extern template cudaError_t router_forward<float>(const RouterForward &, const RouterCut &, cudaStream_t);
+extern template cudaError_t router_forward<__half>(const RouterForward &, const RouterCut &,
+                                                  cudaStream_t);
+extern template cudaError_t router_forward<__nv_bfloat16>(const RouterForward &, const RouterCut &,
+                                                  cudaStream_t);
+extern template cudaError_t router_backward<float>(const RouterBackward &, const RouterCut &,
+                                                  cudaStream_t);
+extern template cudaError_t router_backward<__half>(const RouterBackward &, const RouterCut &,
+                                                  cudaStream_t);
+extern template cudaError_t router_backward<__nv_bfloat16>(const RouterBackward &, const RouterCut &,
+                                                  cudaStream_t);
 
 // Adds the parts of 32 experts of one group, 32 threads to an expert, and leaves
 // their share of the balance loss; the last block adds the shares, in their order.
@@ -108,13 +117,29 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// Enough blocks to fill the GPU, of a row a warp at least.
+cudaError_t router_allow(const void *kernel)
+{
+    static std::mutex mu;
+    // never destroyed: calls may come from threads that outlive the statics
+    static auto *const done = new (std::nothrow) std::set<std::pair<const void *, int>>;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lock(mu);
+    if (done && done->count({kernel, dev})) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e != cudaSuccess) return e;
+    try {
+        if (done) done->insert({kernel, dev});
+    } catch (const std::bad_alloc &) {  // set again next time
+    }
+    return cudaSuccess;
+}
+
 int64_t router_parts(int64_t sequences, int64_t tokens, int64_t groups)
 {
     if (sequences * tokens == 0) return 1;
-    const int64_t per = sequences * tokens / groups;
-    const int64_t most = std::max<int64_t>(1, 1216 / groups);
-    return std::min(most, (per + FC_ROUTER_WARPS - 1) / FC_ROUTER_WARPS);
+    return std::min<int64_t>(sequences * tokens / groups, std::max<int64_t>(1, 1216 / groups));
 }
 
 size_t router_workspace(int64_t sequences, int64_t tokens, int64_t experts, int64_t groups)
@@ -124,27 +149,46 @@ size_t router_workspace(int64_t sequences, int64_t tokens, int64_t experts, int6
     return (size_t)((words * 4 + 255) / 256 * 256);
 }
 
+// Rows of a warp at a time: 32, so that every lane has one where lanes take rows, but
+// fewer where that would leave warps of the GPU without any; at least as many as lie
+// side by side.
+static RouterCut router_cut(const RouterShape &n)
+{
+    const int64_t rows = n.sequences * n.tokens, per = rows / n.groups;
+    int beside = 32;
+    while (beside > 1 && 256 / beside < n.experts) beside /= 2;
+    RouterCut c = {};
+    c.rows = 32;
+    while (c.rows > beside && rows / c.rows < 2432) c.rows /= 2;
+    c.warps = FC_ROUTER_WARPS;
+    while (c.warps > 1 && per <= (int64_t)c.rows * (c.warps / 2)) c.warps /= 2;
+    const int64_t most = router_parts(n.sequences, n.tokens, n.groups);
+    c.parts = (int)std::max<int64_t>(1, std::min(most, (per + c.rows * c.warps - 1) / (c.rows * c.warps)));
+    c.joins = n.groups * c.parts <= FC_ROUTER_JOIN;
+    return c;
+}
+
 cudaError_t launch_router_forward(const RouterForward &a, int type, cudaStream_t s)
 {
-    const int parts = (int)router_parts(a.n.sequences, a.n.tokens, a.n.groups);
+    const RouterCut cut = router_cut(a.n);
     cudaError_t e;
     if (type == FC_TYPE_F32)
-        e = router_forward<float>(a, parts, s);
+        e = router_forward<float>(a, cut, s);
     else if (type == FC_TYPE_F16)
-        e = router_forward<__half>(a, parts, s);
+        e = router_forward<__half>(a, cut, s);
     else
-        e = router_forward<__nv_bfloat16>(a, parts, s);
-    if (e != cudaSuccess) return e;
+        e = router_forward<__nv_bfloat16>(a, cut, s);
+    if (e != cudaSuccess || cut.joins) return e;
     const unsigned tiles = (unsigned)((a.n.experts + 31) / 32);
-    return launch_after_prior(k_router_join, (unsigned)(a.n.groups * tiles), 1024, 0, s, a, parts);
+    return launch_after_prior(k_router_join, (unsigned)(a.n.groups * tiles), 1024, 0, s, a, cut.parts);
 }
 
 cudaError_t launch_router_backward(const RouterBackward &a, int type, cudaStream_t s)
 {
-    const int parts = (int)router_parts(a.n.sequences, a.n.tokens, a.n.groups);
-    if (type == FC_TYPE_F32) return router_backward<float>(a, parts, s);
-    if (type == FC_TYPE_F16) return router_backward<__half>(a, parts, s);
-    return router_backward<__nv_bfloat16>(a, parts, s);
+    const RouterCut cut = router_cut(a.n);
+    if (type == FC_TYPE_F32) return router_backward<float>(a, cut, s);
+    if (type == FC_TYPE_F16) return router_backward<__half>(a, cut, s);
+    return router_backward<__nv_bfloat16>(a, cut, s);
 }
 
 }  // namespace fc

@@ -1,8 +1,17 @@
 // The router of a mixture of experts, for one element type T: softmax over the
 // experts, the k largest, and what the balance loss needs; and its gradient.
 //
-// A warp holds a row, lane l the experts l, l + 32, ...: a lane's experts stay the
-// same from row to row, so the sums of the probabilities stay in its registers.
+// Experts are cut into groups of eight, a vector load or two.  LPR lanes of a warp
+// share a row, each with one group (VPL groups where there are more than 256 experts),
+// 32 / LPR rows side by side, so that a lane's experts stay the same from row to row
+// and the sums of their probabilities stay in its registers.
+//
+// Choosing the k largest with the lanes of a row side by side would cost a reduction
+// over the warp for each of them.  Instead the lanes leave the largest of every group in
+// shared memory, and then each lane chooses for a row of its own: the largest of the
+// groups' largest, that group's elements once more (from L1 or L2), the largest that is
+// left of them; 32 rows at a time.  At 256 experts and k = 8 that is 30 instructions of
+// a warp a row, beside 60 for the softmax; a choice by warp reductions took 500.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -11,36 +20,174 @@
 #include "fc.h"
 #include "fc_cluster.cuh"
 #include "fc_internal.h"
+#include "fc_pairs.cuh"
 #include "fc_router.h"
 
 namespace fc {
 
-#define FC_ROUTER_BLOCK 256
+#define FC_ROUTER_WARPS 8   // of a block at most
+#define FC_ROUTER_JOIN 8    // blocks of a cluster that join what they leave themselves
 #define FC_ROUTER_FAR 16.f
-#define FC_ROUTER_WARPS (FC_ROUTER_BLOCK / 32)
 
-__device__ __forceinline__ float rt_f32(float x) { return x; }
-__device__ __forceinline__ float rt_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ float rt_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+constexpr float kRtLog2e = 1.44269504f;
 
-template <class T>
-__device__ __forceinline__ T rt_round(float x)
+__device__ __forceinline__ float rt_ex2(float x)
 {
-    if constexpr (sizeof(T) == 4)
-        return x;
-    else if constexpr (__is_same(T, __half))
-        return __float2half_rn(x);
-    else
-        return __float2bfloat16_rn(x);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// Ordered like the number it stands for: -0 like 0, NaN below everything, and
-// above 0 for whatever is more than -infinity.
-__device__ __forceinline__ uint32_t rt_key(float x)
+// Eight elements of a row, loaded ahead of their use.  ALIGNED: E is whole 16-byte
+// vectors and so is every row's start; what lies past E, or is not there, is -infinity.
+template <class T, bool ALIGNED>
+struct Rt8 {
+    static constexpr bool kWord = ALIGNED && sizeof(T) == 2;
+    uint4 q;
+    F2 f[kWord ? 1 : 4];
+
+    __device__ __forceinline__ void load(const T *row, int e0, int E, bool here)
+    {
+        if constexpr (kWord) {
+            const uint32_t none = __is_same(T, __half) ? 0xfc00fc00u : 0xff80ff80u;
+            q = make_uint4(none, none, none, none);
+            if (here && e0 < E) q = *reinterpret_cast<const uint4 *>(row + e0);
+        } else if constexpr (ALIGNED) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                if (here && e0 + 4 * h < E) v = *reinterpret_cast<const float4 *>(row + e0 + 4 * h);
+                f[2 * h] = f2(v.x, v.y);
+                f[2 * h + 1] = f2(v.z, v.w);
+            }
+        } else {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = -INFINITY;
+                if (here && e0 + i < E) {
+                    if constexpr (sizeof(T) == 4)
+                        v[i] = row[e0 + i];
+                    else if constexpr (__is_same(T, __half))
+                        v[i] = __half2float(row[e0 + i]);
+                    else
+                        v[i] = __bfloat162float(row[e0 + i]);
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) f[p] = f2(v[2 * p], v[2 * p + 1]);
+        }
+    }
+    __device__ __forceinline__ void get(F2 (&x)[4]) const
+    {
+        if constexpr (kWord) {
+            x[0] = pair_of_word<T>(q.x);
+            x[1] = pair_of_word<T>(q.y);
+            x[2] = pair_of_word<T>(q.z);
+            x[3] = pair_of_word<T>(q.w);
+        } else {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) x[p] = f[p];
+        }
+    }
+};
+
+template <class T, bool ALIGNED>
+__device__ __forceinline__ void rt_store(T *row, int e0, int E, const F2 (&f)[4])
 {
-    const uint32_t u = __float_as_uint(x + 0.f);
-    const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-    return x > -INFINITY ? key : 0u;
+    if constexpr (ALIGNED && sizeof(T) == 2) {
+        if (e0 < E) __stcs(reinterpret_cast<uint4 *>(row + e0), from_pairs<T>(f));
+    } else if constexpr (ALIGNED) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 a = un2(f[2 * h]), b = un2(f[2 * h + 1]);
+            if (e0 + 4 * h < E)
+                __stcs(reinterpret_cast<float4 *>(row + e0 + 4 * h), make_float4(a.x, a.y, b.x, b.y));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 a = un2(f[i / 2]);
+            const float v = i & 1 ? a.y : a.x;
+            if (e0 + i < E) {
+                if constexpr (sizeof(T) == 4)
+                    row[e0 + i] = v;
+                else if constexpr (__is_same(T, __half))
+                    row[e0 + i] = __float2half_rn(v);
+                else
+                    row[e0 + i] = __float2bfloat16_rn(v);
+            }
+        }
+    }
+}
+
+// What a group leaves of its largest element: a word that is ordered by the element,
+// then from the lowest group up, and that also says which of the eight are chosen
+// already.  0: none is left that is more than -infinity (NaN counts as less).
+template <class T>
+struct RtWord {
+    using type = uint32_t;
+    // 16-bit values are the upper halves of words of fp32 (bf16), or as many of their bits
+    static __device__ __forceinline__ uint32_t make(float x, int group, uint32_t taken)
+    {
+        if (!(x > -INFINITY)) return 0;
+        uint32_t h;
+        if constexpr (__is_same(T, __half))
+            h = __half_as_ushort(__float2half_rn(x + 0.f));
+        else
+            h = __float_as_uint(x + 0.f) >> 16;
+        h ^= h & 0x8000u ? 0xffffu : 0x8000u;
+        return h << 16 | (uint32_t)(127 - group) << 8 | taken;
+    }
+    static __device__ __forceinline__ float value(uint32_t w)
+    {
+        uint32_t h = w >> 16;
+        h ^= h & 0x8000u ? 0x8000u : 0xffffu;
+        if constexpr (__is_same(T, __half))
+            return __half2float(__ushort_as_half((unsigned short)h));
+        else
+            return __uint_as_float(h << 16);
+    }
+    static __device__ __forceinline__ int group(uint32_t w) { return 127 - (int)(w >> 8 & 127); }
+    static __device__ __forceinline__ uint32_t taken(uint32_t w) { return w & 255; }
+};
+
+template <>
+struct RtWord<float> {
+    using type = unsigned long long;
+    static __device__ __forceinline__ type make(float x, int group, uint32_t taken)
+    {
+        if (!(x > -INFINITY)) return 0;
+        const uint32_t u = __float_as_uint(x + 0.f);
+        const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+        return (type)key << 32 | (uint32_t)(127 - group) << 8 | taken;
+    }
+    static __device__ __forceinline__ float value(type w)
+    {
+        const uint32_t key = (uint32_t)(w >> 32);
+        return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+    }
+    static __device__ __forceinline__ int group(type w) { return 127 - (int)((uint32_t)w >> 8 & 127); }
+    static __device__ __forceinline__ uint32_t taken(type w) { return (uint32_t)w & 255; }
+};
+
+// Words of a row in shared memory: whole 16-byte vectors, an odd number of them, so that
+// 32 lanes with a row each read theirs without a conflict.
+template <class T>
+__host__ __device__ constexpr int rt_stride(int groups)
+{
+    constexpr int per = 16 / (int)sizeof(typename RtWord<T>::type);
+    const int vecs = (groups + per - 1) / per;
+    return (vecs | 1) * per;
+}
+
+// A warp's shared memory: the words of `rows` rows, two numbers a row, and the chosen
+// experts and their weights.
+template <class T>
+__host__ __device__ constexpr int rt_warp_bytes(int groups, int rows, int k)
+{
+    return (rt_stride<T>(groups) * (int)sizeof(typename RtWord<T>::type) * rows + 8 * rows +
+            8 * rows * k + 15) / 16 * 16;
 }
 
 // What the blocks leave, and where.
@@ -65,265 +212,624 @@ __host__ __device__ inline RouterWs router_ws(void *ws, int64_t groups, int64_t 
     return w;
 }
 
-template <class T, int EPL>
-__global__ void __launch_bounds__(FC_ROUTER_BLOCK)
-    k_router_fwd(const RouterForward a, const int parts)
+struct RouterCut {
+    int parts;  // blocks a group
+    int rows;   // rows of a warp at a time
+    int warps;  // of a block
+    bool joins; // the grid is one cluster, which joins what it leaves
+};
+
+// Sum over the LPR lanes of a row.
+template <int LPR>
+__device__ __forceinline__ float rt_row_sum(float x)
 {
-    __shared__ int s_counts[32 * EPL];
-    __shared__ float s_probs[FC_ROUTER_WARPS][32 * EPL];
-    __shared__ float s_z[FC_ROUTER_WARPS];
-    __shared__ int s_n[FC_ROUTER_WARPS];
-    wait_for_prior_grid();
-    allow_dependent_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int E = a.n.experts, k = a.n.k;
-    const int64_t group = blockIdx.x / parts;
-    const int part = (int)(blockIdx.x - group * parts);
-    const int64_t per = a.n.sequences * a.n.tokens / a.n.groups;  // rows of a group
-    const RouterWs ws = router_ws(a.ws, a.n.groups, parts, E);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *ws.done = 0;
-    for (int e = threadIdx.x; e < 32 * EPL; e += FC_ROUTER_BLOCK) s_counts[e] = 0;
-    __syncthreads();
-    float sum[EPL], zsum = 0.f;
-    int routed = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sum[i] = 0.f;
-    for (int64_t at = (int64_t)part * FC_ROUTER_WARPS + warp; at < per;
-         at += (int64_t)parts * FC_ROUTER_WARPS) {
-        const int64_t row = group * per + at;
-        bool live = true;
-        if (a.lengths) {
-            const int64_t seq = row / a.n.tokens;
-            live = row - seq * a.n.tokens < __ldg(a.lengths + seq);
-        }
-        float x[EPL], top = -INFINITY;
-        bool any = false;
-        if (live) {
-            const T *p = static_cast<const T *>(a.logits) + row * a.ld;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = lane + 32 * i;
-                x[i] = e < E ? rt_f32(__ldcs(p + e)) : -INFINITY;
-                top = fmaxf(top, x[i]);
-                any |= !(x[i] == -INFINITY);
-            }
-            live = __any_sync(0xffffffffu, any);
-        }
-        if (!live) {  // behind the end, or no expert is open to it
-            if (lane < k) {
-                a.chosen[row * k + lane] = -1;
-                a.weights[row * k + lane] = 0.f;
-            }
-            if (lane == 0) a.lse[row] = -INFINITY;
-            continue;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float total = 0.f, p[EPL];
-        uint32_t key[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            p[i] = expf(x[i] - top);
-            total += p[i];
-            key[i] = rt_key(x[i]);
-        }
-        total = warp_sum_f32(total);
-        const float inv = 1.f / total, lse = top + logf(total);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) sum[i] = fmaf(p[i], inv, sum[i]);
-        zsum = fmaf(lse, lse, zsum);
-        ++routed;
-        // the k largest, one after another; of equal ones the lowest
-        int mine = -1;
-        float value = -INFINITY;
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = 0;
-            int at_i = 0;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at_i = i;
-                }
-            const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-            if (most == 0) break;
-            const int e = (int)__reduce_min_sync(0xffffffffu,
-                                                 best == most ? (unsigned)(lane + 32 * at_i) : ~0u);
-            const bool owner = best == most && lane + 32 * at_i == e;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (owner && i == at_i) key[i] = 0;
-            if (lane == j) {
-                mine = e;
-                const uint32_t u = most & 0x80000000u ? most ^ 0x80000000u : ~most;
-                value = __uint_as_float(u);
-            }
-        }
-        float w = mine >= 0 ? expf(value - top) : 0.f;
-        // a row with a NaN has a total of NaN, and so weights of NaN
-        const float chosen = a.n.normalise ? fmaf(0.f, total, warp_sum_f32(w)) : total;
-        if (lane < k) {
-            a.chosen[row * k + lane] = mine;
-            a.weights[row * k + lane] = mine >= 0 ? w / chosen : 0.f;
-            if (mine >= 0) atomicAdd(&s_counts[mine], 1);
-        }
-        if (lane == 0) a.lse[row] = lse;
+    for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+template <int LPR>
+__device__ __forceinline__ float rt_row_max(float x)
+{
+    if constexpr (LPR == 32) {
+        float y;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+        return y;
     }
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s_probs[warp][lane + 32 * i] = sum[i];
+    for (int o = LPR / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// Adds the parts of expert e of a group of rows, and returns its share of the balance
+// loss but for E / k.
+__device__ __forceinline__ float rt_join_experts(const RouterForward &a, const RouterWs &ws,
+                                                 int64_t group, int parts, int n, int e)
+{
+    const int E = a.n.experts;
+    const float each = 1.f / (float)max(n, 1);
+    float p = 0.f;
+    int c = 0;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        p += __ldcg(ws.probs + (group * parts + i) * E + e);
+        c += __ldcg(ws.counts + (group * parts + i) * E + e);
+    }
+    p *= each;
+    a.probs[group * E + e] = p;
+    a.counts[group * E + e] = c;
+    return (float)c * p * each;
+}
+
+template <class T, int LPR, int VPL, bool ALIGNED>
+__global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
+    k_router_fwd(const __grid_constant__ RouterForward a, const __grid_constant__ RouterCut cut)
+{
+    using Word = typename RtWord<T>::type;
+    constexpr int RPI = 32 / LPR;  // rows side by side
+    constexpr int U = LPR < 8 ? 1 : LPR < 16 ? 2 : VPL == 1 ? 4 : VPL == 2 ? 2 : 1;
+    extern __shared__ uint4 dyn[];
+    __shared__ float s_z[FC_ROUTER_WARPS];
+    __shared__ int s_n[FC_ROUTER_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = cut.warps;
+    const int E = a.n.experts, k = a.n.k, G = (E + 7) / 8;
+    const int stride = rt_stride<T>(G);
+    // the block's counts and, at the end, its sums; then each warp's own
+    int *const s_counts = reinterpret_cast<int *>(dyn);
+    char *const own = reinterpret_cast<char *>(s_counts + (E + 3) / 4 * 4) +
+                      (size_t)warp * rt_warp_bytes<T>(G, cut.rows, k);
+    Word *const words = reinterpret_cast<Word *>(own);
+    float2 *const stats = reinterpret_cast<float2 *>(words + stride * cut.rows);
+    int *const chosen = reinterpret_cast<int *>(stats + cut.rows);
+    float *const weights = reinterpret_cast<float *>(chosen + cut.rows * k);
+    const int64_t group = blockIdx.x / (unsigned)cut.parts;
+    const int part = (int)(blockIdx.x - group * cut.parts);
+    const int64_t per = a.n.sequences * a.n.tokens / a.n.groups;  // rows of a group
+    const RouterWs ws = router_ws(a.ws, a.n.groups, cut.parts, E);
+    for (int e = threadIdx.x; e < E; e += 32 * warps) s_counts[e] = 0;
+    const int q = lane % LPR, sub = lane / LPR;  // of the row, of the rows side by side
+    F2 sum[VPL][4];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) sum[v][p] = f2(0.f, 0.f);
+    float zsum = 0.f;
+    int routed = 0;
+    wait_for_prior_grid();
+    allow_dependent_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ws.done = 0;
+    __syncthreads();
+    const T *const logits = static_cast<const T *>(a.logits);
+    const int64_t tile0 = ((int64_t)part * warps + warp) * cut.rows;
+    for (int64_t at = tile0; at < per; at += (int64_t)cut.parts * warps * cut.rows) {
+        const int64_t row0 = group * per + at;
+        const int rows = (int)(per - at < cut.rows ? per - at : cut.rows);
+        // which of the tile's rows are there
+        bool there = lane < rows;
+        if (there && a.lengths) {
+            const int64_t row = row0 + lane, seq = row / a.n.tokens;
+            there = row - seq * a.n.tokens < __ldg(a.lengths + seq);
+        }
+        const unsigned present = __ballot_sync(0xffffffffu, there);
+        // the softmax, U rows of a lane at a time
+        for (int r0 = 0; r0 < rows; r0 += RPI * U) {
+            Rt8<T, ALIGNED> raw[U][VPL];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) {
+                    const int r = r0 + u * RPI + sub;
+                    raw[u][v].load(logits + (row0 + r) * a.ld, 8 * (q + LPR * v), E,
+                                   r < rows && present >> r & 1);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * RPI + sub;
+                const bool live = r < rows && present >> r & 1;
+                F2 x[VPL][4];
+                float top = -INFINITY;
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) {
+                    const int g = q + LPR * v;
+                    raw[u][v].get(x[v]);
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float2 e = un2(x[v][p]);
+                        most = fmaxf(most, fmaxf(e.x, e.y));
+                    }
+                    top = fmaxf(top, most);
+                    if (r < rows && g < G) words[r * stride + g] = RtWord<T>::make(most, g, 0);
+                }
+                top = rt_row_max<LPR>(top);
+                F2 acc = f2(0.f, 0.f);
+                bool nan = false;
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        // x - top first: products of large numbers would not cancel
+                        const F2 d = add2(x[v][p], f2(-top, -top));
+                        const float2 e = un2(mul2(d, f2(kRtLog2e, kRtLog2e)));
+                        const F2 y = f2(rt_ex2(e.x), rt_ex2(e.y));
+                        acc = add2(acc, y);
+                        x[v][p] = y;
+                    }
+                const float2 both = un2(acc);
+                const float total = rt_row_sum<LPR>(both.x + both.y);
+                // closed to all experts, or nothing but NaN
+                const bool closed = !(top > -INFINITY);
+                bool routes = live;
+                if (__any_sync(0xffffffffu, live && closed)) {
+                    if (live && closed) {
+#pragma unroll
+                        for (int v = 0; v < VPL; ++v) {
+                            raw[u][v].get(x[v]);
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                const float2 e = un2(x[v][p]);
+                                nan |= e.x != e.x || e.y != e.y;
+                            }
+                        }
+                    }
+                    // of the row's own lanes
+                    const unsigned votes = __ballot_sync(0xffffffffu, nan);
+                    const unsigned mine = (LPR == 32 ? ~0u : (1u << (LPR & 31)) - 1u) << (sub * LPR);
+                    routes = live && (!closed || (votes & mine));
+                }
+                const float inv = routes ? 1.f / total : 0.f;
+                if (routes) {
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v)
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            sum[v][p] = fma2(x[v][p], f2(inv, inv), sum[v][p]);
+                }
+                if (q == 0 && r < rows) stats[r] = make_float2(top, routes ? total : -1.f);
+            }
+        }
+        __syncwarp();
+        // the choice, a lane a row
+        if (lane < rows) {
+            const float2 st = stats[lane];
+            const T *const row = logits + (row0 + lane) * a.ld;
+            Word *const mine = words + lane * stride;
+            const bool routes = !(st.y < 0.f);
+            const float scale = 1.f / st.y;
+            float chosen_sum = 0.f;
+            int j = 0;
+            if (routes) {
+                for (; j < k; ++j) {
+                    Word most = 0;
+                    if constexpr (sizeof(Word) == 4) {
+                        const uint4 *w4 = reinterpret_cast<const uint4 *>(mine);
+                        int g = 0;
+                        for (; g + 4 <= G; g += 4) {
+                            const uint4 w = w4[g / 4];
+                            most = max(max(max(most, w.x), max(w.y, w.z)), w.w);
+                        }
+                        for (; g < G; ++g) most = max(most, mine[g]);
+                    } else {
+                        for (int g = 0; g < G; ++g) most = max(most, mine[g]);
+                    }
+                    if (most == 0) break;
+                    const int g = RtWord<T>::group(most);
+                    const uint32_t taken = RtWord<T>::taken(most);
+                    const float value = RtWord<T>::value(most);
+                    Rt8<T, ALIGNED> raw;
+                    F2 f[4];
+                    raw.load(row, 8 * g, E, true);
+                    raw.get(f);
+                    int at_e = 0;
+                    float left = -INFINITY;
+                    float x[8];
+#pragma unroll
+                    for (int i = 7; i >= 0; --i) {
+                        const float2 e = un2(f[i / 2]);
+                        x[i] = taken >> i & 1 ? -INFINITY : i & 1 ? e.y : e.x;
+                        if (x[i] == value) at_e = i;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) left = fmaxf(left, i == at_e ? -INFINITY : x[i]);
+                    mine[g] = RtWord<T>::make(left, g, taken | 1u << at_e);
+                    const float p = rt_ex2((value - st.x) * kRtLog2e);
+                    chosen_sum += p;
+                    chosen[lane * k + j] = 8 * g + at_e;
+                    weights[lane * k + j] = p;
+                    atomicAdd(&s_counts[8 * g + at_e], 1);
+                }
+                const float lse = st.x + logf(st.y);
+                zsum = fmaf(lse, lse, zsum);
+                ++routed;
+                a.lse[row0 + lane] = lse;
+                // a row with a NaN has a total of NaN, and so weights of NaN
+                const float by = a.n.normalise ? 1.f / fmaf(0.f, st.y, chosen_sum) : scale;
+                for (int i = 0; i < j; ++i) weights[lane * k + i] *= by;
+            } else {
+                a.lse[row0 + lane] = -INFINITY;
+            }
+            for (; j < k; ++j) {
+                chosen[lane * k + j] = -1;
+                weights[lane * k + j] = 0.f;
+            }
+        }
+        __syncwarp();
+        for (int i = lane; i < rows * k; i += 32) {
+            __stcs(a.chosen + row0 * k + i, chosen[i]);
+            __stcs(a.weights + row0 * k + i, weights[i]);
+        }
+        __syncwarp();
+    }
+    // over the rows side by side, then over the warps
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float2 e = un2(sum[v][p]);
+                sum[v][p] = add2(sum[v][p], f2(__shfl_xor_sync(0xffffffffu, e.x, o),
+                                               __shfl_xor_sync(0xffffffffu, e.y, o)));
+            }
+    zsum = warp_sum_f32(zsum);
+    routed = __reduce_add_sync(0xffffffffu, routed);
+    __syncthreads();
+    float *const s_probs = reinterpret_cast<float *>(s_counts + (E + 3) / 4 * 4);
+    const int width = G * 8;
+    if (sub == 0) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const int g = q + LPR * v;
+            if (g < G) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const float2 e = un2(sum[v][p]);
+                    s_probs[warp * width + 8 * g + 2 * p] = e.x;
+                    s_probs[warp * width + 8 * g + 2 * p + 1] = e.y;
+                }
+            }
+        }
+    }
     if (lane == 0) {
         s_z[warp] = zsum;
         s_n[warp] = routed;
     }
     __syncthreads();
-    const int64_t out = (group * parts + part) * E;
-    for (int e = threadIdx.x; e < E; e += FC_ROUTER_BLOCK) {
+    const int64_t out = (group * cut.parts + part) * E;
+    for (int e = threadIdx.x; e < E; e += 32 * warps) {
         float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < FC_ROUTER_WARPS; ++w) v += s_probs[w][e];
+        for (int w = 0; w < warps; ++w) v += s_probs[w * width + e];
         ws.probs[out + e] = v;
         ws.counts[out + e] = s_counts[e];
     }
     if (threadIdx.x == 0) {
         float v = 0.f;
         int n = 0;
-#pragma unroll
-        for (int w = 0; w < FC_ROUTER_WARPS; ++w) {
+        for (int w = 0; w < warps; ++w) {
             v += s_z[w];
             n += s_n[w];
         }
-        ws.z[group * parts + part] = v;
-        ws.routed[group * parts + part] = n;
+        ws.z[group * cut.parts + part] = v;
+        ws.routed[group * cut.parts + part] = n;
     }
+    if (!cut.joins) return;
+    // few blocks: one cluster, whose first block joins what all have left
+    cluster_sync();
+    if (blockIdx.x != 0) return;
+    float b = 0.f, z = 0.f;
+    for (int64_t g = 0; g < a.n.groups; ++g) {
+        int n = 0;
+        float gz = 0.f;
+        for (int i = 0; i < cut.parts; ++i) {
+            n += __ldcg(ws.routed + g * cut.parts + i);
+            gz += __ldcg(ws.z + g * cut.parts + i);
+        }
+        for (int e = threadIdx.x; e < E; e += 32 * warps)
+            b += rt_join_experts(a, ws, g, cut.parts, n, e) * ((float)E / (float)k);
+        z += gz / (float)max(n, 1);
+        if (threadIdx.x == 0) a.routed[g] = n;
+    }
+    b = warp_sum_f32(b);
+    __syncthreads();
+    if (lane == 0) s_z[warp] = b;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        b = 0.f;
+        for (int w = 0; w < warps; ++w) b += s_z[w];
+        a.loss[0] = b / (float)a.n.groups;
+        a.loss[1] = z / (float)a.n.groups;
+    }
+}
+
+// Rows of a lane at a time.
+template <int LPR, int VPL>
+__host__ __device__ constexpr int rt_rows_bwd()
+{
+    return LPR < 8 ? 1 : LPR < 16 ? 2 : VPL == 1 ? 4 : VPL == 2 ? 2 : 1;
+}
+
+// A warp's shared memory in the backward pass: lse and the weights' common part of each
+// row, the chosen experts and what their weights add, and U * 256 * VPL sums by expert.
+__host__ __device__ constexpr int rt_warp_bytes_bwd(int rows, int k, int adds)
+{
+    return (8 * rows + 8 * rows * k + 15) / 16 * 16 + 4 * adds;
 }
 
 // Backward: with c_e the derivative of the balance loss by every probability of
 // expert e in the row's group,
 //   dlogits_e = p_e (c_e - sum_j p_j c_j + 2 dz lse / (groups n)) + the weights' part
-template <class T, int EPL>
-__global__ void __launch_bounds__(FC_ROUTER_BLOCK)
-    k_router_bwd(const RouterBackward a, const int parts)
+template <class T, int LPR, int VPL, bool ALIGNED>
+__global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
+    k_router_bwd(const __grid_constant__ RouterBackward a, const __grid_constant__ RouterCut cut)
 {
-    __shared__ float s_add[FC_ROUTER_WARPS][32 * EPL];
+    constexpr int RPI = 32 / LPR;
+    constexpr int U = rt_rows_bwd<LPR, VPL>();
+    extern __shared__ uint4 dyn[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = cut.warps;
+    const int E = a.n.experts, k = a.n.k;
+    const int q = lane % LPR, sub = lane / LPR;
+    char *const own = reinterpret_cast<char *>(dyn) +
+                      (size_t)warp * rt_warp_bytes_bwd(cut.rows, k, U * 256 * VPL);
+    // what the weights add to the experts of the U * RPI rows at hand
+    float *const add = reinterpret_cast<float *>(own);
+    float2 *const stats = reinterpret_cast<float2 *>(add + U * 256 * VPL);
+    int *const chosen = reinterpret_cast<int *>(stats + cut.rows);
+    float *const value = reinterpret_cast<float *>(chosen + cut.rows * k);
+    for (int i = lane; i < U * 256 * VPL; i += 32) add[i] = 0.f;
+    const int64_t group = blockIdx.x / (unsigned)cut.parts;
+    const int part = (int)(blockIdx.x - group * cut.parts);
+    const int64_t per = a.n.sequences * a.n.tokens / a.n.groups;
     wait_for_prior_grid();
     allow_dependent_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int E = a.n.experts, k = a.n.k;
-    const int64_t group = blockIdx.x / parts;
-    const int part = (int)(blockIdx.x - group * parts);
-    const int64_t per = a.n.sequences * a.n.tokens / a.n.groups;
-    float *const add = s_add[warp];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) add[lane + 32 * i] = 0.f;
     const float n = a.dloss ? (float)max(__ldg(a.routed + group), 1) : 1.f;
     const float each = 1.f / (n * (float)a.n.groups);
     const float d0 = a.dloss ? __ldg(a.dloss) : 0.f, d1 = a.dloss ? __ldg(a.dloss + 1) : 0.f;
     const float scale = d0 * ((float)E / (float)k) * each / n;
-    float c[EPL];
+    F2 c[VPL][4];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        c[i] = a.dloss && e < E ? scale * (float)__ldg(a.counts + group * E + e) : 0.f;
-    }
-    __syncwarp();
-    for (int64_t at = (int64_t)part * FC_ROUTER_WARPS + warp; at < per;
-         at += (int64_t)parts * FC_ROUTER_WARPS) {
-        const int64_t row = group * per + at;
-        const float lse = __ldg(a.lse + row);
-        T *const out = static_cast<T *>(a.dlogits) + row * a.lddl;
-        if (lse == -INFINITY) {
+    for (int v = 0; v < VPL; ++v)
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (lane + 32 * i < E) __stcs(out + lane + 32 * i, rt_round<T>(0.f));
-            continue;
+        for (int p = 0; p < 4; ++p) {
+            const int e = 8 * (q + LPR * v) + 2 * p;
+            c[v][p] = f2(a.dloss && e < E ? scale * (float)__ldg(a.counts + group * E + e) : 0.f,
+                         a.dloss && e + 1 < E ? scale * (float)__ldg(a.counts + group * E + e + 1) : 0.f);
         }
-        const T *x = static_cast<const T *>(a.logits) + row * a.ld;
-        float p[EPL], inner = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 32 * i;
-            p[i] = e < E ? expf(rt_f32(__ldcs(x + e)) - lse) : 0.f;
-            inner = fmaf(p[i], c[i], inner);
-        }
-        if (fabsf(lse) > FC_ROUTER_FAR) {
-            // lse's own rounding is |lse| units of a probability: added up again
-            float total = 0.f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) total += p[i];
-            const float inv = 1.f / warp_sum_f32(total);
-            inner *= inv;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) p[i] *= inv;
-        }
-        float part2 = 0.f;
-        int e = -1;
-        float w = 0.f, dw = 0.f;
+    const T *const logits = static_cast<const T *>(a.logits);
+    T *const dlogits = static_cast<T *>(a.dlogits);
+    const int64_t tile0 = ((int64_t)part * warps + warp) * cut.rows;
+    for (int64_t at = tile0; at < per; at += (int64_t)cut.parts * warps * cut.rows) {
+        const int64_t row0 = group * per + at;
+        const int rows = (int)(per - at < cut.rows ? per - at : cut.rows);
+        // a lane a row: its lse, and what the weights' gradients come to
+        const float my_lse = lane < rows ? __ldg(a.lse + row0 + lane) : -INFINITY;
+        const unsigned live_rows = __ballot_sync(0xffffffffu, my_lse != -INFINITY);
         if (a.dweights) {
-            if (lane < k) {
-                e = __ldg(a.chosen + row * k + lane);
-                if ((unsigned)e < (unsigned)E) {
-                    w = __ldg(a.weights + row * k + lane);
-                    dw = __ldg(a.dweights + row * k + lane);
-                } else {
-                    e = -1;
+            for (int i = lane; i < rows * k; i += 32) {
+                const int e = __ldg(a.chosen + row0 * k + i);
+                const bool ok = (unsigned)e < (unsigned)E;
+                chosen[i] = ok ? e : -1;
+                value[i] = ok ? __ldg(a.weights + row0 * k + i) : 0.f;
+            }
+            __syncwarp();
+            float inner = 0.f;
+            if (lane < rows && my_lse != -INFINITY) {
+                const float *const dw = a.dweights + (row0 + lane) * k;
+                for (int j = 0; j < k; ++j)
+                    if (chosen[lane * k + j] >= 0)
+                        inner = fmaf(value[lane * k + j], __ldg(dw + j), inner);
+                for (int j = 0; j < k; ++j)
+                    if (chosen[lane * k + j] >= 0)
+                        value[lane * k + j] *= a.n.normalise ? __ldg(dw + j) - inner : __ldg(dw + j);
+            }
+            if (lane < rows)
+                stats[lane] = make_float2(my_lse, (a.n.normalise ? 0.f : -inner) +
+                                                      (my_lse != -INFINITY ? 2.f * d1 * my_lse * each : 0.f));
+        } else if (lane < rows) {
+            stats[lane] = make_float2(my_lse, my_lse != -INFINITY ? 2.f * d1 * my_lse * each : 0.f);
+        }
+        __syncwarp();
+        for (int r0 = 0; r0 < rows; r0 += RPI * U) {
+            Rt8<T, ALIGNED> raw[U][VPL];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) {
+                    const int r = r0 + u * RPI + sub;
+                    raw[u][v].load(logits + (row0 + r) * a.ld, 8 * (q + LPR * v), E,
+                                   r < rows && live_rows >> r & 1);
+                }
+            // the entries of rows r0 .. are next to one another, as are the rows' sums
+            const int entries = min(RPI * U, rows - r0) * k;
+            if (a.dweights) {
+                for (int i = lane; i < entries; i += 32) {
+                    const int e = chosen[r0 * k + i];
+                    if (e >= 0) add[i / k * (LPR * VPL * 8) + e] = value[r0 * k + i];
+                }
+                __syncwarp();
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * RPI + sub;
+                const bool here = r < rows, live = here && live_rows >> r & 1;
+                const float2 st = live ? stats[r] : make_float2(0.f, 0.f);
+                F2 x[VPL][4];
+                F2 acc = f2(0.f, 0.f);
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) {
+                    raw[u][v].get(x[v]);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float2 e = un2(mul2(add2(x[v][p], f2(-st.x, -st.x)),
+                                                  f2(kRtLog2e, kRtLog2e)));
+                        x[v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                        acc = fma2(x[v][p], c[v][p], acc);
+                    }
+                }
+                const float2 both = un2(acc);
+                float inner = rt_row_sum<LPR>(both.x + both.y);
+                const bool far = fabsf(st.x) > FC_ROUTER_FAR;
+                if (__any_sync(0xffffffffu, far)) {
+                    // lse's own rounding is |lse| units of a probability: added up again
+                    F2 all = f2(0.f, 0.f);
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v)
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) all = add2(all, x[v][p]);
+                    const float2 t = un2(all);
+                    const float total = rt_row_sum<LPR>(t.x + t.y);
+                    if (far) {
+                        const float inv = 1.f / total;
+                        inner *= inv;
+#pragma unroll
+                        for (int v = 0; v < VPL; ++v)
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) x[v][p] = mul2(x[v][p], f2(inv, inv));
+                    }
+                }
+                const float less = st.y - inner;
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) {
+                    const float4 *const s4 = reinterpret_cast<const float4 *>(
+                        add + (u * RPI + sub) * (LPR * VPL * 8) + 8 * (q + LPR * v));
+                    const float4 u0 = s4[0], u1 = s4[1];
+                    const F2 w[4] = {f2(u0.x, u0.y), f2(u0.z, u0.w), f2(u1.x, u1.y), f2(u1.z, u1.w)};
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        x[v][p] = live ? fma2(x[v][p], add2(c[v][p], f2(less, less)), w[p])
+                                       : f2(0.f, 0.f);
+                    if (here)
+                        rt_store<T, ALIGNED>(dlogits + (row0 + r) * a.lddl, 8 * (q + LPR * v), E, x[v]);
                 }
             }
-            part2 = warp_sum_f32(w * dw);
-            if (e >= 0) add[e] = a.n.normalise ? w * (dw - part2) : w * dw;
-            if (a.n.normalise) part2 = 0.f;
-            __syncwarp();
+            if (a.dweights) {
+                __syncwarp();
+                for (int i = lane; i < entries; i += 32) {
+                    const int e = chosen[r0 * k + i];
+                    if (e >= 0) add[i / k * (LPR * VPL * 8) + e] = 0.f;
+                }
+                __syncwarp();
+            }
         }
-        inner = warp_sum_f32(inner);
-        const float sub = 2.f * d1 * lse * each - inner - part2;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int q = lane + 32 * i;
-            if (q < E) __stcs(out + q, rt_round<T>(fmaf(p[i], c[i] + sub, add[q])));
-        }
-        if (a.dweights) {
-            __syncwarp();
-            if (e >= 0) add[e] = 0.f;
-            __syncwarp();
-        }
+        __syncwarp();
     }
 }
 
-template <class T, int EPL>
-cudaError_t router_forward_width(const RouterForward &a, int parts, cudaStream_t s)
+// ---- host ------------------------------------------------------------------------------------
+
+// Raises the kernel's limit of shared memory, once a kernel and device.
+cudaError_t router_allow(const void *kernel);
+
+template <class T, int LPR, int VPL, bool ALIGNED>
+cudaError_t router_forward_one(const RouterForward &a, RouterCut cut, cudaStream_t s)
 {
-    return launch_after_prior(k_router_fwd<T, EPL>, (unsigned)(a.n.groups * parts), FC_ROUTER_BLOCK, 0,
-                              s, a, parts);
+    auto *const kernel = k_router_fwd<T, LPR, VPL, ALIGNED>;
+    const int E = a.n.experts, G = (E + 7) / 8;
+    // as many warps to a block as leave room for two blocks to an SM
+    auto bytes = [&](int warps) {
+        const size_t own = (size_t)warps * rt_warp_bytes<T>(G, cut.rows, a.n.k);
+        const size_t sums = (size_t)warps * G * 8 * sizeof(float);
+        return (size_t)(E + 3) / 4 * 16 + (own > sums ? own : sums);
+    };
+    while (cut.warps > 1 && bytes(cut.warps) > 110 * 1024) cut.warps /= 2;
+    const size_t smem = bytes(cut.warps);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = router_allow((const void *)kernel);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.n.groups * cut.parts));
+    cfg.blockDim = dim3(32 * cut.warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cfg.gridDim.x;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cut.joins ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, cut);
 }
 
-template <class T, int EPL>
-cudaError_t router_backward_width(const RouterBackward &a, int parts, cudaStream_t s)
+template <class T, int LPR, int VPL, bool ALIGNED>
+cudaError_t router_backward_one(const RouterBackward &a, RouterCut cut, cudaStream_t s)
 {
-    return launch_after_prior(k_router_bwd<T, EPL>, (unsigned)(a.n.groups * parts), FC_ROUTER_BLOCK, 0,
-                              s, a, parts);
+    auto *const kernel = k_router_bwd<T, LPR, VPL, ALIGNED>;
+    const int own = rt_warp_bytes_bwd(cut.rows, a.n.k, rt_rows_bwd<LPR, VPL>() * 256 * VPL);
+    while (cut.warps > 1 && own * cut.warps > 110 * 1024) cut.warps /= 2;
+    if (own * cut.warps > 40 * 1024) {
+        const cudaError_t e = router_allow((const void *)kernel);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_after_prior(kernel, (unsigned)(a.n.groups * cut.parts), 32 * cut.warps,
+                              (size_t)own * cut.warps, s, a, cut);
+}
+
+// Calls f.template run<LPR, VPL>() for the lanes and groups that a row of E experts takes.
+template <class F>
+cudaError_t router_width(int E, F f)
+{
+    if (E <= 8) return f.template run<1, 1>();
+    if (E <= 16) return f.template run<2, 1>();
+    if (E <= 32) return f.template run<4, 1>();
+    if (E <= 64) return f.template run<8, 1>();
+    if (E <= 128) return f.template run<16, 1>();
+    if (E <= 256) return f.template run<32, 1>();
+    if (E <= 512) return f.template run<32, 2>();
+    return f.template run<32, 4>();
 }
 
 template <class T>
-cudaError_t router_forward(const RouterForward &a, int parts, cudaStream_t s)
+bool router_aligned(int E, const void *p, int64_t ld, int64_t rows)
 {
-    const int e = a.n.experts;
-    if (e <= 32) return router_forward_width<T, 1>(a, parts, s);
-    if (e <= 64) return router_forward_width<T, 2>(a, parts, s);
-    if (e <= 128) return router_forward_width<T, 4>(a, parts, s);
-    if (e <= 256) return router_forward_width<T, 8>(a, parts, s);
-    if (e <= 512) return router_forward_width<T, 16>(a, parts, s);
-    return router_forward_width<T, 32>(a, parts, s);
+    uintptr_t bits = (uintptr_t)p | (uintptr_t)E * sizeof(T);
+    if (rows > 1) bits |= (uintptr_t)ld * sizeof(T);
+    return bits % 16 == 0;
 }
 
 template <class T>
-cudaError_t router_backward(const RouterBackward &a, int parts, cudaStream_t s)
+struct RouterForwardRun {
+    const RouterForward &a;
+    const RouterCut &cut;
+    cudaStream_t s;
+    bool aligned;
+    template <int LPR, int VPL>
+    cudaError_t run() const
+    {
+        return aligned ? router_forward_one<T, LPR, VPL, true>(a, cut, s)
+                       : router_forward_one<T, LPR, VPL, false>(a, cut, s);
+    }
+};
+
+template <class T>
+cudaError_t router_forward(const RouterForward &a, const RouterCut &cut, cudaStream_t s)
 {
-    const int e = a.n.experts;
-    if (e <= 32) return router_backward_width<T, 1>(a, parts, s);
-    if (e <= 64) return router_backward_width<T, 2>(a, parts, s);
-    if (e <= 128) return router_backward_width<T, 4>(a, parts, s);
-    if (e <= 256) return router_backward_width<T, 8>(a, parts, s);
-    if (e <= 512) return router_backward_width<T, 16>(a, parts, s);
-    return router_backward_width<T, 32>(a, parts, s);
+    const bool aligned = router_aligned<T>(a.n.experts, a.logits, a.ld, a.n.sequences * a.n.tokens);
+    return router_width(a.n.experts, RouterForwardRun<T>{a, cut, s, aligned});
+}
+
+template <class T>
+struct RouterBackwardRun {
+    const RouterBackward &a;
+    const RouterCut &cut;
+    cudaStream_t s;
+    bool aligned;
+    template <int LPR, int VPL>
+    cudaError_t run() const
+    {
+        return aligned ? router_backward_one<T, LPR, VPL, true>(a, cut, s)
+                       : router_backward_one<T, LPR, VPL, false>(a, cut, s);
+    }
+};
+
+template <class T>
+cudaError_t router_backward(const RouterBackward &a, const RouterCut &cut, cudaStream_t s)
+{
+    const int64_t rows = a.n.sequences * a.n.tokens;
+    const bool aligned = router_aligned<T>(a.n.experts, a.logits, a.ld, rows) &&
+                         router_aligned<T>(a.n.experts, a.dlogits, a.lddl, rows);
+    return router_width(a.n.experts, RouterBackwardRun<T>{a, cut, s, aligned});
 }
 
 }  // namespace fc

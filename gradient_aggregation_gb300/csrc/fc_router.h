@@ -39,7 +39,7 @@ struct RouterBackward {
 
 // The workspace: what each block of the first kernel leaves, then the groups' shares
 // of the losses, then a counter.
-int64_t router_parts(int64_t sequences, int64_t tokens, int64_t groups);  // blocks a group
+int64_t router_parts(int64_t sequences, int64_t tokens, int64_t groups);  // most blocks a group
 size_t router_workspace(int64_t sequences, int64_t tokens, int64_t experts, int64_t groups);
 
 cudaError_t launch_router_forward(const RouterForward &a, int type, cudaStream_t s);

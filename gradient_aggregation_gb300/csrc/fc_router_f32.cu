@@ -2,7 +2,7 @@
 
 namespace fc {
 
-template cudaError_t router_forward<float>(const RouterForward &, int, cudaStream_t);
-template cudaError_t router_backward<float>(const RouterBackward &, int, cudaStream_t);
+template cudaError_t router_forward<float>(const RouterForward &, const RouterCut &, cudaStream_t);
+template cudaError_t router_backward<float>(const RouterBackward &, const RouterCut &, cudaStream_t);
 
 }  // namespace fc

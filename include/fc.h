@@ -716,8 +716,9 @@ FC_API size_t fc_router_workspace_size(int64_t sequences, int64_t tokens, int64_
  *   loss[0] = 1/B sum_b sum_e (counts[b, e] * experts / (k n)) * probs[b, e]
  *   loss[1] = 1/B sum_b sum_t lse[t]^2 / n
  * (a group with n = 0 adds nothing).  loss[0] is 1 where every expert is as likely
- * and as often chosen as every other; loss[1] keeps the logits small.  All in fp32,
- * sums in a fixed order: the same inputs on the same GPU give the same bits.
+ * and as often chosen as every other; loss[1] keeps the logits small.  All in fp32
+ * (a probability below 2^-126 counts as 0), sums in a fixed order: the same inputs on
+ * the same GPU give the same bits.
  *  logits     device [sequences * tokens, experts] of `type`, rows ld elements
  *             apart, aligned to their element.
  *  lengths    device int32 [sequences], routed tokens at the start of each sequence
@@ -745,7 +746,8 @@ FC_API fc_status fc_router_forward(const void *logits, int64_t sequences, int64_
  * where, w and dw being the row's weights and dweights, i = sum_j w[j] dw[j]:
  *   normalise:  v[chosen[j]] = w[j] * (dw[j] - i), else 0
  *   otherwise:  v[e] = -p[e] * i, plus w[j] * dw[j] for e = chosen[j]
- * in fp32, rounded once.  Rows that were not routed get zeros.
+ * in fp32 (a probability below 2^-126 counts as 0), rounded once.  Rows that were not
+ * routed get zeros.
  *  logits, sequences .. per_sequence, chosen .. routed  as in, or from, the forward
  *             pass (chosen and weights may be NULL without dweights, counts and
  *             routed without dloss).

@@ -169,16 +169,19 @@ def router_backward(logits, sequences, k, normalise, per_sequence, chosen, weigh
     mean = (p * c).sum(1, keepdim=True)
     if normalise:
         v = torch.zeros_like(p).scatter_add_(1, at, torch.where(taken, w * (dw - inner), 0.0))
-        size = p * (c.abs() + (p * c.abs()).sum(1, keepdim=True) + z.abs())
+        factor = c.abs() + (p * c.abs()).sum(1, keepdim=True) + z.abs()
         sizev = w * (dw.abs() + (w * dw).abs().sum(1, keepdim=True))
     else:
         v = torch.zeros_like(p).scatter_add_(1, at, w * dw) - p * inner
-        size = p * (c.abs() + (p * c.abs()).sum(1, keepdim=True) + z.abs()
-                    + (w * dw).abs().sum(1, keepdim=True))
+        factor = (c.abs() + (p * c.abs()).sum(1, keepdim=True) + z.abs()
+                  + (w * dw).abs().sum(1, keepdim=True))
         sizev = w * dw.abs()
     out = p * (c - mean + z) + v
     far = torch.where(live[:, None], (x - lse[:, None]).abs(), 0.0)
     far = torch.where(far < 110, far, 0.0)
     add = (e / 32 + 30 + far.amax(1, keepdim=True) + 2 * lse.abs()[:, None]) * U
-    bound = add * (size + torch.zeros_like(p).scatter_add_(1, at, sizev * taken)) + 2.0 ** -126
+    # a probability below 2^-126 is taken as 0: what it would have been multiplied by, times
+    # that (and a product below 2^-126 may itself be 0)
+    bound = (add * (p * factor + torch.zeros_like(p).scatter_add_(1, at, sizev * taken))
+             + 2.0 ** -126 * (1 + factor))
     return torch.where(live[:, None], out, 0.0), torch.where(live[:, None], bound, 0.0)
