@@ -536,7 +536,7 @@ static bool router_shape(int64_t sequences, int64_t tokens, int64_t experts)
 {
     return sequences >= 0 && tokens >= 0 && sequences <= INT32_MAX && tokens <= INT32_MAX &&
            sequences * tokens <= INT32_MAX && experts >= 1 && experts <= FC_MAX_EXPERTS &&
-           sequences * ((experts + 31) / 32) <= INT32_MAX;
+           sequences * ((experts + 7) / 8) <= INT32_MAX;
 }
 
 static fc_status check_router(int32_t type, int64_t sequences, int64_t tokens, int64_t experts,

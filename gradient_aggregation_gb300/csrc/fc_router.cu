@@ -23,97 +23,104 @@ extern template cudaError_t router_backward<__half>(const RouterBackward &, cons
 extern template cudaError_t router_backward<__nv_bfloat16>(const RouterBackward &, const RouterCut &,
                                                   cudaStream_t);
 
-// Adds the parts of 32 experts of one group, 32 threads to an expert, and leaves
-// their share of the balance loss; the last block adds the shares, in their order.
-__global__ void __launch_bounds__(1024)
-    k_router_join(const RouterForward a, const int parts)
+// Adds the parts of 8 experts of one group, 32 threads to an expert, all their loads in
+// flight, and leaves their share of the balance loss; the last block adds the shares, in
+// their order.
+__global__ void __launch_bounds__(256) k_router_join(const RouterForward a, const int parts)
 {
-    __shared__ float s_p[32][33];
-    __shared__ int s_c[32][33];
-    __shared__ float s_w[32];
-    __shared__ int s_n, s_last;
-    __shared__ float s_b[32], s_z[32];
+    __shared__ float s_p[32][9];
+    __shared__ int s_c[32][9];
+    __shared__ float s_w[8], s_z[8];
+    __shared__ int s_n[8], s_last;
     wait_for_prior_grid();
     allow_dependent_launch();
-    const int E = a.n.experts, tiles = (E + 31) / 32;
-    const int64_t group = blockIdx.x / tiles;
+    const int E = a.n.experts, tiles = (E + 7) / 8;
+    const int64_t group = blockIdx.x / (unsigned)tiles;
     const int tile = (int)(blockIdx.x - group * tiles);
     const RouterWs ws = router_ws(a.ws, a.n.groups, parts, E);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e = tile * 32 + lane;
+    const int q = threadIdx.x >> 3, e = tile * 8 + (threadIdx.x & 7);
     float p = 0.f;
     int c = 0;
     if (e < E) {
-#pragma unroll 4
-        for (int i = warp; i < parts; i += 32) {
-            p += __ldcg(ws.probs + (group * parts + i) * E + e);
-            c += __ldcg(ws.counts + (group * parts + i) * E + e);
+        const int64_t at = group * parts * E + e;
+#pragma unroll 8
+        for (int i = q; i < parts; i += 32) {
+            p += __ldcg(ws.probs + at + (int64_t)i * E);
+            c += __ldcg(ws.counts + at + (int64_t)i * E);
         }
     }
-    s_p[warp][lane] = p;
-    s_c[warp][lane] = c;
-    if (warp == 0) {
-        int n = 0;
-        float z = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            n += __ldcg(ws.routed + group * parts + i);
-            z += __ldcg(ws.z + group * parts + i);
-        }
-        n = __reduce_add_sync(0xffffffffu, n);
-        z = warp_sum_f32(z);
-        if (lane == 0) {
-            s_n = n;
-            s_w[0] = z;
-        }
+    s_p[q][threadIdx.x & 7] = p;
+    s_c[q][threadIdx.x & 7] = c;
+    int n = 0;
+    float z = 0.f;
+    for (int i = threadIdx.x; i < parts; i += 256) {
+        n += __ldcg(ws.routed + group * parts + i);
+        z += __ldcg(ws.z + group * parts + i);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    z = warp_sum_f32(z);
+    if (lane == 0) {
+        s_n[warp] = n;
+        s_z[warp] = z;
     }
     __syncthreads();
-    const int n = s_n;
-    const float each = 1.f / (float)max(n, 1);
-    if (warp == 0) {
-        p = 0.f;
-        c = 0;
+    n = 0;
+    z = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            p += s_p[i][lane];
-            c += s_c[i][lane];
+    for (int i = 0; i < 8; ++i) {
+        n += s_n[i];
+        z += s_z[i];
+    }
+    const float each = 1.f / (float)max(n, 1);
+    // a warp an expert
+    p = warp_sum_f32(s_p[lane][warp]) * each;
+    c = __reduce_add_sync(0xffffffffu, s_c[lane][warp]);
+    if (lane == 0) {
+        const int w = tile * 8 + warp;
+        if (w < E) {
+            a.probs[group * E + w] = p;
+            a.counts[group * E + w] = c;
         }
-        p *= each;
-        if (e < E) {
-            a.probs[group * E + e] = p;
-            a.counts[group * E + e] = c;
-        }
-        const float b = warp_sum_f32(e < E ? (float)c * p : 0.f);
-        if (lane == 0) {
-            if (tile == 0) a.routed[group] = n;
-            float *const share = ws.share + 2 * (group * tiles + tile);
-            share[0] = b * each * ((float)E / (float)a.n.k);
-            share[1] = tile == 0 ? s_w[0] * each : 0.f;
-            __threadfence();
-            s_last = atomicAdd(ws.done, 1u) + 1 == gridDim.x;
-        }
+        s_w[warp] = w < E ? (float)c * p : 0.f;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float b = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b += s_w[i];
+        if (tile == 0) a.routed[group] = n;
+        float *const share = ws.share + 2 * (group * tiles + tile);
+        share[0] = b * each * ((float)E / (float)a.n.k);
+        share[1] = tile == 0 ? z * each : 0.f;
+        __threadfence();
+        s_last = atomicAdd(ws.done, 1u) + 1 == gridDim.x;
+        __threadfence();
     }
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
-    float b = 0.f, z = 0.f;
-    for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += 1024) {
+    float b = 0.f;
+    z = 0.f;
+    for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += 256) {
         b += __ldcg(ws.share + 2 * i);
         z += __ldcg(ws.share + 2 * i + 1);
     }
     b = warp_sum_f32(b);
     z = warp_sum_f32(z);
     if (lane == 0) {
-        s_b[warp] = b;
+        s_w[warp] = b;
         s_z[warp] = z;
     }
     __syncthreads();
-    if (warp == 0) {
-        b = warp_sum_f32(s_b[lane]);
-        z = warp_sum_f32(s_z[lane]);
-        if (lane == 0) {
-            a.loss[0] = b / (float)a.n.groups;
-            a.loss[1] = z / (float)a.n.groups;
+    if (threadIdx.x == 0) {
+        b = z = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            b += s_w[i];
+            z += s_z[i];
         }
+        a.loss[0] = b / (float)a.n.groups;
+        a.loss[1] = z / (float)a.n.groups;
     }
 }
 
@@ -145,7 +152,7 @@ int64_t router_parts(int64_t sequences, int64_t tokens, int64_t groups)
 size_t router_workspace(int64_t sequences, int64_t tokens, int64_t experts, int64_t groups)
 {
     const int64_t parts = router_parts(sequences, tokens, groups);
-    const int64_t words = groups * parts * (2 * experts + 2) + 2 * groups * ((experts + 31) / 32) + 1;
+    const int64_t words = groups * parts * (2 * experts + 2) + 2 * groups * ((experts + 7) / 8) + 1;
     return (size_t)((words * 4 + 255) / 256 * 256);
 }
 
@@ -179,8 +186,8 @@ cudaError_t launch_router_forward(const RouterForward &a, int type, cudaStream_t
     else
         e = router_forward<__nv_bfloat16>(a, cut, s);
     if (e != cudaSuccess || cut.joins) return e;
-    const unsigned tiles = (unsigned)((a.n.experts + 31) / 32);
-    return launch_after_prior(k_router_join, (unsigned)(a.n.groups * tiles), 1024, 0, s, a, cut.parts);
+    const unsigned tiles = (unsigned)((a.n.experts + 7) / 8);
+    return launch_after_prior(k_router_join, (unsigned)(a.n.groups * tiles), 256, 0, s, a, cut.parts);
 }
 
 cudaError_t launch_router_backward(const RouterBackward &a, int type, cudaStream_t s)

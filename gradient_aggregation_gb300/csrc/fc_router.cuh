@@ -49,7 +49,7 @@ struct Rt8 {
     __device__ __forceinline__ void load(const T *row, int e0, int E, bool here)
     {
         if constexpr (kWord) {
-            const uint32_t none = __is_same(T, __half) ? 0xfc00fc00u : 0xff80ff80u;
+            constexpr uint32_t none = __is_same(T, __half) ? 0xfc00fc00u : 0xff80ff80u;
             q = make_uint4(none, none, none, none);
             if (here && e0 < E) q = *reinterpret_cast<const uint4 *>(row + e0);
         } else if constexpr (ALIGNED) {
@@ -208,7 +208,7 @@ __host__ __device__ inline RouterWs router_ws(void *ws, int64_t groups, int64_t 
     w.z = reinterpret_cast<float *>(w.counts + groups * parts * e);
     w.routed = reinterpret_cast<int32_t *>(w.z + groups * parts);
     w.share = reinterpret_cast<float *>(w.routed + groups * parts);
-    w.done = reinterpret_cast<unsigned *>(w.share + 2 * groups * ((e + 31) / 32));
+    w.done = reinterpret_cast<unsigned *>(w.share + 2 * groups * ((e + 7) / 8));
     return w;
 }
 
@@ -219,6 +219,13 @@ struct RouterCut {
     bool joins; // the grid is one cluster, which joins what it leaves
 };
 
+__device__ __forceinline__ float rt_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Sum over the LPR lanes of a row.
 template <int LPR>
 __device__ __forceinline__ float rt_row_sum(float x)
@@ -226,6 +233,28 @@ __device__ __forceinline__ float rt_row_sum(float x)
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
+}
+
+// The sums of U values, each over the LPR lanes of its rows.  Four sums over a whole
+// warp take 6 shuffles and 4 that hand them back, not 20.
+template <int LPR, int U>
+__device__ __forceinline__ void rt_row_sums(float (&x)[U])
+{
+    if constexpr (LPR == 32 && U == 4) {
+        const int lane = threadIdx.x & 31;
+        const bool high = lane & 16, odd = lane & 8;
+        float a = high ? x[2] : x[0], b = high ? x[3] : x[1];
+        a += __shfl_xor_sync(0xffffffffu, high ? x[0] : x[2], 16);
+        b += __shfl_xor_sync(0xffffffffu, high ? x[1] : x[3], 16);
+        float c = odd ? b : a;
+        c += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+        c = rt_row_sum<8>(c);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = __shfl_sync(0xffffffffu, c, 8 * u);
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = rt_row_sum<LPR>(x[u]);
+    }
 }
 
 template <int LPR>
@@ -260,6 +289,11 @@ __device__ __forceinline__ float rt_join_experts(const RouterForward &a, const R
     a.counts[group * E + e] = c;
     return (float)c * p * each;
 }
+
+template <bool YES>
+struct RtYes {
+    static constexpr bool value = YES;
+};
 
 template <class T, int LPR, int VPL, bool ALIGNED>
 __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
@@ -311,82 +345,117 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
             there = row - seq * a.n.tokens < __ldg(a.lengths + seq);
         }
         const unsigned present = __ballot_sync(0xffffffffu, there);
-        // the softmax, U rows of a lane at a time
-        for (int r0 = 0; r0 < rows; r0 += RPI * U) {
+        // the softmax, U rows of a lane at a time.  WHOLE: all of them are there
+        auto softmax = [&](int r0, auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
             Rt8<T, ALIGNED> raw[U][VPL];
+            const T *from = logits + (row0 + r0 + sub) * a.ld;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u, from += RPI * a.ld)
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
                     const int r = r0 + u * RPI + sub;
-                    raw[u][v].load(logits + (row0 + r) * a.ld, 8 * (q + LPR * v), E,
-                                   r < rows && present >> r & 1);
+                    raw[u][v].load(from, 8 * (q + LPR * v), E,
+                                   WHOLE || (r < rows && present >> r & 1));
                 }
+            F2 x[U][VPL][4];
+            float top[U], total[U];
+            bool odd = false;
+            Word *to = words + (r0 + sub) * stride + q;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U; ++u, to += RPI * stride) {
                 const int r = r0 + u * RPI + sub;
-                const bool live = r < rows && present >> r & 1;
-                F2 x[VPL][4];
-                float top = -INFINITY;
+                top[u] = -INFINITY;
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
-                    const int g = q + LPR * v;
-                    raw[u][v].get(x[v]);
+                    raw[u][v].get(x[u][v]);
                     float most = -INFINITY;
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const float2 e = un2(x[v][p]);
+                        const float2 e = un2(x[u][v][p]);
                         most = fmaxf(most, fmaxf(e.x, e.y));
                     }
-                    top = fmaxf(top, most);
-                    if (r < rows && g < G) words[r * stride + g] = RtWord<T>::make(most, g, 0);
+                    top[u] = fmaxf(top[u], most);
+                    if ((WHOLE || r < rows) && q + LPR * v < G)
+                        to[LPR * v] = RtWord<T>::make(most, q + LPR * v, 0);
                 }
-                top = rt_row_max<LPR>(top);
+                top[u] = rt_row_max<LPR>(top[u]);
+                odd |= !(fabsf(top[u]) < 1e38f);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // one shift for all of a row, whatever its rounding, leaves the quotients
+                const float shift = -top[u] * kRtLog2e;
                 F2 acc = f2(0.f, 0.f);
-                bool nan = false;
 #pragma unroll
                 for (int v = 0; v < VPL; ++v)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        // x - top first: products of large numbers would not cancel
-                        const F2 d = add2(x[v][p], f2(-top, -top));
-                        const float2 e = un2(mul2(d, f2(kRtLog2e, kRtLog2e)));
-                        const F2 y = f2(rt_ex2(e.x), rt_ex2(e.y));
-                        acc = add2(acc, y);
-                        x[v][p] = y;
+                        const float2 e = un2(fma2(x[u][v][p], f2(kRtLog2e, kRtLog2e),
+                                                  f2(shift, shift)));
+                        x[u][v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                        acc = add2(acc, x[u][v][p]);
                     }
                 const float2 both = un2(acc);
-                const float total = rt_row_sum<LPR>(both.x + both.y);
-                // closed to all experts, or nothing but NaN
-                const bool closed = !(top > -INFINITY);
-                bool routes = live;
-                if (__any_sync(0xffffffffu, live && closed)) {
-                    if (live && closed) {
+                total[u] = both.x + both.y;
+            }
+            unsigned routes = WHOLE ? ~0u : 0u;  // a bit for each u
+            if (!WHOLE) {
 #pragma unroll
-                        for (int v = 0; v < VPL; ++v) {
-                            raw[u][v].get(x[v]);
+                for (int u = 0; u < U; ++u) {
+                    const int r = r0 + u * RPI + sub;
+                    routes |= (unsigned)(r < rows && present >> r & 1) << u;
+                }
+            }
+            if (__any_sync(0xffffffffu, odd)) {
+                // rows closed to all experts, or with numbers whose product overflows: those
+                // once more, the difference first
 #pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                const float2 e = un2(x[v][p]);
-                                nan |= e.x != e.x || e.y != e.y;
-                            }
+                for (int u = 0; u < U; ++u) {
+                    const bool live = routes >> u & 1, closed = !(top[u] > -INFINITY);
+                    bool nan = false;
+                    F2 acc = f2(0.f, 0.f);
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v) {
+                        raw[u][v].get(x[u][v]);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const F2 d = add2(x[u][v][p], f2(-top[u], -top[u]));
+                            const float2 e = un2(mul2(d, f2(kRtLog2e, kRtLog2e)));
+                            const float2 y = un2(x[u][v][p]);
+                            nan |= y.x != y.x || y.y != y.y;
+                            x[u][v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                            acc = add2(acc, x[u][v][p]);
                         }
                     }
-                    // of the row's own lanes
+                    const float2 both = un2(acc);
+                    total[u] = both.x + both.y;
+                    // of the row's own lanes: nothing but NaN makes no closed row
                     const unsigned votes = __ballot_sync(0xffffffffu, nan);
-                    const unsigned mine = (LPR == 32 ? ~0u : (1u << (LPR & 31)) - 1u) << (sub * LPR);
-                    routes = live && (!closed || (votes & mine));
+                    const unsigned own_lanes = (LPR == 32 ? ~0u : (1u << (LPR & 31)) - 1u) << (sub * LPR);
+                    if (!live || (closed && !(votes & own_lanes))) routes &= ~(1u << u);
                 }
-                const float inv = routes ? 1.f / total : 0.f;
-                if (routes) {
+            }
+            rt_row_sums<LPR, U>(total);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * RPI + sub;
+                const float inv = rt_rcp(total[u]);
+                const bool on = routes >> u & 1;
+                if (on) {
 #pragma unroll
                     for (int v = 0; v < VPL; ++v)
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
-                            sum[v][p] = fma2(x[v][p], f2(inv, inv), sum[v][p]);
+                            sum[v][p] = fma2(x[u][v][p], f2(inv, inv), sum[v][p]);
                 }
-                if (q == 0 && r < rows) stats[r] = make_float2(top, routes ? total : -1.f);
+                if (q == 0 && (WHOLE || r < rows)) stats[r] = make_float2(top[u], on ? total[u] : -1.f);
             }
+        };
+        if (rows % (RPI * U) == 0 && present == (rows == 32 ? ~0u : (1u << rows) - 1u)) {
+            for (int r0 = 0; r0 < rows; r0 += RPI * U) softmax(r0, RtYes<true>());
+        } else {
+            for (int r0 = 0; r0 < rows; r0 += RPI * U) softmax(r0, RtYes<false>());
         }
         __syncwarp();
         // the choice, a lane a row
@@ -585,6 +654,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
     const float each = 1.f / (n * (float)a.n.groups);
     const float d0 = a.dloss ? __ldg(a.dloss) : 0.f, d1 = a.dloss ? __ldg(a.dloss + 1) : 0.f;
     const float scale = d0 * ((float)E / (float)k) * each / n;
+    const int logk = 31 - __clz(k);
     F2 c[VPL][4];
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
@@ -603,112 +673,165 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
         // a lane a row: its lse, and what the weights' gradients come to
         const float my_lse = lane < rows ? __ldg(a.lse + row0 + lane) : -INFINITY;
         const unsigned live_rows = __ballot_sync(0xffffffffu, my_lse != -INFINITY);
+        if (lane < rows)
+            stats[lane] = make_float2(my_lse, my_lse != -INFINITY ? 2.f * d1 * my_lse * each : 0.f);
+        __syncwarp();
         if (a.dweights) {
-            for (int i = lane; i < rows * k; i += 32) {
-                const int e = __ldg(a.chosen + row0 * k + i);
-                const bool ok = (unsigned)e < (unsigned)E;
-                chosen[i] = ok ? e : -1;
-                value[i] = ok ? __ldg(a.weights + row0 * k + i) : 0.f;
+            const int all = rows * k;
+            if (!(k & (k - 1))) {
+                // k lanes side by side have a row's entries
+                for (int i0 = 0; i0 < all; i0 += 32) {
+                    const int i = i0 + lane;
+                    int e = -1;
+                    float w = 0.f, dw = 0.f;
+                    if (i < all) {
+                        e = __ldg(a.chosen + row0 * k + i);
+                        w = __ldg(a.weights + row0 * k + i);
+                        dw = __ldg(a.dweights + row0 * k + i);
+                        if ((unsigned)e >= (unsigned)E || !(live_rows >> (i >> logk) & 1)) {
+                            e = -1;
+                            w = dw = 0.f;
+                        }
+                    }
+                    float inner = w * dw;
+                    for (int o = k >> 1; o > 0; o >>= 1)
+                        inner += __shfl_xor_sync(0xffffffffu, inner, o);
+                    if (i < all) {
+                        chosen[i] = e;
+                        value[i] = w * (a.n.normalise ? dw - inner : dw);
+                        if (!a.n.normalise && !(i & (k - 1))) stats[i >> logk].y -= inner;
+                    }
+                }
+            } else {
+                for (int i = lane; i < all; i += 32) {
+                    const int e = __ldg(a.chosen + row0 * k + i);
+                    const bool ok = (unsigned)e < (unsigned)E;
+                    chosen[i] = ok ? e : -1;
+                    value[i] = ok ? __ldg(a.weights + row0 * k + i) : 0.f;
+                }
+                __syncwarp();
+                if (lane < rows && my_lse != -INFINITY) {
+                    const float *const dw = a.dweights + (row0 + lane) * k;
+                    float inner = 0.f;
+                    for (int j = 0; j < k; ++j)
+                        if (chosen[lane * k + j] >= 0)
+                            inner = fmaf(value[lane * k + j], __ldg(dw + j), inner);
+                    for (int j = 0; j < k; ++j)
+                        if (chosen[lane * k + j] >= 0)
+                            value[lane * k + j] *= a.n.normalise ? __ldg(dw + j) - inner : __ldg(dw + j);
+                    if (!a.n.normalise) stats[lane].y -= inner;
+                }
             }
             __syncwarp();
-            float inner = 0.f;
-            if (lane < rows && my_lse != -INFINITY) {
-                const float *const dw = a.dweights + (row0 + lane) * k;
-                for (int j = 0; j < k; ++j)
-                    if (chosen[lane * k + j] >= 0)
-                        inner = fmaf(value[lane * k + j], __ldg(dw + j), inner);
-                for (int j = 0; j < k; ++j)
-                    if (chosen[lane * k + j] >= 0)
-                        value[lane * k + j] *= a.n.normalise ? __ldg(dw + j) - inner : __ldg(dw + j);
-            }
-            if (lane < rows)
-                stats[lane] = make_float2(my_lse, (a.n.normalise ? 0.f : -inner) +
-                                                      (my_lse != -INFINITY ? 2.f * d1 * my_lse * each : 0.f));
-        } else if (lane < rows) {
-            stats[lane] = make_float2(my_lse, my_lse != -INFINITY ? 2.f * d1 * my_lse * each : 0.f);
         }
-        __syncwarp();
-        for (int r0 = 0; r0 < rows; r0 += RPI * U) {
+        // U rows of a lane at a time.  WHOLE: all of them are there
+        auto gradient = [&](int r0, auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
             Rt8<T, ALIGNED> raw[U][VPL];
+            const T *from = logits + (row0 + r0 + sub) * a.ld;
+            T *to = dlogits + (row0 + r0 + sub) * a.lddl;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u, from += RPI * a.ld)
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
                     const int r = r0 + u * RPI + sub;
-                    raw[u][v].load(logits + (row0 + r) * a.ld, 8 * (q + LPR * v), E,
-                                   r < rows && live_rows >> r & 1);
+                    raw[u][v].load(from, 8 * (q + LPR * v), E,
+                                   WHOLE || (r < rows && live_rows >> r & 1));
                 }
             // the entries of rows r0 .. are next to one another, as are the rows' sums
             const int entries = min(RPI * U, rows - r0) * k;
-            if (a.dweights) {
+            auto scatter = [&](bool clear) {
                 for (int i = lane; i < entries; i += 32) {
                     const int e = chosen[r0 * k + i];
-                    if (e >= 0) add[i / k * (LPR * VPL * 8) + e] = value[r0 * k + i];
+                    const int r = k & (k - 1) ? i / k : i >> logk;
+                    if (e >= 0) add[r * (LPR * VPL * 8) + e] = clear ? 0.f : value[r0 * k + i];
                 }
                 __syncwarp();
-            }
+            };
+            if (a.dweights) scatter(false);
+            F2 x[U][VPL][4];
+            float inner[U];
+            float2 st[U];
+            bool far = false;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int r = r0 + u * RPI + sub;
-                const bool here = r < rows, live = here && live_rows >> r & 1;
-                const float2 st = live ? stats[r] : make_float2(0.f, 0.f);
-                F2 x[VPL][4];
+                st[u] = make_float2(0.f, 0.f);
+                if (WHOLE || (r < rows && live_rows >> r & 1)) st[u] = stats[r];
+                far |= fabsf(st[u].x) > FC_ROUTER_FAR;
+                const float shift = -st[u].x * kRtLog2e;
                 F2 acc = f2(0.f, 0.f);
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
-                    raw[u][v].get(x[v]);
+                    raw[u][v].get(x[u][v]);
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const float2 e = un2(mul2(add2(x[v][p], f2(-st.x, -st.x)),
-                                                  f2(kRtLog2e, kRtLog2e)));
-                        x[v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
-                        acc = fma2(x[v][p], c[v][p], acc);
+                        const float2 e = un2(fma2(x[u][v][p], f2(kRtLog2e, kRtLog2e),
+                                                  f2(shift, shift)));
+                        x[u][v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                        acc = fma2(x[u][v][p], c[v][p], acc);
                     }
                 }
                 const float2 both = un2(acc);
-                float inner = rt_row_sum<LPR>(both.x + both.y);
-                const bool far = fabsf(st.x) > FC_ROUTER_FAR;
-                if (__any_sync(0xffffffffu, far)) {
-                    // lse's own rounding is |lse| units of a probability: added up again
-                    F2 all = f2(0.f, 0.f);
+                inner[u] = both.x + both.y;
+            }
+            if (__any_sync(0xffffffffu, far)) {
+                // lse's own rounding is |lse| units of a probability: the differences first,
+                // and added up again
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    F2 all = f2(0.f, 0.f), acc = f2(0.f, 0.f);
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v) {
+                        raw[u][v].get(x[u][v]);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const F2 d = add2(x[u][v][p], f2(-st[u].x, -st[u].x));
+                            const float2 e = un2(mul2(d, f2(kRtLog2e, kRtLog2e)));
+                            x[u][v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                            all = add2(all, x[u][v][p]);
+                            acc = fma2(x[u][v][p], c[v][p], acc);
+                        }
+                    }
+                    const float2 t = un2(all), both = un2(acc);
+                    const float total = rt_row_sum<LPR>(t.x + t.y);
+                    const float inv = fabsf(st[u].x) > FC_ROUTER_FAR ? 1.f / total : 1.f;
+                    inner[u] = (both.x + both.y) * inv;
 #pragma unroll
                     for (int v = 0; v < VPL; ++v)
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) all = add2(all, x[v][p]);
-                    const float2 t = un2(all);
-                    const float total = rt_row_sum<LPR>(t.x + t.y);
-                    if (far) {
-                        const float inv = 1.f / total;
-                        inner *= inv;
-#pragma unroll
-                        for (int v = 0; v < VPL; ++v)
-#pragma unroll
-                            for (int p = 0; p < 4; ++p) x[v][p] = mul2(x[v][p], f2(inv, inv));
-                    }
+                        for (int p = 0; p < 4; ++p) x[u][v][p] = mul2(x[u][v][p], f2(inv, inv));
                 }
-                const float less = st.y - inner;
+            }
+            rt_row_sums<LPR, U>(inner);
+            const float *plus = add + sub * (LPR * VPL * 8) + 8 * q;
+#pragma unroll
+            for (int u = 0; u < U; ++u, to += RPI * a.lddl, plus += RPI * LPR * VPL * 8) {
+                const int r = r0 + u * RPI + sub;
+                const bool here = WHOLE || r < rows, live = WHOLE || (here && live_rows >> r & 1);
+                const float less = st[u].y - inner[u];
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
-                    const float4 *const s4 = reinterpret_cast<const float4 *>(
-                        add + (u * RPI + sub) * (LPR * VPL * 8) + 8 * (q + LPR * v));
+                    const float4 *const s4 = reinterpret_cast<const float4 *>(plus + 8 * LPR * v);
                     const float4 u0 = s4[0], u1 = s4[1];
                     const F2 w[4] = {f2(u0.x, u0.y), f2(u0.z, u0.w), f2(u1.x, u1.y), f2(u1.z, u1.w)};
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        x[v][p] = live ? fma2(x[v][p], add2(c[v][p], f2(less, less)), w[p])
-                                       : f2(0.f, 0.f);
-                    if (here)
-                        rt_store<T, ALIGNED>(dlogits + (row0 + r) * a.lddl, 8 * (q + LPR * v), E, x[v]);
+                    for (int p = 0; p < 4; ++p) {
+                        x[u][v][p] = fma2(x[u][v][p], add2(c[v][p], f2(less, less)), w[p]);
+                        if (!live) x[u][v][p] = f2(0.f, 0.f);
+                    }
+                    if (here) rt_store<T, ALIGNED>(to, 8 * (q + LPR * v), E, x[u][v]);
                 }
             }
             if (a.dweights) {
                 __syncwarp();
-                for (int i = lane; i < entries; i += 32) {
-                    const int e = chosen[r0 * k + i];
-                    if (e >= 0) add[i / k * (LPR * VPL * 8) + e] = 0.f;
-                }
-                __syncwarp();
+                scatter(true);
             }
+        };
+        if (rows % (RPI * U) == 0 && live_rows == (rows == 32 ? ~0u : (1u << rows) - 1u)) {
+            for (int r0 = 0; r0 < rows; r0 += RPI * U) gradient(r0, RtYes<true>());
+        } else {
+            for (int r0 = 0; r0 < rows; r0 += RPI * U) gradient(r0, RtYes<false>());
         }
         __syncwarp();
     }
