@@ -11,17 +11,12 @@
 
 namespace fc {
 
-extern template cudaError_t router_forward<float>(const RouterForward &, const RouterCut &, cudaStream_t);
-extern template cudaError_t router_forward<__half>(const RouterForward &, const RouterCut &,
-                                                  cudaStream_t);
-extern template cudaError_t router_forward<__nv_bfloat16>(const RouterForward &, const RouterCut &,
-                                                  cudaStream_t);
-extern template cudaError_t router_backward<float>(const RouterBackward &, const RouterCut &,
-                                                  cudaStream_t);
-extern template cudaError_t router_backward<__half>(const RouterBackward &, const RouterCut &,
-                                                  cudaStream_t);
-extern template cudaError_t router_backward<__nv_bfloat16>(const RouterBackward &, const RouterCut &,
-                                                  cudaStream_t);
+extern template cudaError_t router_forward<float>(const RouterForward &, bool *, int *, cudaStream_t);
+extern template cudaError_t router_forward<__half>(const RouterForward &, bool *, int *, cudaStream_t);
+extern template cudaError_t router_forward<__nv_bfloat16>(const RouterForward &, bool *, int *, cudaStream_t);
+extern template cudaError_t router_backward<float>(const RouterBackward &, cudaStream_t);
+extern template cudaError_t router_backward<__half>(const RouterBackward &, cudaStream_t);
+extern template cudaError_t router_backward<__nv_bfloat16>(const RouterBackward &, cudaStream_t);
 
 // Adds the parts of 8 experts of one group, 32 threads to an expert, all their loads in
 // flight, and leaves their share of the balance loss; the last block adds the shares, in
@@ -156,46 +151,27 @@ size_t router_workspace(int64_t sequences, int64_t tokens, int64_t experts, int6
     return (size_t)((words * 4 + 255) / 256 * 256);
 }
 
-// Rows of a warp at a time: 32, so that every lane has one where lanes take rows, but
-// fewer where that would leave warps of the GPU without any; at least as many as lie
-// side by side.
-static RouterCut router_cut(const RouterShape &n)
-{
-    const int64_t rows = n.sequences * n.tokens, per = rows / n.groups;
-    int beside = 32;
-    while (beside > 1 && 256 / beside < n.experts) beside /= 2;
-    RouterCut c = {};
-    c.rows = 32;
-    while (c.rows > beside && rows / c.rows < 2432) c.rows /= 2;
-    c.warps = FC_ROUTER_WARPS;
-    while (c.warps > 1 && per <= (int64_t)c.rows * (c.warps / 2)) c.warps /= 2;
-    const int64_t most = router_parts(n.sequences, n.tokens, n.groups);
-    c.parts = (int)std::max<int64_t>(1, std::min(most, (per + c.rows * c.warps - 1) / (c.rows * c.warps)));
-    c.joins = n.groups * c.parts <= FC_ROUTER_JOIN;
-    return c;
-}
-
 cudaError_t launch_router_forward(const RouterForward &a, int type, cudaStream_t s)
 {
-    const RouterCut cut = router_cut(a.n);
+    bool joins = false;
+    int parts = 1;
     cudaError_t e;
     if (type == FC_TYPE_F32)
-        e = router_forward<float>(a, cut, s);
+        e = router_forward<float>(a, &joins, &parts, s);
     else if (type == FC_TYPE_F16)
-        e = router_forward<__half>(a, cut, s);
+        e = router_forward<__half>(a, &joins, &parts, s);
     else
-        e = router_forward<__nv_bfloat16>(a, cut, s);
-    if (e != cudaSuccess || cut.joins) return e;
+        e = router_forward<__nv_bfloat16>(a, &joins, &parts, s);
+    if (e != cudaSuccess || joins) return e;
     const unsigned tiles = (unsigned)((a.n.experts + 7) / 8);
-    return launch_after_prior(k_router_join, (unsigned)(a.n.groups * tiles), 256, 0, s, a, cut.parts);
+    return launch_after_prior(k_router_join, (unsigned)(a.n.groups * tiles), 256, 0, s, a, parts);
 }
 
 cudaError_t launch_router_backward(const RouterBackward &a, int type, cudaStream_t s)
 {
-    const RouterCut cut = router_cut(a.n);
-    if (type == FC_TYPE_F32) return router_backward<float>(a, cut, s);
-    if (type == FC_TYPE_F16) return router_backward<__half>(a, cut, s);
-    return router_backward<__nv_bfloat16>(a, cut, s);
+    if (type == FC_TYPE_F32) return router_backward<float>(a, s);
+    if (type == FC_TYPE_F16) return router_backward<__half>(a, s);
+    return router_backward<__nv_bfloat16>(a, s);
 }
 
 }  // namespace fc

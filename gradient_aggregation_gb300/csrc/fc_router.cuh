@@ -14,6 +14,8 @@
 // a warp a row, beside 60 for the softmax; a choice by warp reductions took 500.
 #pragma once
 
+#include <algorithm>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,8 +27,8 @@
 
 namespace fc {
 
-#define FC_ROUTER_WARPS 8   // of a block at most
-#define FC_ROUTER_JOIN 8    // blocks of a cluster that join what they leave themselves
+#define FC_ROUTER_WARPS 4   // of a block at most: of small blocks an SM takes nearly as many as another
+#define FC_ROUTER_JOIN 8    // blocks of a cluster
 #define FC_ROUTER_FAR 16.f
 
 constexpr float kRtLog2e = 1.44269504f;
@@ -216,7 +218,7 @@ struct RouterCut {
     int parts;  // blocks a group
     int rows;   // rows of a warp at a time
     int warps;  // of a block
-    bool joins; // the grid is one cluster, which joins what it leaves
+    bool joins; // the grid is one cluster, which joins all
 };
 
 __device__ __forceinline__ float rt_rcp(float x)
@@ -235,22 +237,19 @@ __device__ __forceinline__ float rt_row_sum(float x)
     return x;
 }
 
-// The sums of U values, each over the LPR lanes of its rows.  Four sums over a whole
-// warp take 6 shuffles and 4 that hand them back, not 20.
+// The sums of U values, each over the LPR lanes of its rows.  Two sums take a shuffle
+// for each step of one, and one more.
 template <int LPR, int U>
 __device__ __forceinline__ void rt_row_sums(float (&x)[U])
 {
-    if constexpr (LPR == 32 && U == 4) {
-        const int lane = threadIdx.x & 31;
-        const bool high = lane & 16, odd = lane & 8;
-        float a = high ? x[2] : x[0], b = high ? x[3] : x[1];
-        a += __shfl_xor_sync(0xffffffffu, high ? x[0] : x[2], 16);
-        b += __shfl_xor_sync(0xffffffffu, high ? x[1] : x[3], 16);
-        float c = odd ? b : a;
-        c += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
-        c = rt_row_sum<8>(c);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = __shfl_sync(0xffffffffu, c, 8 * u);
+    if constexpr (LPR >= 4 && U == 2) {
+        const bool high = threadIdx.x & (LPR / 2);
+        float a = high ? x[1] : x[0];
+        a += __shfl_xor_sync(0xffffffffu, high ? x[0] : x[1], LPR / 2);
+        a = rt_row_sum<LPR / 2>(a);
+        const float b = __shfl_xor_sync(0xffffffffu, a, LPR / 2);
+        x[0] = high ? b : a;
+        x[1] = high ? a : b;
     } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) x[u] = rt_row_sum<LPR>(x[u]);
@@ -270,48 +269,37 @@ __device__ __forceinline__ float rt_row_max(float x)
     return x;
 }
 
-// Adds the parts of expert e of a group of rows, and returns its share of the balance
-// loss but for E / k.
-__device__ __forceinline__ float rt_join_experts(const RouterForward &a, const RouterWs &ws,
-                                                 int64_t group, int parts, int n, int e)
-{
-    const int E = a.n.experts;
-    const float each = 1.f / (float)max(n, 1);
-    float p = 0.f;
-    int c = 0;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        p += __ldcg(ws.probs + (group * parts + i) * E + e);
-        c += __ldcg(ws.counts + (group * parts + i) * E + e);
-    }
-    p *= each;
-    a.probs[group * E + e] = p;
-    a.counts[group * E + e] = c;
-    return (float)c * p * each;
-}
-
 template <bool YES>
 struct RtYes {
     static constexpr bool value = YES;
 };
 
+// Blocks of an SM that the registers leave room for: loads in flight matter more than
+// their number in one warp (256 bf16 experts: 64 registers and two rows of a lane at a
+// time 39 us, 124 and four 45).
+template <class T, int VPL>
+__host__ __device__ constexpr int rt_blocks()
+{
+    return VPL > 1 ? 4 : sizeof(T) == 2 ? 7 : 5;
+}
+
 template <class T, int LPR, int VPL, bool ALIGNED>
-__global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
+__global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
     k_router_fwd(const __grid_constant__ RouterForward a, const __grid_constant__ RouterCut cut)
 {
     using Word = typename RtWord<T>::type;
     constexpr int RPI = 32 / LPR;  // rows side by side
-    constexpr int U = LPR < 8 ? 1 : LPR < 16 ? 2 : VPL == 1 ? 4 : VPL == 2 ? 2 : 1;
+    constexpr int U = LPR < 8 ? 1 : VPL <= 2 ? 2 : 1;
     extern __shared__ uint4 dyn[];
     __shared__ float s_z[FC_ROUTER_WARPS];
     __shared__ int s_n[FC_ROUTER_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = cut.warps;
     const int E = a.n.experts, k = a.n.k, G = (E + 7) / 8;
-    const int stride = rt_stride<T>(G);
+    constexpr int NG = LPR * VPL, stride = rt_stride<T>(NG);  // groups, with those past E
     // the block's counts and, at the end, its sums; then each warp's own
     int *const s_counts = reinterpret_cast<int *>(dyn);
     char *const own = reinterpret_cast<char *>(s_counts + (E + 3) / 4 * 4) +
-                      (size_t)warp * rt_warp_bytes<T>(G, cut.rows, k);
+                      (size_t)warp * rt_warp_bytes<T>(NG, cut.rows, k);
     Word *const words = reinterpret_cast<Word *>(own);
     float2 *const stats = reinterpret_cast<float2 *>(words + stride * cut.rows);
     int *const chosen = reinterpret_cast<int *>(stats + cut.rows);
@@ -321,6 +309,8 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
     const int64_t per = a.n.sequences * a.n.tokens / a.n.groups;  // rows of a group
     const RouterWs ws = router_ws(a.ws, a.n.groups, cut.parts, E);
     for (int e = threadIdx.x; e < E; e += 32 * warps) s_counts[e] = 0;
+    if (NG % 4)  // the vectors that end behind a row's words
+        for (int i = lane; i < stride * cut.rows; i += 32) words[i] = 0;
     const int q = lane % LPR, sub = lane / LPR;  // of the row, of the rows side by side
     F2 sum[VPL][4];
 #pragma unroll
@@ -376,7 +366,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
                         most = fmaxf(most, fmaxf(e.x, e.y));
                     }
                     top[u] = fmaxf(top[u], most);
-                    if ((WHOLE || r < rows) && q + LPR * v < G)
+                    if (WHOLE || r < rows)
                         to[LPR * v] = RtWord<T>::make(most, q + LPR * v, 0);
                 }
                 top[u] = rt_row_max<LPR>(top[u]);
@@ -471,15 +461,27 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
                 for (; j < k; ++j) {
                     Word most = 0;
                     if constexpr (sizeof(Word) == 4) {
-                        const uint4 *w4 = reinterpret_cast<const uint4 *>(mine);
-                        int g = 0;
-                        for (; g + 4 <= G; g += 4) {
-                            const uint4 w = w4[g / 4];
-                            most = max(max(max(most, w.x), max(w.y, w.z)), w.w);
+                        const uint4 *const w4 = reinterpret_cast<const uint4 *>(mine);
+                        uint4 m = w4[0];
+#pragma unroll
+                        for (int g = 1; g < (NG + 3) / 4; ++g) {
+                            const uint4 w = w4[g];
+                            m.x = max(m.x, w.x);
+                            m.y = max(m.y, w.y);
+                            m.z = max(m.z, w.z);
+                            m.w = max(m.w, w.w);
                         }
-                        for (; g < G; ++g) most = max(most, mine[g]);
+                        most = max(max(m.x, m.y), max(m.z, m.w));
                     } else {
-                        for (int g = 0; g < G; ++g) most = max(most, mine[g]);
+                        const ulonglong2 *const w2 = reinterpret_cast<const ulonglong2 *>(mine);
+                        ulonglong2 m = w2[0];
+#pragma unroll
+                        for (int g = 1; g < (NG + 1) / 2; ++g) {
+                            const ulonglong2 w = w2[g];
+                            m.x = max(m.x, w.x);
+                            m.y = max(m.y, w.y);
+                        }
+                        most = max(m.x, m.y);
                     }
                     if (most == 0) break;
                     const int g = RtWord<T>::group(most);
@@ -489,18 +491,27 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
                     F2 f[4];
                     raw.load(row, 8 * g, E, true);
                     raw.get(f);
-                    int at_e = 0;
-                    float left = -INFINITY;
-                    float x[8];
+                    // the first of its equals that is not chosen yet, and what then is the
+                    // group's largest: an equal, or the largest below
+                    uint32_t same = 0;
+                    float below[8];
 #pragma unroll
-                    for (int i = 7; i >= 0; --i) {
+                    for (int i = 0; i < 8; ++i) {
                         const float2 e = un2(f[i / 2]);
-                        x[i] = taken >> i & 1 ? -INFINITY : i & 1 ? e.y : e.x;
-                        if (x[i] == value) at_e = i;
+                        const float x = i & 1 ? e.y : e.x;
+                        if (x == value) same |= 1u << i;
+                        below[i] = x < value ? x : -INFINITY;
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) left = fmaxf(left, i == at_e ? -INFINITY : x[i]);
-                    mine[g] = RtWord<T>::make(left, g, taken | 1u << at_e);
+                    for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                        for (int i = 0; i < o; ++i) below[i] = fmaxf(below[i], below[i + o]);
+                    const float left = below[0];
+                    same &= ~taken;
+                    const int at_e = __ffs(same) - 1;
+                    const bool again = same & (same - 1);
+                    mine[g] = RtWord<T>::make(again ? value : left, g,
+                                              again ? taken | 1u << at_e : 0);
                     const float p = rt_ex2((value - st.x) * kRtLog2e);
                     chosen_sum += p;
                     chosen[lane * k + j] = 8 * g + at_e;
@@ -564,49 +575,85 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
         s_n[warp] = routed;
     }
     __syncthreads();
-    const int64_t out = (group * cut.parts + part) * E;
+    float z = 0.f;
+    int n = 0;
+    for (int w = 0; w < warps; ++w) {
+        z += s_z[w];
+        n += s_n[w];
+    }
+    // the block's sums by expert, in place of the first warp's
     for (int e = threadIdx.x; e < E; e += 32 * warps) {
         float v = 0.f;
         for (int w = 0; w < warps; ++w) v += s_probs[w * width + e];
-        ws.probs[out + e] = v;
+        s_probs[e] = v;
+    }
+    if (cut.joins) {
+        // few blocks: one cluster, which holds all there is
+        __shared__ float s_b[FC_ROUTER_WARPS];
+        __shared__ float2 s_all;
+        if (threadIdx.x == 0) s_all = make_float2(z, (float)n);
+        if (gridDim.x > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        // the blocks share the experts; the first adds the losses
+        __shared__ float2 s_share;
+        float b = 0.f, zs = 0.f;
+        for (int64_t g = 0; g < a.n.groups; ++g) {
+            int gn = 0;
+            float gz = 0.f;
+            for (int i = 0; i < cut.parts; ++i) {
+                const uint32_t from = (uint32_t)(g * cut.parts + i);
+                gz += ld_cluster_f32(&s_all.x, from);
+                gn += (int)ld_cluster_f32(&s_all.y, from);
+            }
+            const float each = 1.f / (float)max(gn, 1);
+            for (int e = blockIdx.x * 32 * warps + threadIdx.x; e < E; e += gridDim.x * 32 * warps) {
+                float p = 0.f;
+                int c = 0;
+#pragma unroll 4
+                for (int i = 0; i < cut.parts; ++i) {
+                    const uint32_t from = (uint32_t)(g * cut.parts + i);
+                    p += ld_cluster_f32(s_probs + e, from);
+                    c += __float_as_int(ld_cluster_f32(reinterpret_cast<float *>(s_counts) + e, from));
+                }
+                p *= each;
+                a.probs[g * E + e] = p;
+                a.counts[g * E + e] = c;
+                b = fmaf((float)c * p, each, b);
+            }
+            zs += gz * each;
+            if (blockIdx.x == 0 && threadIdx.x == 0) a.routed[g] = gn;
+        }
+        b = warp_sum_f32(b);
+        if (lane == 0) s_b[warp] = b;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            b = 0.f;
+            for (int w = 0; w < warps; ++w) b += s_b[w];
+            s_share = make_float2(b, zs);
+        }
+        if (gridDim.x > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            b = 0.f;
+            for (uint32_t i = 0; i < gridDim.x; ++i) b += ld_cluster_f32(&s_share.x, i);
+            a.loss[0] = b * ((float)E / (float)k) / (float)a.n.groups;
+            a.loss[1] = zs / (float)a.n.groups;
+        }
+        if (gridDim.x > 1) cluster_sync();  // no block leaves while another reads its sums
+        return;
+    }
+    const int64_t out = (group * cut.parts + part) * E;
+    for (int e = threadIdx.x; e < E; e += 32 * warps) {
+        ws.probs[out + e] = s_probs[e];
         ws.counts[out + e] = s_counts[e];
     }
     if (threadIdx.x == 0) {
-        float v = 0.f;
-        int n = 0;
-        for (int w = 0; w < warps; ++w) {
-            v += s_z[w];
-            n += s_n[w];
-        }
-        ws.z[group * cut.parts + part] = v;
+        ws.z[group * cut.parts + part] = z;
         ws.routed[group * cut.parts + part] = n;
-    }
-    if (!cut.joins) return;
-    // few blocks: one cluster, whose first block joins what all have left
-    cluster_sync();
-    if (blockIdx.x != 0) return;
-    float b = 0.f, z = 0.f;
-    for (int64_t g = 0; g < a.n.groups; ++g) {
-        int n = 0;
-        float gz = 0.f;
-        for (int i = 0; i < cut.parts; ++i) {
-            n += __ldcg(ws.routed + g * cut.parts + i);
-            gz += __ldcg(ws.z + g * cut.parts + i);
-        }
-        for (int e = threadIdx.x; e < E; e += 32 * warps)
-            b += rt_join_experts(a, ws, g, cut.parts, n, e) * ((float)E / (float)k);
-        z += gz / (float)max(n, 1);
-        if (threadIdx.x == 0) a.routed[g] = n;
-    }
-    b = warp_sum_f32(b);
-    __syncthreads();
-    if (lane == 0) s_z[warp] = b;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        b = 0.f;
-        for (int w = 0; w < warps; ++w) b += s_z[w];
-        a.loss[0] = b / (float)a.n.groups;
-        a.loss[1] = z / (float)a.n.groups;
     }
 }
 
@@ -614,7 +661,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
 template <int LPR, int VPL>
 __host__ __device__ constexpr int rt_rows_bwd()
 {
-    return LPR < 8 ? 1 : LPR < 16 ? 2 : VPL == 1 ? 4 : VPL == 2 ? 2 : 1;
+    return LPR < 8 ? 1 : VPL <= 2 ? 2 : 1;
 }
 
 // A warp's shared memory in the backward pass: lse and the weights' common part of each
@@ -628,7 +675,7 @@ __host__ __device__ constexpr int rt_warp_bytes_bwd(int rows, int k, int adds)
 // expert e in the row's group,
 //   dlogits_e = p_e (c_e - sum_j p_j c_j + 2 dz lse / (groups n)) + the weights' part
 template <class T, int LPR, int VPL, bool ALIGNED>
-__global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
+__global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
     k_router_bwd(const __grid_constant__ RouterBackward a, const __grid_constant__ RouterCut cut)
 {
     constexpr int RPI = 32 / LPR;
@@ -842,19 +889,63 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS)
 // Raises the kernel's limit of shared memory, once a kernel and device.
 cudaError_t router_allow(const void *kernel);
 
+// How to cut the rows: as many of a warp at a time as leave the SMs' warps about the same
+// number of tiles each, counting the instructions of a tile (some for each set of rows
+// side by side, some for each tile) and what a tile waits for, in cycles.  `bytes` says
+// what a block of `warps` warps with `rows` rows each needs of shared memory.
+template <class F>
+RouterCut router_cut(const RouterShape &n, int beside, int blocks, int step, int each, int tile, F bytes)
+{
+    const int64_t per = n.sequences * n.tokens / n.groups;
+    const int64_t most = router_parts(n.sequences, n.tokens, n.groups);
+    RouterCut best = {};
+    double least = 0;
+    for (int rows = 32; rows >= (step < 32 ? step : 32); rows -= step) {
+        RouterCut c = {};
+        c.rows = rows;
+        c.warps = FC_ROUTER_WARPS;
+        while (c.warps > 1 && (per <= (int64_t)rows * (c.warps / 2) || bytes(c.warps, rows) > 110 * 1024))
+            c.warps /= 2;
+        const int64_t fit = 232448 / (int64_t)(bytes(c.warps, rows) + 1024);
+        const int64_t slots = 152 * std::min<int64_t>(fit, blocks * FC_ROUTER_WARPS / c.warps) * c.warps;
+        const int64_t tiles = n.groups * ((per + rows - 1) / rows);
+        int64_t rounds = (tiles + slots - 1) / slots;
+        const int64_t parts = (per + rows * c.warps * rounds - 1) / (rows * c.warps * rounds);
+        c.parts = (int)std::max<int64_t>(1, std::min(parts, most));
+        rounds = (per + (int64_t)rows * c.warps * c.parts - 1) / ((int64_t)rows * c.warps * c.parts);
+        const int64_t an_sm = (std::min(n.groups * c.parts * c.warps, slots) + 151) / 152;
+        const double sets = (rows + beside - 1) / beside;
+        const double issue = rounds * an_sm * (each * sets + tile) / 4;
+        const double wait = rounds * (200 * sets + 4 * tile + 1000);
+        const double cost = std::max(issue, wait) + .3 * std::min(issue, wait);
+        if (best.rows == 0 || cost < least) {
+            least = cost;
+            best = c;
+        }
+    }
+    best.joins = n.groups * best.parts <= FC_ROUTER_JOIN;
+    return best;
+}
+
+// Raises the kernel's limit of shared memory, once a kernel and device.
+cudaError_t router_allow(const void *kernel);
+
 template <class T, int LPR, int VPL, bool ALIGNED>
-cudaError_t router_forward_one(const RouterForward &a, RouterCut cut, cudaStream_t s)
+cudaError_t router_forward_one(const RouterForward &a, bool *joins, int *parts, cudaStream_t s)
 {
     auto *const kernel = k_router_fwd<T, LPR, VPL, ALIGNED>;
     const int E = a.n.experts, G = (E + 7) / 8;
-    // as many warps to a block as leave room for two blocks to an SM
-    auto bytes = [&](int warps) {
-        const size_t own = (size_t)warps * rt_warp_bytes<T>(G, cut.rows, a.n.k);
+    auto bytes = [&](int warps, int rows) {
+        const size_t own = (size_t)warps * rt_warp_bytes<T>(LPR * VPL, rows, a.n.k);
         const size_t sums = (size_t)warps * G * 8 * sizeof(float);
         return (size_t)(E + 3) / 4 * 16 + (own > sums ? own : sums);
     };
-    while (cut.warps > 1 && bytes(cut.warps) > 110 * 1024) cut.warps /= 2;
-    const size_t smem = bytes(cut.warps);
+    const int choose = a.n.k * (100 + (int)sizeof(T) / 2 * LPR * VPL) + 200;
+    const RouterCut cut = router_cut(a.n, 32 / LPR, rt_blocks<T, VPL>(), 32 / LPR, 30 + 60 * VPL, choose,
+                                     bytes);
+    *joins = cut.joins;
+    *parts = cut.parts;
+    const size_t smem = bytes(cut.warps, cut.rows);
     if (smem > 40 * 1024) {
         const cudaError_t e = router_allow((const void *)kernel);
         if (e != cudaSuccess) return e;
@@ -871,22 +962,25 @@ cudaError_t router_forward_one(const RouterForward &a, RouterCut cut, cudaStream
     attr[1].val.clusterDim.x = cfg.gridDim.x;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cut.joins ? 2 : 1;
+    cfg.numAttrs = cut.joins && cfg.gridDim.x > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a, cut);
 }
 
 template <class T, int LPR, int VPL, bool ALIGNED>
-cudaError_t router_backward_one(const RouterBackward &a, RouterCut cut, cudaStream_t s)
+cudaError_t router_backward_one(const RouterBackward &a, cudaStream_t s)
 {
     auto *const kernel = k_router_bwd<T, LPR, VPL, ALIGNED>;
-    const int own = rt_warp_bytes_bwd(cut.rows, a.n.k, rt_rows_bwd<LPR, VPL>() * 256 * VPL);
-    while (cut.warps > 1 && own * cut.warps > 110 * 1024) cut.warps /= 2;
-    if (own * cut.warps > 40 * 1024) {
+    auto bytes = [&](int warps, int rows) {
+        return (size_t)warps * rt_warp_bytes_bwd(rows, a.n.k, rt_rows_bwd<LPR, VPL>() * 256 * VPL);
+    };
+    const RouterCut cut = router_cut(a.n, 32 / LPR, rt_blocks<T, VPL>(), 32 / LPR, 40 + 60 * VPL,
+                                     100 + 20 * a.n.k, bytes);
+    const size_t smem = bytes(cut.warps, cut.rows);
+    if (smem > 40 * 1024) {
         const cudaError_t e = router_allow((const void *)kernel);
         if (e != cudaSuccess) return e;
     }
-    return launch_after_prior(kernel, (unsigned)(a.n.groups * cut.parts), 32 * cut.warps,
-                              (size_t)own * cut.warps, s, a, cut);
+    return launch_after_prior(kernel, (unsigned)(a.n.groups * cut.parts), 32 * cut.warps, smem, s, a, cut);
 }
 
 // Calls f.template run<LPR, VPL>() for the lanes and groups that a row of E experts takes.
@@ -914,45 +1008,46 @@ bool router_aligned(int E, const void *p, int64_t ld, int64_t rows)
 template <class T>
 struct RouterForwardRun {
     const RouterForward &a;
-    const RouterCut &cut;
+    bool *joins;
+    int *parts;
     cudaStream_t s;
     bool aligned;
     template <int LPR, int VPL>
     cudaError_t run() const
     {
-        return aligned ? router_forward_one<T, LPR, VPL, true>(a, cut, s)
-                       : router_forward_one<T, LPR, VPL, false>(a, cut, s);
+        return aligned ? router_forward_one<T, LPR, VPL, true>(a, joins, parts, s)
+                       : router_forward_one<T, LPR, VPL, false>(a, joins, parts, s);
     }
 };
 
+// *joins: the launch has joined what its blocks left, `parts` of a group.
 template <class T>
-cudaError_t router_forward(const RouterForward &a, const RouterCut &cut, cudaStream_t s)
+cudaError_t router_forward(const RouterForward &a, bool *joins, int *parts, cudaStream_t s)
 {
     const bool aligned = router_aligned<T>(a.n.experts, a.logits, a.ld, a.n.sequences * a.n.tokens);
-    return router_width(a.n.experts, RouterForwardRun<T>{a, cut, s, aligned});
+    return router_width(a.n.experts, RouterForwardRun<T>{a, joins, parts, s, aligned});
 }
 
 template <class T>
 struct RouterBackwardRun {
     const RouterBackward &a;
-    const RouterCut &cut;
     cudaStream_t s;
     bool aligned;
     template <int LPR, int VPL>
     cudaError_t run() const
     {
-        return aligned ? router_backward_one<T, LPR, VPL, true>(a, cut, s)
-                       : router_backward_one<T, LPR, VPL, false>(a, cut, s);
+        return aligned ? router_backward_one<T, LPR, VPL, true>(a, s)
+                       : router_backward_one<T, LPR, VPL, false>(a, s);
     }
 };
 
 template <class T>
-cudaError_t router_backward(const RouterBackward &a, const RouterCut &cut, cudaStream_t s)
+cudaError_t router_backward(const RouterBackward &a, cudaStream_t s)
 {
     const int64_t rows = a.n.sequences * a.n.tokens;
     const bool aligned = router_aligned<T>(a.n.experts, a.logits, a.ld, rows) &&
                          router_aligned<T>(a.n.experts, a.dlogits, a.lddl, rows);
-    return router_width(a.n.experts, RouterBackwardRun<T>{a, cut, s, aligned});
+    return router_width(a.n.experts, RouterBackwardRun<T>{a, s, aligned});
 }
 
 }  // namespace fc

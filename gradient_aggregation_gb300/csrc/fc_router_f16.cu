@@ -2,7 +2,7 @@
 
 namespace fc {
 
-template cudaError_t router_forward<__half>(const RouterForward &, const RouterCut &, cudaStream_t);
-template cudaError_t router_backward<__half>(const RouterBackward &, const RouterCut &, cudaStream_t);
+template cudaError_t router_forward<__half>(const RouterForward &, bool *, int *, cudaStream_t);
+template cudaError_t router_backward<__half>(const RouterBackward &, cudaStream_t);
 
 }  // namespace fc

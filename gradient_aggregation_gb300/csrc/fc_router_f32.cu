@@ -2,7 +2,7 @@
 
 namespace fc {
 
-template cudaError_t router_forward<float>(const RouterForward &, const RouterCut &, cudaStream_t);
-template cudaError_t router_backward<float>(const RouterBackward &, const RouterCut &, cudaStream_t);
+template cudaError_t router_forward<float>(const RouterForward &, bool *, int *, cudaStream_t);
+template cudaError_t router_backward<float>(const RouterBackward &, cudaStream_t);
 
 }  // namespace fc
