@@ -274,6 +274,13 @@ struct RtYes {
     static constexpr bool value = YES;
 };
 
+// Rows of a lane at a time.
+template <int LPR, int VPL>
+__host__ __device__ constexpr int rt_rows()
+{
+    return LPR < 8 ? 1 : VPL <= 2 ? 2 : 1;
+}
+
 // Blocks of an SM that the registers leave room for: loads in flight matter more than
 // their number in one warp (256 bf16 experts: 64 registers and two rows of a lane at a
 // time 39 us, 124 and four 45).
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
 {
     using Word = typename RtWord<T>::type;
     constexpr int RPI = 32 / LPR;  // rows side by side
-    constexpr int U = LPR < 8 ? 1 : VPL <= 2 ? 2 : 1;
+    constexpr int U = rt_rows<LPR, VPL>();
     extern __shared__ uint4 dyn[];
     __shared__ float s_z[FC_ROUTER_WARPS];
     __shared__ int s_n[FC_ROUTER_WARPS];
@@ -403,23 +410,26 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const bool live = routes >> u & 1, closed = !(top[u] > -INFINITY);
+                    const bool again = !(fabsf(top[u]) < 1e38f);  // the others keep their bits
                     bool nan = false;
                     F2 acc = f2(0.f, 0.f);
 #pragma unroll
                     for (int v = 0; v < VPL; ++v) {
-                        raw[u][v].get(x[u][v]);
+                        F2 y[4];
+                        raw[u][v].get(y);
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
-                            const F2 d = add2(x[u][v][p], f2(-top[u], -top[u]));
+                            const F2 d = add2(y[p], f2(-top[u], -top[u]));
                             const float2 e = un2(mul2(d, f2(kRtLog2e, kRtLog2e)));
-                            const float2 y = un2(x[u][v][p]);
-                            nan |= y.x != y.x || y.y != y.y;
-                            x[u][v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
-                            acc = add2(acc, x[u][v][p]);
+                            const float2 w = un2(y[p]);
+                            nan |= w.x != w.x || w.y != w.y;
+                            const F2 o = f2(rt_ex2(e.x), rt_ex2(e.y));
+                            if (again) x[u][v][p] = o;
+                            acc = add2(acc, o);
                         }
                     }
                     const float2 both = un2(acc);
-                    total[u] = both.x + both.y;
+                    if (again) total[u] = both.x + both.y;
                     // of the row's own lanes: nothing but NaN makes no closed row
                     const unsigned votes = __ballot_sync(0xffffffffu, nan);
                     const unsigned own_lanes = (LPR == 32 ? ~0u : (1u << (LPR & 31)) - 1u) << (sub * LPR);
@@ -657,13 +667,6 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
     }
 }
 
-// Rows of a lane at a time.
-template <int LPR, int VPL>
-__host__ __device__ constexpr int rt_rows_bwd()
-{
-    return LPR < 8 ? 1 : VPL <= 2 ? 2 : 1;
-}
-
 // A warp's shared memory in the backward pass: lse and the weights' common part of each
 // row, the chosen experts and what their weights add, and U * 256 * VPL sums by expert.
 __host__ __device__ constexpr int rt_warp_bytes_bwd(int rows, int k, int adds)
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
     k_router_bwd(const __grid_constant__ RouterBackward a, const __grid_constant__ RouterCut cut)
 {
     constexpr int RPI = 32 / LPR;
-    constexpr int U = rt_rows_bwd<LPR, VPL>();
+    constexpr int U = rt_rows<LPR, VPL>();
     extern __shared__ uint4 dyn[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = cut.warps;
     const int E = a.n.experts, k = a.n.k;
@@ -827,27 +830,29 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                 // and added up again
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    F2 all = f2(0.f, 0.f), acc = f2(0.f, 0.f);
+                    const bool again = fabsf(st[u].x) > FC_ROUTER_FAR;  // the others keep their bits
+                    F2 all = f2(0.f, 0.f), acc = f2(0.f, 0.f), y[VPL][4];
 #pragma unroll
                     for (int v = 0; v < VPL; ++v) {
-                        raw[u][v].get(x[u][v]);
+                        raw[u][v].get(y[v]);
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
-                            const F2 d = add2(x[u][v][p], f2(-st[u].x, -st[u].x));
+                            const F2 d = add2(y[v][p], f2(-st[u].x, -st[u].x));
                             const float2 e = un2(mul2(d, f2(kRtLog2e, kRtLog2e)));
-                            x[u][v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
-                            all = add2(all, x[u][v][p]);
-                            acc = fma2(x[u][v][p], c[v][p], acc);
+                            y[v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                            all = add2(all, y[v][p]);
+                            acc = fma2(y[v][p], c[v][p], acc);
                         }
                     }
                     const float2 t = un2(all), both = un2(acc);
-                    const float total = rt_row_sum<LPR>(t.x + t.y);
-                    const float inv = fabsf(st[u].x) > FC_ROUTER_FAR ? 1.f / total : 1.f;
-                    inner[u] = (both.x + both.y) * inv;
+                    const float inv = 1.f / rt_row_sum<LPR>(t.x + t.y);
+                    if (again) {
+                        inner[u] = (both.x + both.y) * inv;
 #pragma unroll
-                    for (int v = 0; v < VPL; ++v)
+                        for (int v = 0; v < VPL; ++v)
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) x[u][v][p] = mul2(x[u][v][p], f2(inv, inv));
+                            for (int p = 0; p < 4; ++p) x[u][v][p] = mul2(y[v][p], f2(inv, inv));
+                    }
                 }
             }
             rt_row_sums<LPR, U>(inner);
@@ -900,7 +905,7 @@ RouterCut router_cut(const RouterShape &n, int beside, int blocks, int step, int
     const int64_t most = router_parts(n.sequences, n.tokens, n.groups);
     RouterCut best = {};
     double least = 0;
-    for (int rows = 32; rows >= (step < 32 ? step : 32); rows -= step) {
+    for (int rows = 32; rows >= step; rows -= step) {  // whole steps: no tests of the rows
         RouterCut c = {};
         c.rows = rows;
         c.warps = FC_ROUTER_WARPS;
@@ -941,7 +946,8 @@ cudaError_t router_forward_one(const RouterForward &a, bool *joins, int *parts, 
         return (size_t)(E + 3) / 4 * 16 + (own > sums ? own : sums);
     };
     const int choose = a.n.k * (100 + (int)sizeof(T) / 2 * LPR * VPL) + 200;
-    const RouterCut cut = router_cut(a.n, 32 / LPR, rt_blocks<T, VPL>(), 32 / LPR, 30 + 60 * VPL, choose,
+    const RouterCut cut = router_cut(a.n, 32 / LPR, rt_blocks<T, VPL>(),
+                                     32 / LPR * rt_rows<LPR, VPL>(), 30 + 60 * VPL, choose,
                                      bytes);
     *joins = cut.joins;
     *parts = cut.parts;
@@ -971,9 +977,10 @@ cudaError_t router_backward_one(const RouterBackward &a, cudaStream_t s)
 {
     auto *const kernel = k_router_bwd<T, LPR, VPL, ALIGNED>;
     auto bytes = [&](int warps, int rows) {
-        return (size_t)warps * rt_warp_bytes_bwd(rows, a.n.k, rt_rows_bwd<LPR, VPL>() * 256 * VPL);
+        return (size_t)warps * rt_warp_bytes_bwd(rows, a.n.k, rt_rows<LPR, VPL>() * 256 * VPL);
     };
-    const RouterCut cut = router_cut(a.n, 32 / LPR, rt_blocks<T, VPL>(), 32 / LPR, 40 + 60 * VPL,
+    const RouterCut cut = router_cut(a.n, 32 / LPR, rt_blocks<T, VPL>(),
+                                     32 / LPR * rt_rows<LPR, VPL>(), 40 + 60 * VPL,
                                      100 + 20 * a.n.k, bytes);
     const size_t smem = bytes(cut.warps, cut.rows);
     if (smem > 40 * 1024) {
