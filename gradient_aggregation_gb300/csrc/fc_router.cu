@@ -18,15 +18,17 @@ extern template cudaError_t router_backward<float>(const RouterBackward &, cudaS
 extern template cudaError_t router_backward<__half>(const RouterBackward &, cudaStream_t);
 extern template cudaError_t router_backward<__nv_bfloat16>(const RouterBackward &, cudaStream_t);
 
-// Adds the parts of 8 experts of one group, 32 threads to an expert, all their loads in
-// flight, and leaves their share of the balance loss; the last block adds the shares, in
-// their order.
-__global__ void __launch_bounds__(256) k_router_join(const RouterForward a, const int parts)
+// Adds the parts of 8 experts of one group, ADD / 8 threads to an expert, eight of their
+// loads in flight, and leaves their share of the balance loss; the last block adds the
+// shares, in their order.
+template <int ADD>
+__global__ void __launch_bounds__(ADD) k_router_join(const RouterForward a, const int parts)
 {
-    __shared__ float s_p[32][9];
-    __shared__ int s_c[32][9];
-    __shared__ float s_w[8], s_z[8];
-    __shared__ int s_n[8], s_last;
+    constexpr int kTeam = ADD / 8, kWarps = ADD / 32;
+    __shared__ float s_p[kTeam][9];
+    __shared__ int s_c[kTeam][9];
+    __shared__ float s_w[kWarps], s_z[kWarps];
+    __shared__ int s_n[kWarps], s_last;
     wait_for_prior_grid();
     allow_dependent_launch();
     const int E = a.n.experts, tiles = (E + 7) / 8;
@@ -40,7 +42,7 @@ __global__ void __launch_bounds__(256) k_router_join(const RouterForward a, cons
     if (e < E) {
         const int64_t at = group * parts * E + e;
 #pragma unroll 8
-        for (int i = q; i < parts; i += 32) {
+        for (int i = q; i < parts; i += kTeam) {
             p += __ldcg(ws.probs + at + (int64_t)i * E);
             c += __ldcg(ws.counts + at + (int64_t)i * E);
         }
@@ -49,7 +51,7 @@ __global__ void __launch_bounds__(256) k_router_join(const RouterForward a, cons
     s_c[q][threadIdx.x & 7] = c;
     int n = 0;
     float z = 0.f;
-    for (int i = threadIdx.x; i < parts; i += 256) {
+    for (int i = threadIdx.x; i < parts; i += ADD) {
         n += __ldcg(ws.routed + group * parts + i);
         z += __ldcg(ws.z + group * parts + i);
     }
@@ -60,24 +62,27 @@ __global__ void __launch_bounds__(256) k_router_join(const RouterForward a, cons
         s_z[warp] = z;
     }
     __syncthreads();
-    n = 0;
-    z = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        n += s_n[i];
-        z += s_z[i];
-    }
+    n = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_n[lane] : 0);
+    z = warp_sum_f32(lane < kWarps ? s_z[lane] : 0.f);
     const float each = 1.f / (float)max(n, 1);
-    // a warp an expert
-    p = warp_sum_f32(s_p[lane][warp]) * each;
-    c = __reduce_add_sync(0xffffffffu, s_c[lane][warp]);
-    if (lane == 0) {
-        const int w = tile * 8 + warp;
-        if (w < E) {
-            a.probs[group * E + w] = p;
-            a.counts[group * E + w] = c;
+    if (warp < 8) {  // an expert each
+        p = 0.f;
+        c = 0;
+#pragma unroll
+        for (int i = 0; i < kTeam; i += 32) {
+            p += s_p[i + lane][warp];
+            c += s_c[i + lane][warp];
         }
-        s_w[warp] = w < E ? (float)c * p : 0.f;
+        p = warp_sum_f32(p) * each;
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) {
+            const int w = tile * 8 + warp;
+            if (w < E) {
+                a.probs[group * E + w] = p;
+                a.counts[group * E + w] = c;
+            }
+            s_w[warp] = w < E ? (float)c * p : 0.f;
+        }
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -96,7 +101,7 @@ __global__ void __launch_bounds__(256) k_router_join(const RouterForward a, cons
     if (!s_last) return;
     float b = 0.f;
     z = 0.f;
-    for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += 256) {
+    for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += ADD) {
         b += __ldcg(ws.share + 2 * i);
         z += __ldcg(ws.share + 2 * i + 1);
     }
@@ -107,15 +112,13 @@ __global__ void __launch_bounds__(256) k_router_join(const RouterForward a, cons
         s_z[warp] = z;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        b = z = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            b += s_w[i];
-            z += s_z[i];
+    if (warp == 0) {
+        b = warp_sum_f32(lane < kWarps ? s_w[lane] : 0.f);
+        z = warp_sum_f32(lane < kWarps ? s_z[lane] : 0.f);
+        if (lane == 0) {
+            a.loss[0] = b / (float)a.n.groups;
+            a.loss[1] = z / (float)a.n.groups;
         }
-        a.loss[0] = b / (float)a.n.groups;
-        a.loss[1] = z / (float)a.n.groups;
     }
 }
 
@@ -164,7 +167,11 @@ cudaError_t launch_router_forward(const RouterForward &a, int type, cudaStream_t
         e = router_forward<__nv_bfloat16>(a, &joins, &parts, s);
     if (e != cudaSuccess || joins) return e;
     const unsigned tiles = (unsigned)((a.n.experts + 7) / 8);
-    return launch_after_prior(k_router_join, (unsigned)(a.n.groups * tiles), 256, 0, s, a, parts);
+    const unsigned grid = (unsigned)(a.n.groups * tiles);
+    // one round of loads either way (131072 x 8 bf16: 12.8 us with small blocks, 10.6 with
+    // large ones; 16 groups of 2048 x 60 fp32: 11.1 and 12.9)
+    if (parts <= 256) return launch_after_prior(k_router_join<256>, grid, 256, 0, s, a, parts);
+    return launch_after_prior(k_router_join<1024>, grid, 1024, 0, s, a, parts);
 }
 
 cudaError_t launch_router_backward(const RouterBackward &a, int type, cudaStream_t s)

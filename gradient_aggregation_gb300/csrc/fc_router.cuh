@@ -794,7 +794,9 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                 for (int i = lane; i < entries; i += 32) {
                     const int e = chosen[r0 * k + i];
                     const int r = k & (k - 1) ? i / k : i >> logk;
-                    if (e >= 0) add[r * (LPR * VPL * 8) + e] = clear ? 0.f : value[r0 * k + i];
+                    if (e >= 0)
+                        add[r * (LPR * VPL * 8) + (e >> 2 & 1) * (LPR * VPL * 4) + (e >> 3) * 4 +
+                            (e & 3)] = clear ? 0.f : value[r0 * k + i];
                 }
                 __syncwarp();
             };
@@ -856,7 +858,8 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                 }
             }
             rt_row_sums<LPR, U>(inner);
-            const float *plus = add + sub * (LPR * VPL * 8) + 8 * q;
+            // a row's sums: the first halves of all groups, then the second ones
+            const float *plus = add + sub * (LPR * VPL * 8) + 4 * q;
 #pragma unroll
             for (int u = 0; u < U; ++u, to += RPI * a.lddl, plus += RPI * LPR * VPL * 8) {
                 const int r = r0 + u * RPI + sub;
@@ -864,8 +867,8 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                 const float less = st[u].y - inner[u];
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
-                    const float4 *const s4 = reinterpret_cast<const float4 *>(plus + 8 * LPR * v);
-                    const float4 u0 = s4[0], u1 = s4[1];
+                    const float4 u0 = *reinterpret_cast<const float4 *>(plus + 4 * LPR * v);
+                    const float4 u1 = *reinterpret_cast<const float4 *>(plus + 4 * LPR * (v + VPL));
                     const F2 w[4] = {f2(u0.x, u0.y), f2(u0.z, u0.w), f2(u1.x, u1.y), f2(u1.z, u1.w)};
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
