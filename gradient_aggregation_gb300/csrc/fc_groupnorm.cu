@@ -27,12 +27,13 @@ bool gn_may_stream(const GnShape &n)
     return cpg > 256 || n.positions * cpg > 1 << 16;
 }
 
-// Parts of 64 positions or more, as many as make 1024 blocks over the samples; none is
-// empty.
+// As many parts as make 1024 blocks over the samples, of 16 positions or more and of 4096
+// elements or more (16 a thread); none is empty.
 int64_t gn_parts(const GnShape &n)
 {
     const int64_t most = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, n.samples));
-    const int64_t want = std::min(most, (n.positions + 63) / 64);
+    const int64_t least = std::max<int64_t>(16, 4096 / n.channels);
+    const int64_t want = std::min(most, (n.positions + least - 1) / least);
     const int64_t rows = (n.positions + want - 1) / want;
     return (n.positions + rows - 1) / rows;
 }
@@ -142,12 +143,13 @@ bool find_plan(const GnShape &n, int ab, int ne, int tensors, const void *kernel
     p.ns = ns;
     p.total = (float)n.positions * (float)cpg;
     p.divn = cpg % ne == 0 ? (int)(((1 << 20) + cpg / ne - 1) / (cpg / ne)) : 0;
+    // units of a slab; the last slab may have fewer
+    const int64_t slabs[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256, 384, 512, units};
     for (int T = 128; T <= FC_GN_THREADS; T *= 2) {
-        for (int64_t u = 1; u <= units && u * uv <= T; u *= 2) {
-            while (units % u) ++u;  // slabs all alike
-            if (u * uv > T) break;
+        for (const int64_t u : slabs) {
+            if (u > units || u * uv > T) continue;
             const int V = (int)(u * uv), R = T / V, gs = (int)(u * unit / cpg);
-            const int64_t nslab = units / u, items = n.samples * nslab;
+            const int64_t nslab = (units + u - 1) / u, items = n.samples * nslab;
             for (int K = 1; K <= limit && (K == 1 || K <= n.positions); K *= 2) {
                 const int64_t rows = (n.positions + K - 1) / K, iters = (rows + R - 1) / R;
                 const int64_t part = (iters * T * ab + 15) / 16 * 16;
@@ -167,7 +169,8 @@ bool find_plan(const GnShape &n, int ab, int ne, int tensors, const void *kernel
                 const int64_t rounds = (items + at_once - 1) / at_once;
                 const int64_t an_sm = std::min(occ, (at_once * K + 151) / 152);
                 // us of a round: HBM's, the instructions', and what neither hides
-                const double wide = V * ab >= 128 ? 1 : V * ab >= 64 ? 1.03 : V * ab >= 32 ? 1.35 : 2;
+                const double wide = V * ab >= 128 ? 1 : V * ab >= 64 ? 1.03 : V * ab >= 32 ? 1.35
+                                    : V * ab >= 16 ? 2 : V * ab >= 8 ? 3 : 24. / (V * ab);
                 const double mem = (double)at_once * rows * K * V * ab * (tensors + 1) * wide / 6.6e6;
                 const double inst = (tensors == 2 ? 22 : 11) * ne + 10;
                 const double issue = an_sm * (T / 32) * (iters * inst + 600) / 7600.;

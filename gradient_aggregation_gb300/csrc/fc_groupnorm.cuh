@@ -357,7 +357,16 @@ struct GnTile {
 };
 
 #define FC_GN_BLOCK 256
-#define FC_GN_RUN 64  // rows between two fresh pivots
+#define FC_GN_RUN 64  // rows between two fresh pivots, a multiple of any batch
+
+// Rows whose loads a thread has in flight at a time: up to 64 bytes, of two tensors 32
+// each; narrow vectors are bound by the wait for them (8 x 16427 x 384 bf16 at an odd
+// pitch, backward: 658 us two at a time).
+template <int AB, int TENSORS>
+constexpr int gn_batch()
+{
+    return AB == 16 ? 4 / TENSORS : AB == 8 ? 8 / TENSORS : 8;
+}
 
 struct GnPlace {
     int64_t n, first, end;  // sample, this block's positions
@@ -397,12 +406,13 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
                const int64_t sets)
 {
     using V = Gv<T, AB>;
-    constexpr int NE = V::NE, NP = V::NP;
+    constexpr int NE = V::NE, NP = V::NP, U = gn_batch<AB, 1>();
     __shared__ float sm[2][FC_GN_BLOCK * NE];
     wait_for_prior_grid();
     allow_dependent_launch();
     const GnPlace q = gn_place<NE>(tile, n.positions);
     const T *base = static_cast<const T *>(x.p) + q.n * x.ss + q.c0;
+    const int64_t step = q.R * x.ld;
     F2 mean[NP], m2[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) mean[p] = m2[p] = f2(0.f, 0.f);
@@ -411,24 +421,32 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
         for (int64_t run = q.first + q.r; run < q.end; run += (int64_t)FC_GN_RUN * q.R) {
             F2 neg[NP], s[NP], ss[NP];
             float k = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < FC_GN_RUN; ++i) {
-                const int64_t row = run + (int64_t)i * q.R;
-                if (row >= q.end) break;
-                F2 f[NP];
-                V::get(*reinterpret_cast<const typename V::Raw *>(base + row * x.ld), f);
+            const T *at = base + run * x.ld;
+            int left = (int)min((int64_t)FC_GN_RUN, (q.end - run + q.R - 1) / q.R);
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    if (i == 0) {
-                        neg[p] = neg2(f[p]);
-                        s[p] = ss[p] = f2(0.f, 0.f);
-                    } else {
+            for (int p = 0; p < NP; ++p) s[p] = ss[p] = f2(0.f, 0.f);
+            V::get(*reinterpret_cast<const typename V::Raw *>(at), neg);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) neg[p] = neg2(neg[p]);
+            k = (float)left;
+            for (; left > 0; left -= U, at += U * step) {
+                typename V::Raw raw[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < left)
+                        raw[u] = *reinterpret_cast<const typename V::Raw *>(at + u * step);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u >= left) break;
+                    F2 f[NP];
+                    V::get(raw[u], f);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
                         const F2 d = add2(f[p], neg[p]);
                         s[p] = add2(s[p], d);
                         ss[p] = fma2(d, d, ss[p]);
                     }
                 }
-                k += 1.f;
             }
             const float inv = 1.f / k, total = count + k, part = k / total;
 #pragma unroll
@@ -491,42 +509,54 @@ __device__ __forceinline__ float gn_team_sum(float v, float *sm)
     return v;
 }
 
+// Calls f(part, channel) for a thread's share of a group's parts and channels, TPG side by
+// side.
+template <int TPG, class F>
+__device__ __forceinline__ void gn_entries(int lane, int parts, int cpg, F f)
+{
+    int p = lane / cpg, c = lane - p * cpg;
+    const int dp = TPG / cpg, dc = TPG - dp * cpg;
+#pragma unroll 4
+    while (p < parts) {
+        f(p, c);
+        p += dp;
+        c += dc;
+        if (c >= cpg) {
+            c -= cpg;
+            ++p;
+        }
+    }
+}
+
 // Joins the parts and channels of every group: TPG threads a group and sample.
 template <int TPG>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(TPG > 256 ? TPG : 256)
     k_gn_finish(const GnShape n, const int parts, const int64_t part_rows,
                 const float *__restrict__ in, const int64_t sets, const float eps,
                 float *__restrict__ stat, float *mean_out, float *rstd_out)
 {
-    __shared__ float sm[8];
+    __shared__ float sm[TPG > 32 ? TPG / 32 : 1];
     wait_for_prior_grid();
     allow_dependent_launch();
-    const int64_t at = (int64_t)blockIdx.x * (256 / TPG) + threadIdx.x / TPG;
+    const int64_t at = (int64_t)blockIdx.x * (TPG < 256 ? 256 / TPG : 1) + threadIdx.x / TPG;
     if (at >= n.samples * n.groups) return;  // whole warps, or whole blocks
     const int lane = threadIdx.x % TPG, cpg = n.channels / n.groups;
     const int64_t sample = at / n.groups, padded = (n.channels + 7) & ~7;
     const int c0 = (int)(at - sample * n.groups) * cpg;
-    const int64_t entries = (int64_t)parts * cpg;
     const float total = (float)n.positions * (float)cpg;
+    const float *const from = in + sample * parts * padded + c0;
+    const float last = (float)(n.positions - (parts - 1) * part_rows);
     float s = 0.f;
-    for (int64_t i = lane; i < entries; i += TPG) {
-        const int64_t p = i / cpg;
-        const int64_t set = sample * parts + p;
-        const int64_t left = n.positions - p * part_rows;
-        const float have = (float)(left < part_rows ? left : part_rows);
-        s = fmaf(have, __ldcg(in + set * padded + c0 + (i - p * cpg)), s);
-    }
+    gn_entries<TPG>(lane, parts, cpg, [&](int p, int c) {
+        s = fmaf(p < parts - 1 ? (float)part_rows : last, __ldcg(from + p * padded + c), s);
+    });
     const float m = gn_team_sum<TPG>(s, sm) / total;
     float q = 0.f;
-    for (int64_t i = lane; i < entries; i += TPG) {
-        const int64_t p = i / cpg;
-        const int64_t set = sample * parts + p;
-        const int64_t left = n.positions - p * part_rows;
-        const float have = (float)(left < part_rows ? left : part_rows);
-        const int64_t j = set * padded + c0 + (i - p * cpg);
-        const float d = __ldcg(in + j) - m;
-        q += fmaf(have * d, d, __ldcg(in + sets * padded + j));
-    }
+    gn_entries<TPG>(lane, parts, cpg, [&](int p, int c) {
+        const float *const at = from + p * padded + c;
+        const float d = __ldcg(at) - m;
+        q += fmaf((p < parts - 1 ? (float)part_rows : last) * d, d, __ldcg(at + sets * padded));
+    });
     q = gn_team_sum<TPG>(q, sm);
     if (lane == 0) {
         const float r = 1.f / sqrtf(q / total + eps);
@@ -545,7 +575,7 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
     k_gn_apply(const GnForward a, const GnTile tile, const float *__restrict__ stat)
 {
     using V = Gv<T, AB>;
-    constexpr int NE = V::NE, NP = V::NP;
+    constexpr int NE = V::NE, NP = V::NP, U = gn_batch<AB, 1>();
     const GnPlace q = gn_place<NE>(tile, a.n.positions);
     const int cpg = a.n.channels / a.n.groups;
     F2 w[NP], b[NP], m[NP];
@@ -563,16 +593,25 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
         m[p] = f2(-__ldcg(st + 2 * g0), -__ldcg(st + 2 * g1));
         w[p] = mul2(w[p], f2(__ldcg(st + 2 * g0 + 1), __ldcg(st + 2 * g1 + 1)));
     }
-    const T *x = static_cast<const T *>(a.x.p) + q.n * a.x.ss + q.c0;
-    T *y = static_cast<T *>(const_cast<void *>(a.y.p)) + q.n * a.y.ss + q.c0;
-#pragma unroll 4
-    for (int64_t row = q.first + q.r; row < q.end; row += q.R) {
-        F2 f[NP];
-        V::get(__ldcs(reinterpret_cast<const typename V::Raw *>(x + row * a.x.ld)), f);
+    const int64_t row = q.first + q.r, sx = q.R * a.x.ld, sy = q.R * a.y.ld;
+    const T *x = static_cast<const T *>(a.x.p) + q.n * a.x.ss + row * a.x.ld + q.c0;
+    T *y = static_cast<T *>(const_cast<void *>(a.y.p)) + q.n * a.y.ss + row * a.y.ld + q.c0;
+    for (int64_t left = row < q.end ? (q.end - row + q.R - 1) / q.R : 0; left > 0;
+         left -= U, x += U * sx, y += U * sy) {
+        typename V::Raw raw[U];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) f[p] = fma2(add2(f[p], m[p]), w[p], b[p]);
-        gn_act<ACT, NP>(f);
-        __stcs(reinterpret_cast<typename V::Raw *>(y + row * a.y.ld), V::put(f));
+        for (int u = 0; u < U; ++u)
+            if (u < left) raw[u] = __ldcs(reinterpret_cast<const typename V::Raw *>(x + u * sx));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u >= left) break;
+            F2 f[NP];
+            V::get(raw[u], f);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) f[p] = fma2(add2(f[p], m[p]), w[p], b[p]);
+            gn_act<ACT, NP>(f);
+            __stcs(reinterpret_cast<typename V::Raw *>(y + u * sy), V::put(f));
+        }
     }
 }
 
@@ -606,7 +645,7 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
     k_gn_sums(const GnBackward a, const GnTile tile, float *__restrict__ out, const int64_t sets)
 {
     using V = Gv<T, AB>;
-    constexpr int NE = V::NE, NP = V::NP;
+    constexpr int NE = V::NE, NP = V::NP, U = gn_batch<AB, 2>();
     __shared__ float sm[2][FC_GN_BLOCK * NE];
     wait_for_prior_grid();
     allow_dependent_launch();
@@ -624,21 +663,34 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
         ch.mean.load(g0, q.c0 - g0 * cpg, cpg, [&](int g) { return __ldg(a.mean + at + g); });
         ch.rstd.load(g0, q.c0 - g0 * cpg, cpg, [&](int g) { return __ldg(a.rstd + at + g); });
         ch.scale(w);
-        const T *x = static_cast<const T *>(a.x.p) + q.n * a.x.ss + q.c0;
-        const T *dy = static_cast<const T *>(a.dy.p) + q.n * a.dy.ss + q.c0;
-#pragma unroll 2
-        for (int64_t row = q.first + q.r; row < q.end; row += q.R) {
-            F2 f[NP], g[NP], h[NP], dz[NP];
-            V::get(*reinterpret_cast<const typename V::Raw *>(x + row * a.x.ld), f);
-            V::get(*reinterpret_cast<const typename V::Raw *>(dy + row * a.dy.ld), g);
-            ch.template at<ACT>(f, g, h, dz, [&] {
-                return GnSource{x + row * a.x.ld, a.mean + at + g0, a.rstd + at + g0, 1,
-                                q.c0 - g0 * cpg, cpg, a.weight, a.bias, a.ptype, q.c0};
-            });
+        const int64_t row = q.first + q.r, sx = q.R * a.x.ld, sy = q.R * a.dy.ld;
+        const T *x = static_cast<const T *>(a.x.p) + q.n * a.x.ss + row * a.x.ld + q.c0;
+        const T *dy = static_cast<const T *>(a.dy.p) + q.n * a.dy.ss + row * a.dy.ld + q.c0;
+        for (int64_t left = row < q.end ? (q.end - row + q.R - 1) / q.R : 0; left > 0;
+             left -= U, x += U * sx, dy += U * sy) {
+            typename V::Raw rx[U], ry[U];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                sh[p] = fma2(dz[p], h[p], sh[p]);
-                s[p] = add2(s[p], dz[p]);
+            for (int u = 0; u < U; ++u) {
+                if (u < left) {
+                    rx[u] = *reinterpret_cast<const typename V::Raw *>(x + u * sx);
+                    ry[u] = *reinterpret_cast<const typename V::Raw *>(dy + u * sy);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u >= left) break;
+                F2 f[NP], g[NP], h[NP], dz[NP];
+                V::get(rx[u], f);
+                V::get(ry[u], g);
+                ch.template at<ACT>(f, g, h, dz, [&] {
+                    return GnSource{x + u * sx, a.mean + at + g0, a.rstd + at + g0, 1,
+                                    q.c0 - g0 * cpg, cpg, a.weight, a.bias, a.ptype, q.c0};
+                });
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    sh[p] = fma2(dz[p], h[p], sh[p]);
+                    s[p] = add2(s[p], dz[p]);
+                }
             }
         }
 #pragma unroll
@@ -667,30 +719,28 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
 
 // sum q / M and sum q h / M of every group and sample, from the parts' sums.
 template <class T, int TPG>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(TPG > 256 ? TPG : 256)
     k_gn_finish_sums(const GnBackward a, const int parts, const float *__restrict__ in,
                      const int64_t sets, float *__restrict__ stat)
 {
-    __shared__ float sm[8];
+    __shared__ float sm[TPG > 32 ? TPG / 32 : 1];
     wait_for_prior_grid();
     allow_dependent_launch();
     const GnShape &n = a.n;
-    const int64_t at = (int64_t)blockIdx.x * (256 / TPG) + threadIdx.x / TPG;
+    const int64_t at = (int64_t)blockIdx.x * (TPG < 256 ? 256 / TPG : 1) + threadIdx.x / TPG;
     if (at >= n.samples * n.groups) return;
     const int lane = threadIdx.x % TPG, cpg = n.channels / n.groups;
     const int64_t sample = at / n.groups, padded = (n.channels + 7) & ~7;
     const int c0 = (int)(at - sample * n.groups) * cpg;
-    const int64_t entries = (int64_t)parts * cpg;
     const float inv = 1.f / ((float)n.positions * (float)cpg);
+    const float *const from = in + sample * parts * padded + c0;
     float s1 = 0.f, s2 = 0.f;
-    for (int64_t i = lane; i < entries; i += TPG) {
-        const int64_t p = i / cpg;
-        const int c = c0 + (int)(i - p * cpg);
-        const float w = gn_param<T>(a.weight, a.ptype, c, 1.f);
-        const int64_t j = (sample * parts + p) * padded + c;
-        s2 = fmaf(w, __ldcg(in + j), s2);
-        s1 = fmaf(w, __ldcg(in + sets * padded + j), s1);
-    }
+    gn_entries<TPG>(lane, parts, cpg, [&](int p, int c) {
+        const float w = gn_param<T>(a.weight, a.ptype, c0 + c, 1.f);
+        const float *const at = from + p * padded + c;
+        s2 = fmaf(w, __ldcg(at), s2);
+        s1 = fmaf(w, __ldcg(at + sets * padded), s1);
+    });
     s1 = gn_team_sum<TPG>(s1, sm);
     s2 = gn_team_sum<TPG>(s2, sm);
     if (lane == 0) {
@@ -725,7 +775,7 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
     k_gn_apply_bwd(const GnBackward a, const GnTile tile, const float *__restrict__ stat)
 {
     using V = Gv<T, AB>;
-    constexpr int NE = V::NE, NP = V::NP;
+    constexpr int NE = V::NE, NP = V::NP, U = gn_batch<AB, 2>();
     wait_for_prior_grid();
     allow_dependent_launch();
     const GnPlace q = gn_place<NE>(tile, a.n.positions);
@@ -744,20 +794,33 @@ __global__ void __launch_bounds__(FC_GN_BLOCK)
     to.k1.load(g0, off, cpg, [&](int g) { return -__ldcg(st + 2 * g); });
     to.k2.load(g0, off, cpg, [&](int g) { return -__ldcg(st + 2 * g + 1); });
     to.scale(ch.rstd);
-    const T *x = static_cast<const T *>(a.x.p) + q.n * a.x.ss + q.c0;
-    const T *dy = static_cast<const T *>(a.dy.p) + q.n * a.dy.ss + q.c0;
-    T *dx = static_cast<T *>(const_cast<void *>(a.dx.p)) + q.n * a.dx.ss + q.c0;
-#pragma unroll 2
-    for (int64_t row = q.first + q.r; row < q.end; row += q.R) {
-        F2 f[NP], g[NP], h[NP], dz[NP];
-        V::get(__ldcs(reinterpret_cast<const typename V::Raw *>(x + row * a.x.ld)), f);
-        V::get(__ldcs(reinterpret_cast<const typename V::Raw *>(dy + row * a.dy.ld)), g);
-        ch.template at<ACT>(f, g, h, dz, [&] {
-            return GnSource{x + row * a.x.ld, a.mean + at + g0, a.rstd + at + g0, 1, off, cpg,
-                            a.weight, a.bias, a.ptype, q.c0};
-        });
-        to.dx(h, ch.rw, dz);
-        __stcs(reinterpret_cast<typename V::Raw *>(dx + row * a.dx.ld), V::put(dz));
+    const int64_t row = q.first + q.r, sx = q.R * a.x.ld, sy = q.R * a.dy.ld, sd = q.R * a.dx.ld;
+    const T *x = static_cast<const T *>(a.x.p) + q.n * a.x.ss + row * a.x.ld + q.c0;
+    const T *dy = static_cast<const T *>(a.dy.p) + q.n * a.dy.ss + row * a.dy.ld + q.c0;
+    T *dx = static_cast<T *>(const_cast<void *>(a.dx.p)) + q.n * a.dx.ss + row * a.dx.ld + q.c0;
+    for (int64_t left = row < q.end ? (q.end - row + q.R - 1) / q.R : 0; left > 0;
+         left -= U, x += U * sx, dy += U * sy, dx += U * sd) {
+        typename V::Raw rx[U], ry[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u < left) {
+                rx[u] = __ldcs(reinterpret_cast<const typename V::Raw *>(x + u * sx));
+                ry[u] = __ldcs(reinterpret_cast<const typename V::Raw *>(dy + u * sy));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u >= left) break;
+            F2 f[NP], g[NP], h[NP], dz[NP];
+            V::get(rx[u], f);
+            V::get(ry[u], g);
+            ch.template at<ACT>(f, g, h, dz, [&] {
+                return GnSource{x + u * sx, a.mean + at + g0, a.rstd + at + g0, 1, off, cpg,
+                                a.weight, a.bias, a.ptype, q.c0};
+            });
+            to.dx(h, ch.rw, dz);
+            __stcs(reinterpret_cast<typename V::Raw *>(dx + u * sd), V::put(dz));
+        }
     }
 }
 

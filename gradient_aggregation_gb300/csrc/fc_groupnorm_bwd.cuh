@@ -34,7 +34,7 @@ cudaError_t gn_backward_streaming(const GnBackward &a, cudaStream_t s)
         e = launch_after_prior(k_gn_finish_sums<T, 32>, (unsigned)((groups + 7) / 8), 256, 0, s, a,
                                t.parts, part, used, stat);
     else
-        e = launch_after_prior(k_gn_finish_sums<T, 256>, (unsigned)groups, 256, 0, s, a, t.parts,
+        e = launch_after_prior(k_gn_finish_sums<T, 1024>, (unsigned)groups, 1024, 0, s, a, t.parts,
                                part, used, stat);
     if (e != cudaSuccess) return e;
     e = launch_after_prior(k_gn_apply_bwd<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);
@@ -65,8 +65,9 @@ cudaError_t gn_backward_groups(const GnBackward &a, cudaStream_t s)
     if constexpr (AB == 16) {
         if (cpg % (NE / 2) == 0) return gn_backward_one<T, AB / 2, ACT, true>(a, s);
         return gn_backward_one<T, AB / 2, ACT, false>(a, s);
+    } else {
+        return gn_backward_one<T, AB, ACT, NE == 1>(a, s);  // a vector of one lies in one group
     }
-    return gn_backward_one<T, AB, ACT, NE == 1>(a, s);  // a vector of one lies in one group
 }
 
 template <class T, int AB>

@@ -20,7 +20,7 @@ cudaError_t gn_forward_streaming(const GnForward &a, cudaStream_t s)
         e = launch_after_prior(k_gn_finish<32>, (unsigned)((groups + 7) / 8), 256, 0, s, a.n, t.parts,
                                t.rows, part, sets, a.eps, stat, a.mean, a.rstd);
     else
-        e = launch_after_prior(k_gn_finish<256>, (unsigned)groups, 256, 0, s, a.n, t.parts, t.rows,
+        e = launch_after_prior(k_gn_finish<1024>, (unsigned)groups, 1024, 0, s, a.n, t.parts, t.rows,
                                part, sets, a.eps, stat, a.mean, a.rstd);
     if (e != cudaSuccess) return e;
     return launch_after_prior(k_gn_apply<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);

@@ -38,9 +38,11 @@ struct GnPlan {
 // Where a thread of a resident kernel stands.
 struct GnSpot {
     int rank, v, r;      // block of the cluster; vector and row of the thread
+    int slab, gs;        // the block's slab, its groups (the last slab may have fewer)
     int g0, off;         // group of the vector's first channel, its place there
     int have, rows;      // the block's positions, the thread's
     int64_t row;         // the thread's first position
+    int first;           // the cluster's first sample
     bool on;
 };
 
@@ -51,7 +53,11 @@ __device__ __forceinline__ GnSpot gn_spot(const GnPlan &p, const GnShape &n)
     s.rank = (int)blockIdx.x & (p.K - 1);
     s.r = (int)threadIdx.x * p.divv >> 20;
     s.v = (int)threadIdx.x - s.r * p.V;
-    s.on = s.r < p.R;
+    const int cluster = (int)(blockIdx.x >> p.logk);
+    s.first = cluster / p.nslab;
+    s.slab = cluster - s.first * p.nslab;
+    s.gs = min(p.gs, n.groups - s.slab * p.gs);
+    s.on = s.r < p.R && s.v * NE < s.gs * p.cpg;
     if (ONE) {
         s.g0 = s.v * p.divn >> 20;
         s.off = 0;
@@ -194,8 +200,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = T_ >> 5;
     const int half = min((p.iters + 1) >> 1, s.rows);
     const GnWalk x = gn_walk<T, NE>(a.x, s, p), y = gn_walk<T, NE>(a.y, s, p);
-    const int cluster = (int)(blockIdx.x >> p.logk);
-    const int q0 = cluster / p.nslab, slab = cluster - q0 * p.nslab, c0 = slab * p.sc;
+    const int q0 = s.first, c0 = s.slab * p.sc;
     const int base = s.have / p.R, rest = s.have - base * p.R;  // threads r >= rest: base rows
     const float have = (float)s.rows, inv = s.rows > 0 ? 1.f / have : 0.f;
     const float block = s.have > 0 ? 1.f / (float)(s.have * p.cpg) : 0.f, all = 1.f / p.total;
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT)
             });
         }
         __syncthreads();
-        for (int k = warp; k < p.gs; k += warps) {
+        for (int k = warp; k < s.gs; k += warps) {
             float t = 0.f, q = 0.f;
             gn_values<NE, ONE>(p, k, [&](int at, int e, int r) {
                 t = fmaf((float)((base + (r < rest)) * e), s_mean[at], t);
@@ -285,8 +290,8 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT)
         }
         gn_block_or_cluster_sync(p.K);
         // a lane for each block of the cluster
-        for (int k = threadIdx.x; k < (((p.gs << p.logk) + 31) & ~31); k += T_) {
-            const int at = min(k >> p.logk, p.gs - 1), j = k & (p.K - 1);
+        for (int k = threadIdx.x; k < (((s.gs << p.logk) + 31) & ~31); k += T_) {
+            const int at = min(k >> p.logk, s.gs - 1), j = k & (p.K - 1);
             float m, q;
             if (p.K > 1) {
                 const float bm = ld_cluster_f32(g + at, j), bq = ld_cluster_f32(g + p.gs + at, j);
@@ -298,12 +303,12 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT)
                 m = g[at];
                 q = g[p.gs + at];
             }
-            if (j == 0 && k >> p.logk < p.gs) {
+            if (j == 0 && k >> p.logk < s.gs) {
                 const float r = 1.f / sqrtf(q * all + a.eps);
                 g[2 * p.gs + at] = -m;
                 g[3 * p.gs + at] = r;
                 if (s.rank == 0 && a.mean) {
-                    const int64_t to = (int64_t)n * a.n.groups + slab * p.gs + at;
+                    const int64_t to = (int64_t)n * a.n.groups + s.slab * p.gs + at;
                     a.mean[to] = m;
                     a.rstd[to] = r;
                 }
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT)
 template <class T, int NE>
 __device__ __forceinline__ void gn_leave_sums(const GnBackward &a, const GnPlan &p, const GnSpot &s,
                                               float *all, const F2 (&th)[(NE + 1) / 2],
-                                              const F2 (&td)[(NE + 1) / 2], int slab, int set)
+                                              const F2 (&td)[(NE + 1) / 2])
 {
     const int T_ = (int)blockDim.x, plane = p.R * p.sc;
     float *const some = all + 2 * plane;
@@ -398,8 +403,9 @@ __device__ __forceinline__ void gn_leave_sums(const GnBackward &a, const GnPlan 
         } else {
             v = sums[j];
         }
-        const int which = j >= p.sc;
-        a.ws[(which * p.per + set) * padded + slab * p.sc + j - which * p.sc] = v;
+        const int which = j >= p.sc, c = j - which * p.sc;
+        if (c < s.gs * p.cpg)
+            a.ws[(which * p.per + s.first) * padded + s.slab * p.sc + c] = v;
     }
     if (p.K > 1) cluster_sync();  // no block leaves while another reads its sums
 }
@@ -423,8 +429,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
     const int half = min((p.iters + 1) >> 1, s.rows);
     const GnWalk x = gn_walk<T, NE>(a.x, s, p), dy = gn_walk<T, NE>(a.dy, s, p);
     const GnWalk dx = gn_walk<T, NE>(a.dx, s, p);
-    const int cluster = (int)(blockIdx.x >> p.logk);
-    const int q0 = cluster / p.nslab, slab = cluster - q0 * p.nslab, c0 = slab * p.sc;
+    const int q0 = s.first, c0 = s.slab * p.sc;
     const float inv = -1.f / p.total;
     wait_for_prior_grid();
     allow_dependent_launch();
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
     };
     auto copy_stats = [&](int n, float *to) {
         if (!s.on) return;
-        const int64_t at = (int64_t)n * a.n.groups + slab * p.gs + s.g0;
+        const int64_t at = (int64_t)n * a.n.groups + s.slab * p.gs + s.g0;
         gn_pieces<NE, ONE>(s.off, p.cpg, [&](int j, int, int) {
             gn_copy<4>(reinterpret_cast<char *>(to + 2 * j * T_),
                        reinterpret_cast<const char *>(a.mean + at + j));
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
             });
         }
         __syncthreads();
-        for (int k = warp; k < p.gs; k += warps) {
+        for (int k = warp; k < s.gs; k += warps) {
             float x1 = 0.f, x2 = 0.f;
             gn_values<NE, ONE>(p, k, [&](int at, int, int) {
                 x1 += s_1[at];
@@ -524,8 +529,8 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
         }
         gn_block_or_cluster_sync(p.K);
         // a lane for each block of the cluster
-        for (int k = threadIdx.x; k < (((p.gs << p.logk) + 31) & ~31); k += T_) {
-            const int at = min(k >> p.logk, p.gs - 1), j = k & (p.K - 1);
+        for (int k = threadIdx.x; k < (((s.gs << p.logk) + 31) & ~31); k += T_) {
+            const int at = min(k >> p.logk, s.gs - 1), j = k & (p.K - 1);
             float x1, x2;
             if (p.K > 1) {
                 x1 = gn_blocks_sum(ld_cluster_f32(g + at, j), p.K);
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
                 x1 = g[at];
                 x2 = g[p.gs + at];
             }
-            if (j == 0 && k >> p.logk < p.gs) {
+            if (j == 0 && k >> p.logk < s.gs) {
                 g[2 * p.gs + at] = x1 * inv;
                 g[3 * p.gs + at] = x2 * inv;
             }
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
         ahead_own = used;
     }
     if (a.dweight || a.dbias)
-        gn_leave_sums<T, NE>(a, p, s, reinterpret_cast<float *>(dyn), th, td, slab, q0);
+        gn_leave_sums<T, NE>(a, p, s, reinterpret_cast<float *>(dyn), th, td);
 }
 
 // ---- host ------------------------------------------------------------------------------------
