@@ -20,11 +20,13 @@ extern template cudaError_t gn_backward<__half>(const GnBackward &, int, cudaStr
 extern template cudaError_t gn_backward<__nv_bfloat16>(const GnBackward &, int, cudaStream_t);
 
 // Whether a call may stream, whatever its type and alignment: not where the group of a
-// sample fits a cluster of any kind (see gn_plan) for two tensors of 4 bytes.
+// sample fits a cluster of any kind (see find_plan) for two tensors of 4 bytes, unless the
+// images are large enough for streaming to be the faster.
 bool gn_may_stream(const GnShape &n)
 {
-    const int cpg = n.channels / n.groups;
-    return cpg > 256 || n.positions * cpg > 1 << 16;
+    const int64_t cpg = n.channels / n.groups;
+    return cpg > 256 || n.positions * cpg > 1 << 16 ||
+           (n.positions >= 64 && n.samples * n.positions * n.channels >= 1 << 22);
 }
 
 // As many parts as make 1024 blocks over the samples, of 16 positions or more and of 4096
@@ -38,12 +40,13 @@ int64_t gn_parts(const GnShape &n)
     return (n.positions + rows - 1) / rows;
 }
 
-// Streaming leaves one for each part, the resident kernels one for each cluster that
-// works on a slab's samples: no more than samples.
+// Streaming leaves one for each part, and one for each sample that has several; the
+// resident kernels one for each cluster that works on a slab's samples: no more than samples.
 int64_t gn_sets(const GnShape &n)
 {
     const int64_t held = std::min<int64_t>(n.samples, FC_GN_SETS);
-    return gn_may_stream(n) ? std::max(n.samples * gn_parts(n), held) : held;
+    const int64_t parts = gn_parts(n);
+    return gn_may_stream(n) ? n.samples * (parts + (parts > 1)) : held;
 }
 
 namespace {
@@ -197,6 +200,14 @@ bool find_plan(const GnShape &n, int ab, int ne, int tensors, const void *kernel
         }
     }
     if (best == 1e30) return false;
+    // Long maps at less than 16 bytes an access: a round of one block an SM takes 1.1 to 5
+    // times as long as reckoned above, and streaming, which has no rounds, 2.5 to 5 times the
+    // floor and 18 us at the least.  8 x 16427 x 384 bf16 at an odd pitch, backward: 640 us held
+    // in shared memory, 233 streamed; 10 x 11404 x 480 in groups of 30: 314 and 150; the other
+    // way round 40 x 1352 x 211 in 211 groups, forward: 27 and 32.
+    const double bytes = (double)n.samples * n.positions * n.channels * (ab / ne) * (tensors + 1);
+    const double floors = ab == 2 ? (tensors == 2 ? 4.5 : 4) : 3.1;
+    if (ab < 16 && gn_may_stream(n) && 1.7 * best > 18 + floors * bytes / 6.8e6) return false;
     for (p.logk = 0; 1 << p.logk < p.K;) ++p.logk;
     p.divv = ((1 << 20) + p.V - 1) / p.V;
     const int held = looked_up({kernel, dev, p.K, p.threads, (int)p.smem}, [&] {
@@ -254,7 +265,7 @@ cudaError_t launch_gn_forward(const GnForward &a, int type, int act, cudaStream_
 
 cudaError_t launch_gn_backward(const GnBackward &a, int type, int act, cudaStream_t s)
 {
-    if (a.n.samples == 0) return gn_join(a, 0, s);
+    if (a.n.samples == 0) return gn_join(a, a.ws, 0, s);
     if (type == FC_TYPE_F32) return gn_backward<float>(a, act, s);
     if (type == FC_TYPE_F16) return gn_backward<__half>(a, act, s);
     return gn_backward<__nv_bfloat16>(a, act, s);

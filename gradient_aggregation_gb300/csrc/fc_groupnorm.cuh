@@ -360,8 +360,8 @@ struct GnTile {
 #define FC_GN_RUN 64  // rows between two fresh pivots, a multiple of any batch
 
 // Rows whose loads a thread has in flight at a time: up to 64 bytes, of two tensors 32
-// each; narrow vectors are bound by the wait for them (8 x 16427 x 384 bf16 at an odd
-// pitch, backward: 658 us two at a time).
+// each.  A store of the row before, which may be to where the next is read from, holds a
+// load up otherwise (4 x 45956 x 182 fp32 in 2 groups, backward: 339 us row by row, 150 now).
 template <int AB, int TENSORS>
 constexpr int gn_batch()
 {
@@ -507,6 +507,82 @@ __device__ __forceinline__ float gn_team_sum(float v, float *sm)
         for (int i = 0; i < TPG / 32; ++i) v += sm[i];
     }
     return v;
+}
+
+// Where the parts of a group are many, a first step joins them channel by channel into
+// one set a sample, 8 threads a channel: a group's own threads alone took 40 us for 318
+// parts of 268 channels.
+#define FC_GN_ENTRIES 4096  // parts times channels of a group that its threads join alone
+
+// Over the block's 8 warps, lane by lane.
+static __device__ __forceinline__ float gn_sum_warps(float (&sm)[8][32], float v)
+{
+    const int c = threadIdx.x & 31;
+    __syncthreads();
+    sm[threadIdx.x >> 5][c] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += sm[k][c];
+    return v;
+}
+
+// SQUARES: of means and sums of squares about them, else of two sums.  Sets of both values
+// are `sets` apart in `in`, `samples` in `out`.
+template <bool SQUARES>
+__global__ void __launch_bounds__(256)
+    k_gn_join_parts(const GnShape n, const int parts, const int64_t part_rows,
+                    const float *__restrict__ in, const int64_t sets, float *__restrict__ out)
+{
+    __shared__ float sm[8][32];
+    wait_for_prior_grid();
+    allow_dependent_launch();
+    const int64_t padded = (n.channels + 7) & ~7;
+    const int strips = (n.channels + 31) / 32, r = threadIdx.x >> 5;
+    const int64_t sample = blockIdx.x / strips;
+    const int c = (int)(blockIdx.x - sample * strips) * 32 + (threadIdx.x & 31);
+    const bool on = c < n.channels;
+    const float *const from = in + sample * parts * padded + c;
+    const float last = (float)(n.positions - (parts - 1) * part_rows);
+    float u = 0.f, v = 0.f;
+    if (on) {
+#pragma unroll 4
+        for (int p = r; p < parts; p += 8) {
+            const float *const at = from + p * padded;
+            if (SQUARES) {
+                u = fmaf(p < parts - 1 ? (float)part_rows : last, __ldcg(at), u);
+            } else {
+                u += __ldcg(at);
+                v += __ldcg(at + sets * padded);
+            }
+        }
+    }
+    u = gn_sum_warps(sm, u);
+    if (SQUARES) {
+        u /= (float)n.positions;
+        if (on) {
+#pragma unroll 4
+            for (int p = r; p < parts; p += 8) {
+                const float *const at = from + p * padded;
+                const float d = __ldcg(at) - u;
+                v += fmaf((p < parts - 1 ? (float)part_rows : last) * d, d,
+                          __ldcg(at + sets * padded));
+            }
+        }
+    }
+    v = gn_sum_warps(sm, v);
+    if (on && r == 0) {
+        out[sample * padded + c] = u;
+        out[(n.samples + sample) * padded + c] = v;
+    }
+}
+
+inline cudaError_t gn_join_parts(bool squares, const GnShape &n, const GnTile &t, const float *in,
+                                 int64_t sets, float *out, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)(n.samples * ((n.channels + 31) / 32));
+    return launch_after_prior(squares ? k_gn_join_parts<true> : k_gn_join_parts<false>, grid, 256, 0,
+                              s, n, t.parts, t.rows, in, sets, out);
 }
 
 // Calls f(part, channel) for a thread's share of a group's parts and channels, TPG side by

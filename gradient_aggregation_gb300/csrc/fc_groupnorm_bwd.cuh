@@ -7,7 +7,7 @@
 namespace fc {
 
 // dweight and dbias from `sets` sets of the channels' sums, as layer norm joins its own.
-inline cudaError_t gn_join(const GnBackward &a, int64_t sets, cudaStream_t s)
+inline cudaError_t gn_join(const GnBackward &a, const float *in, int64_t sets, cudaStream_t s)
 {
     if (!a.dweight && !a.dbias) return cudaSuccess;
     LnBackward l = {};
@@ -15,7 +15,7 @@ inline cudaError_t gn_join(const GnBackward &a, int64_t sets, cudaStream_t s)
     l.dweight = a.dweight;
     l.dbias = a.dbias;
     l.gtype = a.gtype;
-    l.partials = a.ws;
+    l.partials = const_cast<float *>(in);
     return ln_join(l, (int)sets, s);
 }
 
@@ -23,23 +23,33 @@ template <class T, int AB, int ACT>
 cudaError_t gn_backward_streaming(const GnBackward &a, cudaStream_t s)
 {
     const GnTile t = gn_tile(a.n, Gv<T, AB>::NE);
-    const int64_t sets = gn_sets(a.n), used = a.n.samples * t.parts;
     const unsigned grid = gn_grid(a.n, t);
-    float *const part = a.ws, *const stat = a.ws + 2 * sets * gn_padded(a.n.channels);
+    float *part = a.ws, *const stat = a.ws + 2 * gn_sets(a.n) * gn_padded(a.n.channels);
+    int64_t sets = a.n.samples * t.parts;
+    int parts = t.parts;
     cudaError_t e = launch_after_prior(k_gn_sums<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, part,
-                                       used);
+                                       sets);
     if (e != cudaSuccess) return e;
     const int64_t groups = a.n.samples * a.n.groups;
-    if ((int64_t)t.parts * (a.n.channels / a.n.groups) <= 1024)
+    const int cpg = a.n.channels / a.n.groups;
+    if ((int64_t)parts * cpg > FC_GN_ENTRIES && parts > 1) {
+        float *const joined = part + 2 * sets * gn_padded(a.n.channels);
+        e = gn_join_parts(false, a.n, t, part, sets, joined, s);
+        if (e != cudaSuccess) return e;
+        part = joined;
+        sets = a.n.samples;
+        parts = 1;
+    }
+    if ((int64_t)parts * cpg <= 1024)
         e = launch_after_prior(k_gn_finish_sums<T, 32>, (unsigned)((groups + 7) / 8), 256, 0, s, a,
-                               t.parts, part, used, stat);
+                               parts, part, sets, stat);
     else
-        e = launch_after_prior(k_gn_finish_sums<T, 1024>, (unsigned)groups, 1024, 0, s, a, t.parts,
-                               part, used, stat);
+        e = launch_after_prior(k_gn_finish_sums<T, 1024>, (unsigned)groups, 1024, 0, s, a, parts,
+                               part, sets, stat);
     if (e != cudaSuccess) return e;
     e = launch_after_prior(k_gn_apply_bwd<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);
     if (e != cudaSuccess) return e;
-    return gn_join(a, used, s);
+    return gn_join(a, part, sets, s);
 }
 
 template <class T, int AB, int ACT, bool ONE>
@@ -51,7 +61,7 @@ cudaError_t gn_backward_one(const GnBackward &a, cudaStream_t s)
         return gn_backward_streaming<T, AB, ACT>(a, s);
     }
     const cudaError_t e = gn_launch(k_gn_bwd<T, AB, ACT, ONE>, a, p, s);
-    return e == cudaSuccess ? gn_join(a, p.per, s) : e;
+    return e == cudaSuccess ? gn_join(a, a.ws, p.per, s) : e;
 }
 
 // A thread holds five values a channel, and two or four more of each group that its

@@ -9,18 +9,29 @@ template <class T, int AB, int ACT>
 cudaError_t gn_forward_streaming(const GnForward &a, cudaStream_t s)
 {
     const GnTile t = gn_tile(a.n, Gv<T, AB>::NE);
-    const int64_t sets = gn_sets(a.n);
     const unsigned grid = gn_grid(a.n, t);
-    float *const part = a.ws, *const stat = a.ws + 2 * sets * gn_padded(a.n.channels);
+    float *part = a.ws, *const stat = a.ws + 2 * gn_sets(a.n) * gn_padded(a.n.channels);
+    int64_t sets = a.n.samples * t.parts, rows = t.rows;
+    int parts = t.parts;
     cudaError_t e = launch_after_prior(k_gn_stats<T, AB>, grid, FC_GN_BLOCK, 0, s, a.x, a.n, t, part,
                                        sets);
     if (e != cudaSuccess) return e;
     const int64_t groups = a.n.samples * a.n.groups;
-    if ((int64_t)t.parts * (a.n.channels / a.n.groups) <= 1024)
-        e = launch_after_prior(k_gn_finish<32>, (unsigned)((groups + 7) / 8), 256, 0, s, a.n, t.parts,
-                               t.rows, part, sets, a.eps, stat, a.mean, a.rstd);
+    const int cpg = a.n.channels / a.n.groups;
+    if ((int64_t)parts * cpg > FC_GN_ENTRIES && parts > 1) {
+        float *const joined = part + 2 * sets * gn_padded(a.n.channels);
+        e = gn_join_parts(true, a.n, t, part, sets, joined, s);
+        if (e != cudaSuccess) return e;
+        part = joined;
+        sets = a.n.samples;
+        parts = 1;
+        rows = a.n.positions;
+    }
+    if ((int64_t)parts * cpg <= 1024)
+        e = launch_after_prior(k_gn_finish<32>, (unsigned)((groups + 7) / 8), 256, 0, s, a.n, parts,
+                               rows, part, sets, a.eps, stat, a.mean, a.rstd);
     else
-        e = launch_after_prior(k_gn_finish<1024>, (unsigned)groups, 1024, 0, s, a.n, t.parts, t.rows,
+        e = launch_after_prior(k_gn_finish<1024>, (unsigned)groups, 1024, 0, s, a.n, parts, rows,
                                part, sets, a.eps, stat, a.mean, a.rstd);
     if (e != cudaSuccess) return e;
     return launch_after_prior(k_gn_apply<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);

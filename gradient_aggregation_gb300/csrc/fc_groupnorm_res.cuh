@@ -95,7 +95,7 @@ __device__ __forceinline__ void gn_copy(char *to, const char *from)
                          (uint32_t)__cvta_generic_to_shared(to)),
                      "l"(from)
                      : "memory");
-    else
+    else  // there on return: no asynchronous copy is as small
         *reinterpret_cast<unsigned short *>(to) = __ldcs(reinterpret_cast<const unsigned short *>(from));
 }
 
@@ -346,12 +346,14 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT)
                 }
                 if constexpr (decltype(ahead)::value) cp_async_commit();
             };
-            if (AB > 2 && more) {
+            if constexpr (AB == 2) {
+                put(0, s.rows, GnYes<false>());
+                if (more) copy(n + p.per, 0, s.rows);
+            } else if (more) {
                 put(0, half, GnYes<true>());
                 put(half, s.rows, GnYes<true>());
             } else {
                 put(0, s.rows, GnYes<false>());
-                if (more) copy(n + p.per, 0, s.rows);  // 2 bytes at a time
             }
         }
         if (p.K > 1) cluster_wait();
@@ -576,12 +578,14 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
                 }
                 if constexpr (decltype(ahead)::value) cp_async_commit();
             };
-            if (AB > 2 && more) {
+            if constexpr (AB == 2) {
+                put(0, s.rows, GnYes<false>());
+                if (more) copy(n + p.per, 0, s.rows);
+            } else if (more) {
                 put(0, half, GnYes<true>());
                 put(half, s.rows, GnYes<true>());
             } else {
                 put(0, s.rows, GnYes<false>());
-                if (more) copy(n + p.per, 0, s.rows);  // 2 bytes at a time
             }
         }
         if (p.K > 1) cluster_wait();

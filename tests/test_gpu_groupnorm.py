@@ -141,7 +141,8 @@ def test_long_maps(n, s, c, groups, lay, dtype):
     (40, 1352, 211, 211, dict(pad=24)), (3, 5139, 137, 137, {}), (5, 90, 83, 83, {}),
     (7, 400, 304, 19, {}), (2, 700, 176, 11, {}), (9, 333, 1112, 139, dict(pad=8)),
     (3, 129, 1982, 1, dict(pad=5)), (2, 468, 1122, 2, {}), (1, 17, 6000, 1, dict(shift=1)),
-    (2, 1200, 1072, 4, {})], ids=str)
+    (2, 1200, 1072, 4, {}), (2, 9001, 272, 1, {}), (4, 9001, 120, 4, {}),
+    (3, 7001, 210, 35, dict(pad=1))], ids=str)
 def test_uneven_slabs_and_wide_groups(n, s, c, groups, lay, dtype):
     check(n, s, c, groups, dtype, act=RELU if c % 2 else SILU, **lay)
 
