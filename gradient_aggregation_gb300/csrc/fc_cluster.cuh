@@ -32,14 +32,8 @@ __device__ __forceinline__ void cluster_sync()
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The two halves of cluster_sync, for work of a CTA's own between them.
-__device__ __forceinline__ void cluster_arrive()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-
-// An arrival that orders no writes: it says that what the CTA wanted to read it has
-// read.
+// The two halves of a barrier, for work of a CTA's own between them.  The arrival orders
+// no writes: it says that what the CTA wanted to read it has read.
 __device__ __forceinline__ void cluster_arrive_relaxed()
 {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");

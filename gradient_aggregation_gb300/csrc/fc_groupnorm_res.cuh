@@ -10,6 +10,11 @@
 // memory.  A cluster goes from sample to sample; a slot whose result is on its way takes
 // the next sample's vector, and several blocks to an SM keep loads, arithmetic and
 // stores of different samples going side by side.
+//
+// 64 x 4096 x 512 bf16 with SiLU: 108 us forward (floor 79) and 212 backward (118); read two
+// and three times over, without holding the maps, 245 and 380.  A copy through the same
+// slots takes 97 us, so the forward pass is bound by how many bytes they keep in flight; the
+// backward pass, at 16 warps an SM, by the wait of those few warps for one another.
 #pragma once
 
 #include "fc_groupnorm.cuh"

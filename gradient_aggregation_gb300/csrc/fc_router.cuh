@@ -10,8 +10,12 @@
 // over the warp for each of them.  Instead the lanes leave the largest of every group in
 // shared memory, and then each lane chooses for a row of its own: the largest of the
 // groups' largest, that group's elements once more (from L1 or L2), the largest that is
-// left of them; 32 rows at a time.  At 256 experts and k = 8 that is 30 instructions of
-// a warp a row, beside 60 for the softmax; a choice by warp reductions took 500.
+// left of them; 32 rows at a time.  A row of 256 experts takes 147 instructions of a warp
+// with k = 8 and 115 with k = 1.
+//
+// 131072 x 256 bf16, k = 8: 40 us forward, 36 backward (by warp reductions 148 and 68); the
+// bytes alone take 11 and 22.  Bound by instructions and the wait for loads: they issue in
+// 0.55 to 0.6 of the cycles.  64 x 256: 9 us, three trips to memory and a cluster's start.
 #pragma once
 
 #include <algorithm>
