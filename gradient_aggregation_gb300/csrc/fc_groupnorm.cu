@@ -203,7 +203,7 @@ bool find_plan(const GnShape &n, int ab, int ne, int tensors, const void *kernel
     // Long maps at less than 16 bytes an access: a round of one block an SM takes 1.1 to 5
     // times as long as reckoned above, and streaming, which has no rounds, 2.5 to 5 times the
     // floor and 18 us at the least.  8 x 16427 x 384 bf16 at an odd pitch, backward: 640 us held
-    // in shared memory, 233 streamed; 10 x 11404 x 480 in groups of 30: 314 and 150; the other
+    // in shared memory, 233 streamed; 10 x 11404 x 480 in groups of 30: 314 and 137; the other
     // way round 40 x 1352 x 211 in 211 groups, forward: 27 and 32.
     const double bytes = (double)n.samples * n.positions * n.channels * (ab / ne) * (tensors + 1);
     const double floors = ab == 2 ? (tensors == 2 ? 4.5 : 4) : 3.1;

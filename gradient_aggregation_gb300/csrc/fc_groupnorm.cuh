@@ -361,7 +361,7 @@ struct GnTile {
 
 // Rows whose loads a thread has in flight at a time: up to 64 bytes, of two tensors 32
 // each.  A store of the row before, which may be to where the next is read from, holds a
-// load up otherwise (4 x 45956 x 182 fp32 in 2 groups, backward: 339 us row by row, 150 now).
+// load up otherwise (4 x 45956 x 182 fp32 in 2 groups, backward: 339 us row by row, 147 now).
 template <int AB, int TENSORS>
 constexpr int gn_batch()
 {
@@ -715,9 +715,19 @@ struct GnChannels {
     }
 };
 
+// Blocks of an SM that the streaming backward pass's registers are held to.  A fourth is
+// worth more than registers beyond 64 (190 x 1092 x 167 bf16: 163 us without it, 134 with;
+// 10 x 11404 x 480: 151 and 137; against that 8 x 10830 x 304 fp32: 117 and 121), but not
+// with the ReLU's call out of line (8 x 16427 x 384 bf16 at an odd pitch: three 233, four 274).
+template <int AB, int ACT>
+__host__ __device__ constexpr int gn_blocks_bwd()
+{
+    return AB == 16 ? 2 : ACT == FC_ACT_RELU ? 3 : 4;
+}
+
 // Per channel of a part: the sums of dz h and of dz.
 template <class T, int AB, int ACT>
-__global__ void __launch_bounds__(FC_GN_BLOCK)
+__global__ void __launch_bounds__(FC_GN_BLOCK, gn_blocks_bwd<AB, ACT>())
     k_gn_sums(const GnBackward a, const GnTile tile, float *__restrict__ out, const int64_t sets)
 {
     using V = Gv<T, AB>;
@@ -847,7 +857,7 @@ struct GnSlope {
 };
 
 template <class T, int AB, int ACT>
-__global__ void __launch_bounds__(FC_GN_BLOCK)
+__global__ void __launch_bounds__(FC_GN_BLOCK, gn_blocks_bwd<AB, ACT>())
     k_gn_apply_bwd(const GnBackward a, const GnTile tile, const float *__restrict__ stat)
 {
     using V = Gv<T, AB>;
