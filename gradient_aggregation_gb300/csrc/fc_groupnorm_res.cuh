@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
     for (int n = q0;; n += p.per) {
         F2 w[NP];  // needed up to the groups' sums only: not worth registers beyond
         if (s.on) gn_params<T, NE>(a.weight, a.ptype, c0 + s.v * NE, 1.f, w);
-        cp_async_wait<1>();
+        cp_async_wait<1>();  // of the sample's two groups the first: its statistics, half its rows
         if (s.on) {
             ch.mean.load(0, s.off, p.cpg, [&](int k) { return own[2 * k * T_]; });
             ch.rstd.load(0, s.off, p.cpg, [&](int k) { return own[(2 * k + 1) * T_]; });
@@ -585,7 +585,10 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
             };
             if constexpr (AB == 2) {
                 put(0, s.rows, GnYes<false>());
-                if (more) copy(n + p.per, 0, s.rows);
+                if (more) {  // the statistics are in the first of two groups here too
+                    copy(n + p.per, 0, half);
+                    copy(n + p.per, half, s.rows);
+                }
             } else if (more) {
                 put(0, half, GnYes<true>());
                 put(half, s.rows, GnYes<true>());

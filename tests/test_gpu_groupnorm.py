@@ -153,6 +153,18 @@ def test_many_samples(dtype):
     check(3000, 1, 32, 2, dtype, act=RELU)
 
 
+# 16-bit rows of any alignment, several samples to a cluster, rows of threads without a
+# position: what a sample's threads need of the next one has to be there when they read it
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("act", [NONE, RELU, SILU])
+@pytest.mark.parametrize("n,s,c,groups,lay", [
+    (700, 20, 33, 3, {}), (700, 20, 63, 7, {}), (3000, 2, 33, 3, {}), (3000, 1, 33, 3, {}),
+    (5000, 3, 7, 1, {}), (700, 20, 64, 8, dict(pad=1)), (3000, 1, 32, 2, dict(shift=1, gap=3))],
+    ids=str)
+def test_many_samples_at_odd_places(n, s, c, groups, lay, act, dtype):
+    check(n, s, c, groups, dtype, act=act, **lay)
+
+
 @pytest.mark.parametrize("gtype", TYPES, ids=ids)
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 def test_gradient_types(dtype, gtype):
