@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                // one shift for all of a row, whatever its rounding, leaves the quotients
+                // one shift for all of a row, whatever its rounding, leaves the quotients: the
+                // chosen ones' terms are formed with it as well, below
                 const float shift = -top[u] * kRtLog2e;
                 F2 acc = f2(0.f, 0.f);
 #pragma unroll
@@ -469,6 +470,10 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
             Word *const mine = words + lane * stride;
             const bool routes = !(st.y < 0.f);
             const float scale = 1.f / st.y;
+            // a term as the row's total has it, bit for bit: ex2(x log2e + shift), or from the
+            // difference (value - 0 and + 0 round nothing)
+            const bool apart = !(fabsf(st.x) < 1e38f);
+            const float less = apart ? st.x : 0.f, shift = apart ? 0.f : -st.x * kRtLog2e;
             float chosen_sum = 0.f;
             int j = 0;
             if (routes) {
@@ -526,7 +531,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                     const bool again = same & (same - 1);
                     mine[g] = RtWord<T>::make(again ? value : left, g,
                                               again ? taken | 1u << at_e : 0);
-                    const float p = rt_ex2((value - st.x) * kRtLog2e);
+                    const float p = rt_ex2(fmaf(value - less, kRtLog2e, shift));
                     chosen_sum += p;
                     chosen[lane * k + j] = 8 * g + at_e;
                     weights[lane * k + j] = p;

@@ -182,6 +182,40 @@ def test_logits_far_from_zero(shift):
         check_backward(x, check_forward(x, 1, None, 3, True, False))
 
 
+def check_both_ways(x, k, sequences=1):
+    """Both passes, with weights normalised and as they are, balanced together and apart."""
+    rows = x.shape[0]
+    dw = torch.randn(rows, k, generator=torch.Generator("cuda").manual_seed(6), device="cuda")
+    dl = torch.tensor([2.0, 0.0], device="cuda")
+    for normalise in (False, True):
+        for per_sequence in (False, True):
+            o = check_forward(x, sequences, None, k, normalise, per_sequence)
+            dx = torch.empty_like(x)
+            fc.fc_router_backward(x, sequences, normalise, per_sequence, o["chosen"], o["weights"],
+                                  o["lse"], o["counts"], o["routed"], dw, dl, dx)
+            want, bound = ref.router_backward(x, sequences, k, normalise, per_sequence,
+                                              o["chosen"], o["weights"], o["lse"], o["counts"],
+                                              o["routed"], dw, dl)
+            assert_within("dlogits", dx, want, rounded(bound, want, x.dtype))
+
+
+# a softmax does not depend on what is added to all logits: neither do the weights' digits
+@pytest.mark.parametrize("shift", [0.0, 30.0, 100.0, 1e3, 1e4, 1e5, 1e6, 1e8, -100.0, -1e4, -1e8])
+def test_weights_of_logits_far_from_zero(shift):
+    for experts in (6, 40, 60, 200, 700):
+        x, _ = scores(60, experts, F32)
+        x.add_(shift)
+        check_both_ways(x, 4, 3)
+
+
+@pytest.mark.parametrize("dtype,shift", [(F16, 100.0), (F16, 3e4), (BF16, 100.0), (BF16, 5e4)])
+def test_weights_of_16_bit_logits_far_from_zero(dtype, shift):
+    for experts in (8, 60, 256):
+        x, _ = scores(60, experts, dtype, scale=shift / 30)
+        x.add_(shift)
+        check_both_ways(x, 4, 3)
+
+
 # ties, and zeros of both signs
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 def test_ties_go_to_the_lowest_expert(dtype):
