@@ -33,7 +33,8 @@ namespace fc {
 
 #define FC_ROUTER_WARPS 4   // of a block at most: of small blocks an SM takes nearly as many as another
 #define FC_ROUTER_JOIN 8    // blocks of a cluster
-#define FC_ROUTER_FAR 16.f
+#define FC_ROUTER_FAR 16.f  // |lse| from which on the backward pass takes differences first
+#define FC_ROUTER_APART 65536.f  // the largest logit's size from which on the forward pass does
 
 constexpr float kRtLog2e = 1.44269504f;
 
@@ -381,12 +382,13 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                         to[LPR * v] = RtWord<T>::make(most, q + LPR * v, 0);
                 }
                 top[u] = rt_row_max<LPR>(top[u]);
-                odd |= !(fabsf(top[u]) < 1e38f);
+                odd |= !(fabsf(top[u]) < FC_ROUTER_APART);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                // one shift for all of a row, whatever its rounding, leaves the quotients: the
-                // chosen ones' terms are formed with it as well, below
+                // one shift for all of a row: its rounding, of 2^-8 at most here, is a factor of all
+                // terms and leaves their quotients (the chosen ones' terms are formed with it
+                // as well, below), and of the lse it is a rounding
                 const float shift = -top[u] * kRtLog2e;
                 F2 acc = f2(0.f, 0.f);
 #pragma unroll
@@ -410,12 +412,12 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                 }
             }
             if (__any_sync(0xffffffffu, odd)) {
-                // rows closed to all experts, or with numbers whose product overflows: those
-                // once more, the difference first
+                // rows closed to all experts, or with numbers whose shift would be rounded by
+                // more (a factor that fp32 may not hold): those once more, the difference first
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const bool live = routes >> u & 1, closed = !(top[u] > -INFINITY);
-                    const bool again = !(fabsf(top[u]) < 1e38f);  // the others keep their bits
+                    const bool again = !(fabsf(top[u]) < FC_ROUTER_APART);  // the others keep their bits
                     bool nan = false;
                     F2 acc = f2(0.f, 0.f);
 #pragma unroll
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
             const float scale = 1.f / st.y;
             // a term as the row's total has it, bit for bit: ex2(x log2e + shift), or from the
             // difference (value - 0 and + 0 round nothing)
-            const bool apart = !(fabsf(st.x) < 1e38f);
+            const bool apart = !(fabsf(st.x) < FC_ROUTER_APART);
             const float less = apart ? st.x : 0.f, shift = apart ? 0.f : -st.x * kRtLog2e;
             float chosen_sum = 0.f;
             int j = 0;

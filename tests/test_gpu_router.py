@@ -208,6 +208,19 @@ def test_weights_of_logits_far_from_zero(shift):
         check_both_ways(x, 4, 3)
 
 
+# logits whose product with log2(e) rounds by more than fp32's exponents span
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=ids)
+@pytest.mark.parametrize("shift", [65536.0, 7e4, 3e9, 1e10, 1e15, 1e30, 9e37, -7e4, -1e10, -1e37])
+def test_logits_of_any_size(shift, dtype):
+    for experts in (6, 40, 60, 200, 700):
+        x, _ = scores(60, experts, dtype, scale=abs(shift) / 500)
+        x[::2] = scores(30, experts, dtype)[0]  # rows of either size side by side
+        x[1::2] += shift
+        x[3, 1:] = -INF
+        x[5] = shift
+        check_both_ways(x, 4, 3)
+
+
 @pytest.mark.parametrize("dtype,shift", [(F16, 100.0), (F16, 3e4), (BF16, 100.0), (BF16, 5e4)])
 def test_weights_of_16_bit_logits_far_from_zero(dtype, shift):
     for experts in (8, 60, 256):
