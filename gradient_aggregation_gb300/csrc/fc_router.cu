@@ -141,12 +141,6 @@ cudaError_t router_allow(const void *kernel)
     return cudaSuccess;
 }
 
-int64_t router_parts(int64_t sequences, int64_t tokens, int64_t groups)
-{
-    if (sequences * tokens == 0) return 1;
-    return std::min<int64_t>(sequences * tokens / groups, std::max<int64_t>(1, 1216 / groups));
-}
-
 size_t router_workspace(int64_t sequences, int64_t tokens, int64_t experts, int64_t groups)
 {
     const int64_t parts = router_parts(sequences, tokens, groups);

@@ -4,14 +4,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-namespace fc {
+#include "fc_router_cut.h"
 
-struct RouterShape {
-    int64_t sequences, tokens;  // rows = sequences * tokens
-    int experts, k;
-    int64_t groups;             // of rows that are balanced by themselves: 1 or sequences
-    bool normalise;
-};
+namespace fc {
 
 struct RouterForward {
     const void *logits;
@@ -39,7 +34,6 @@ struct RouterBackward {
 
 // The workspace: what each block of the first kernel leaves, then the groups' shares
 // of the losses, then a counter.
-int64_t router_parts(int64_t sequences, int64_t tokens, int64_t groups);  // most blocks a group
 size_t router_workspace(int64_t sequences, int64_t tokens, int64_t experts, int64_t groups);
 
 cudaError_t launch_router_forward(const RouterForward &a, int type, cudaStream_t s);
