@@ -532,15 +532,16 @@ fc_status fc_groupnorm_backward(const void *dy, int64_t lddy, int64_t sdy, const
     return launched(launch_gn_backward(a, type, act, (cudaStream_t)stream), "groupnorm launch");
 }
 
-static bool router_shape(int64_t sequences, int64_t tokens, int64_t experts)
+// The sums of the groups that are balanced by themselves are joined in blocks of 8 experts.
+static bool router_shape(int64_t sequences, int64_t tokens, int64_t experts, int32_t per_sequence)
 {
     return sequences >= 0 && tokens >= 0 && sequences <= INT32_MAX && tokens <= INT32_MAX &&
            sequences * tokens <= INT32_MAX && experts >= 1 && experts <= FC_MAX_EXPERTS &&
-           sequences * ((experts + 7) / 8) <= INT32_MAX;
+           (!per_sequence || sequences * ((experts + 7) / 8) <= INT32_MAX);
 }
 
 static fc_status check_router(int32_t type, int64_t sequences, int64_t tokens, int64_t experts,
-                              int32_t k)
+                              int32_t k, int32_t per_sequence)
 {
     TRY(check_type(type, "type"));
     if (experts > FC_MAX_EXPERTS)
@@ -548,7 +549,7 @@ static fc_status check_router(int32_t type, int64_t sequences, int64_t tokens, i
                     FC_MAX_EXPERTS);
     if (k > FC_MAX_CHOSEN)
         return fail(FC_ERR_LIMIT, "k = %d exceeds FC_MAX_CHOSEN = %d", k, FC_MAX_CHOSEN);
-    if (!router_shape(sequences, tokens, experts))
+    if (!router_shape(sequences, tokens, experts, per_sequence))
         return fail(FC_ERR_INVALID_ARG, "%lld sequences of %lld tokens over %lld experts: out of range",
                     (long long)sequences, (long long)tokens, (long long)experts);
     if (k < 1 || k > experts)
@@ -559,7 +560,7 @@ static fc_status check_router(int32_t type, int64_t sequences, int64_t tokens, i
 size_t fc_router_workspace_size(int64_t sequences, int64_t tokens, int64_t experts,
                                 int32_t per_sequence)
 {
-    if (!router_shape(sequences, tokens, experts)) return 0;
+    if (!router_shape(sequences, tokens, experts, per_sequence)) return 0;
     return router_workspace(sequences, tokens, experts, per_sequence ? sequences : 1);
 }
 
@@ -570,7 +571,7 @@ fc_status fc_router_forward(const void *logits, int64_t sequences, int64_t token
                             void *workspace, size_t workspace_bytes, void *stream)
 {
     TraceRange trace("fc_router_forward");
-    TRY(check_router(type, sequences, tokens, experts, k));
+    TRY(check_router(type, sequences, tokens, experts, k, per_sequence));
     const int64_t rows = sequences * tokens, groups = per_sequence ? sequences : 1;
     TRY(check_matrix(logits, "logits", type, rows, experts, ld));
     TRY(check_ptr(lengths, "lengths", 4, true));
@@ -601,7 +602,7 @@ fc_status fc_router_backward(const void *logits, int64_t sequences, int64_t toke
                              void *stream)
 {
     TraceRange trace("fc_router_backward");
-    TRY(check_router(type, sequences, tokens, experts, k));
+    TRY(check_router(type, sequences, tokens, experts, k, per_sequence));
     const int64_t rows = sequences * tokens, groups = per_sequence ? sequences : 1;
     TRY(check_matrix(logits, "logits", type, rows, experts, ld));
     TRY(check_matrix(dlogits, "dlogits", type, rows, experts, lddl));

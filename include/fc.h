@@ -730,7 +730,8 @@ FC_API size_t fc_router_workspace_size(int64_t sequences, int64_t tokens, int64_
  *  workspace  device, fc_router_workspace_size() bytes, 256-aligned; not shared by
  *             calls that may overlap on the GPU.
  * 1 <= k <= experts, k <= FC_MAX_CHOSEN, experts <= FC_MAX_EXPERTS, fewer than 2^31
- * rows.  Without rows the sums and the losses are 0. */
+ * rows, and with per_sequence fewer than 2^31 blocks of 8 experts over the sequences.
+ * Without rows the sums and the losses are 0. */
 FC_API fc_status fc_router_forward(const void *logits, int64_t sequences, int64_t tokens,
                                    int64_t experts, int64_t ld, int32_t type,
                                    const int32_t *lengths, int32_t k, int32_t normalise,

@@ -144,6 +144,17 @@ def test_router_workspace_sizes(fc_lib):
     assert size(0, 0, 8, True) > 0 and size(1, 1 << 30, 1024) < 32 << 20
 
 
+def test_router_takes_many_sequences_that_are_balanced_together(fc_lib):
+    """Fewer than 2^31 rows, whatever their sequences: the shape is not what is refused."""
+    many = dict(seq=(1 << 24) + 5, tok=2, e=1024, ld=1024, lddx=1024)
+    size = fc.fc_router_workspace_size
+    assert size(many["seq"], 2, 1024) > 0 and size(many["seq"], 2, 1024, True) == 0
+    assert _router(fc_lib, **many, per=0, ws=None) == fc.FC_ERR_WORKSPACE
+    assert _router_bwd(fc_lib, **many, per=0, lse=FAKE + 2) == fc.FC_ERR_ALIGNMENT
+    for call in (_router, _router_bwd):
+        assert call(fc_lib, **many, per=1, lse=FAKE + 2) == fc.FC_ERR_INVALID_ARG
+
+
 def test_binding_refuses_tensors_off_the_gpu(fc_lib):
     x, w = torch.zeros(2, 5, 8), torch.zeros(4096, dtype=torch.uint8)
     with pytest.raises(ValueError):
