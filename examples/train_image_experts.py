@@ -25,6 +25,12 @@ from gradient_aggregation_gb300 import fc  # noqa: E402
 EPS = 1e-5
 
 
+def first_derivatives_only():
+    """A second derivative through a kernel's result would leave out the kernel."""
+    if torch.is_grad_enabled():
+        raise RuntimeError("the kernels give first derivatives only, not create_graph=True")
+
+
 class GroupNormSiLU(torch.autograd.Function):
     """fc.fc_groupnorm_forward and fc.fc_groupnorm_backward as one torch function."""
 
@@ -43,6 +49,7 @@ class GroupNormSiLU(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        first_derivatives_only()
         x, weight, bias, mean, rstd = ctx.saved_tensors
         dx, dweight, dbias = torch.empty_like(x), torch.empty_like(weight), torch.empty_like(bias)
         workspace = torch.empty(fc.fc_groupnorm_workspace_size(*x.shape, ctx.groups),
@@ -75,6 +82,7 @@ class Router(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dweights, dloss, _chosen, _counts):
+        first_derivatives_only()
         logits, chosen, weights, lse, counts, routed = ctx.saved_tensors
         dlogits = torch.empty_like(logits)
         fc.fc_router_backward(logits, ctx.sequences, True, False, chosen, weights, lse, counts,

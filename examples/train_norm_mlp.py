@@ -25,6 +25,12 @@ from gradient_aggregation_gb300 import fc  # noqa: E402
 EPS = 1e-5
 
 
+def first_derivatives_only():
+    """A second derivative through a kernel's result would leave out the kernel."""
+    if torch.is_grad_enabled():
+        raise RuntimeError("the kernels give first derivatives only, not create_graph=True")
+
+
 class LayerNorm(torch.autograd.Function):
     """fc.fc_layernorm_forward and fc.fc_layernorm_backward as one torch function."""
 
@@ -39,6 +45,7 @@ class LayerNorm(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        first_derivatives_only()
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dweight, dbias = torch.empty_like(x), torch.empty_like(weight), torch.empty_like(weight)
         workspace = torch.empty(fc.fc_layernorm_backward_workspace_size(*x.shape),

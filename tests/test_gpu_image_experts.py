@@ -105,6 +105,25 @@ def test_example_gradients_match_torch():
         assert float((a.double() - b).norm()) <= 1e-4 * float(b.norm()) + 1e-7
 
 
+def test_second_derivatives_are_refused():
+    """The kernels give first derivatives: one by these would leave out what goes through them."""
+    mod, x = example(), torch.randn(2, 9, 8, device="cuda", requires_grad=True)
+    weight = torch.ones(8, device="cuda", requires_grad=True)
+    bias = torch.zeros(8, device="cuda", requires_grad=True)
+    lengths = torch.tensor([9, 3], dtype=torch.int32, device="cuda")
+    path = os.path.join(ROOT, "examples", "train_norm_mlp.py")
+    spec = importlib.util.spec_from_file_location("train_norm_mlp", path)
+    norms = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(norms)
+    for call in (lambda: mod.GroupNormSiLU.apply(x, 2, weight, bias),
+                 lambda: mod.Router.apply(x.flatten(0, 1), 2, lengths, 2)[1],
+                 lambda: norms.LayerNorm.apply(x.flatten(0, 1), weight, bias)):
+        loss = call().square().sum() + (x ** 3).sum()
+        with pytest.raises(RuntimeError, match="first derivatives"):
+            grad, = torch.autograd.grad(loss, x, create_graph=True)
+            torch.autograd.grad(grad.square().sum(), x)
+
+
 def test_captured_together_with_one_workspace():
     """Norm, logits, router and back, captured once and replayed on other maps: within the
     bounds of the definitions, and the bits of the calls made one by one."""
