@@ -40,13 +40,35 @@ int64_t gn_parts(const GnShape &n)
     return (n.positions + rows - 1) / rows;
 }
 
-// Streaming leaves one for each part, and one for each sample that has several; the
-// resident kernels one for each cluster that works on a slab's samples: no more than samples.
+// Many samples of few positions are streamed some at a time, so that what they leave is 64 MB
+// at most (a set of two sums is up to 8 bytes for each element of them, which L2 holds so) and
+// no thread adds up more than 256 sets.  All at once, 65536 x 1 x 4096 bf16 at an odd pitch
+// left 2148 MB: 8.77 and 10.44 ms, in chunks 8.71 and 10.26; 9000 x 16 x 2000: 915 and 1356 us,
+// in chunks 951 and 1388.
+int64_t gn_chunk(const GnShape &n)
+{
+    if (gn_parts(n) > 1) return n.samples;  // 512 samples at most
+    const int64_t most = std::min<int64_t>(8192, (1 << 23) / gn_padded(n.channels));
+    return std::min<int64_t>(n.samples, std::max<int64_t>(1, most));
+}
+
+// The same limit for the sets of the resident kernels, above what the GPU holds: clusters run
+// at a time, 2048 threads of an SM at most with 8 channels each.
+int64_t gn_held(const GnShape &n)
+{
+    const int64_t most = std::min<int64_t>(FC_GN_SETS, (1 << 23) / gn_padded(n.channels));
+    return std::min<int64_t>(n.samples, std::max<int64_t>(1, most));
+}
+
+// Streaming leaves one for each part, one for each sample that has several, and one for each
+// chunk of samples where there are several; the resident kernels one for each cluster that
+// works on a slab's samples.
 int64_t gn_sets(const GnShape &n)
 {
-    const int64_t held = std::min<int64_t>(n.samples, FC_GN_SETS);
-    const int64_t parts = gn_parts(n);
-    return gn_may_stream(n) ? n.samples * (parts + (parts > 1)) : held;
+    if (n.samples == 0 || !gn_may_stream(n)) return gn_held(n);
+    const int64_t parts = gn_parts(n), chunk = gn_chunk(n);
+    const int64_t chunks = (n.samples + chunk - 1) / chunk;
+    return std::max(gn_held(n), chunk * (parts + (parts > 1)) + (chunks > 1 ? chunks : 0));
 }
 
 namespace {
@@ -215,7 +237,7 @@ bool find_plan(const GnShape &n, int ab, int ne, int tensors, const void *kernel
     });
     if (held < 1) return false;
     // as many clusters as run at a time, each with as many samples as the others
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(held / p.nslab, FC_GN_SETS));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(held / p.nslab, gn_held(n)));
     const int64_t rounds = (n.samples + most - 1) / most;
     p.per = (int)((n.samples + rounds - 1) / rounds);
     *out = p;

@@ -6,6 +6,8 @@
 // stay the same and what belongs to a channel stays in its registers.
 #pragma once
 
+#include <algorithm>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -934,6 +936,13 @@ inline GnTile gn_tile(const GnShape &n, int ne)
     t.parts = (int)gn_parts(n);
     t.rows = (n.positions + t.parts - 1) / t.parts;
     return t;
+}
+
+// The images from sample `first` on.
+template <class T>
+GnImages gn_from(const GnImages &i, int64_t first)
+{
+    return {static_cast<const T *>(i.p) + first * i.ss, i.ld, i.ss};
 }
 
 inline unsigned gn_grid(const GnShape &n, const GnTile &t)

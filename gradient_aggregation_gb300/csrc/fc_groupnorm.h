@@ -44,6 +44,8 @@ struct GnBackward {
 // The workspace: sets of two values a channel (what blocks leave), then two values a
 // group and sample.
 int64_t gn_parts(const GnShape &n);  // parts of a sample's positions, streaming
+int64_t gn_chunk(const GnShape &n);  // samples at a time, streaming
+int64_t gn_held(const GnShape &n);   // most clusters that work on a slab's samples
 int64_t gn_sets(const GnShape &n);
 bool gn_may_stream(const GnShape &n);  // else the workspace has no room for it
 inline int64_t gn_padded(int channels) { return ((int64_t)channels + 7) & ~(int64_t)7; }

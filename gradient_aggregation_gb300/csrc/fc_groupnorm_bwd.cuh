@@ -19,12 +19,13 @@ inline cudaError_t gn_join(const GnBackward &a, const float *in, int64_t sets, c
     return ln_join(l, (int)sets, s);
 }
 
+// Some of a call's samples, whose sums go to dweight and dbias; `stat` has room for two values
+// a group of each.
 template <class T, int AB, int ACT>
-cudaError_t gn_backward_streaming(const GnBackward &a, cudaStream_t s)
+cudaError_t gn_backward_chunk(const GnBackward &a, const GnTile &t, float *stat, cudaStream_t s)
 {
-    const GnTile t = gn_tile(a.n, Gv<T, AB>::NE);
     const unsigned grid = gn_grid(a.n, t);
-    float *part = a.ws, *const stat = a.ws + 2 * gn_sets(a.n) * gn_padded(a.n.channels);
+    float *part = a.ws;
     int64_t sets = a.n.samples * t.parts;
     int parts = t.parts;
     cudaError_t e = launch_after_prior(k_gn_sums<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, part,
@@ -50,6 +51,33 @@ cudaError_t gn_backward_streaming(const GnBackward &a, cudaStream_t s)
     e = launch_after_prior(k_gn_apply_bwd<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);
     if (e != cudaSuccess) return e;
     return gn_join(a, part, sets, s);
+}
+
+template <class T, int AB, int ACT>
+cudaError_t gn_backward_streaming(const GnBackward &a, cudaStream_t s)
+{
+    const GnTile t = gn_tile(a.n, Gv<T, AB>::NE);
+    const int64_t padded = gn_padded(a.n.channels);
+    float *const stat = a.ws + 2 * gn_sets(a.n) * padded;
+    const int64_t chunk = gn_chunk(a.n), chunks = (a.n.samples + chunk - 1) / chunk;
+    if (chunks == 1) return gn_backward_chunk<T, AB, ACT>(a, t, stat, s);
+    float *const sums = a.ws + 2 * chunk * padded;  // behind what a chunk leaves: a set for each
+    for (int64_t k = 0; k < chunks; ++k) {
+        const int64_t first = k * chunk;
+        GnBackward c = a;
+        c.n.samples = std::min(chunk, a.n.samples - first);
+        c.dy = gn_from<T>(a.dy, first);
+        c.x = gn_from<T>(a.x, first);
+        c.dx = gn_from<T>(a.dx, first);
+        c.mean += first * a.n.groups;
+        c.rstd += first * a.n.groups;
+        c.gtype = FC_TYPE_F32;
+        if (a.dweight) c.dweight = sums + k * padded;
+        if (a.dbias) c.dbias = sums + (chunks + k) * padded;
+        const cudaError_t e = gn_backward_chunk<T, AB, ACT>(c, t, stat, s);
+        if (e != cudaSuccess) return e;
+    }
+    return gn_join(a, sums, chunks, s);
 }
 
 template <class T, int AB, int ACT, bool ONE>

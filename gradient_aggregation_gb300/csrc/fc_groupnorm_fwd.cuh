@@ -5,12 +5,12 @@
 
 namespace fc {
 
+// Some of a call's samples; `stat` has room for two values a group of each.
 template <class T, int AB, int ACT>
-cudaError_t gn_forward_streaming(const GnForward &a, cudaStream_t s)
+cudaError_t gn_forward_chunk(const GnForward &a, const GnTile &t, float *stat, cudaStream_t s)
 {
-    const GnTile t = gn_tile(a.n, Gv<T, AB>::NE);
     const unsigned grid = gn_grid(a.n, t);
-    float *part = a.ws, *const stat = a.ws + 2 * gn_sets(a.n) * gn_padded(a.n.channels);
+    float *part = a.ws;
     int64_t sets = a.n.samples * t.parts, rows = t.rows;
     int parts = t.parts;
     cudaError_t e = launch_after_prior(k_gn_stats<T, AB>, grid, FC_GN_BLOCK, 0, s, a.x, a.n, t, part,
@@ -35,6 +35,27 @@ cudaError_t gn_forward_streaming(const GnForward &a, cudaStream_t s)
                                part, sets, a.eps, stat, a.mean, a.rstd);
     if (e != cudaSuccess) return e;
     return launch_after_prior(k_gn_apply<T, AB, ACT>, grid, FC_GN_BLOCK, 0, s, a, t, stat);
+}
+
+template <class T, int AB, int ACT>
+cudaError_t gn_forward_streaming(const GnForward &a, cudaStream_t s)
+{
+    const GnTile t = gn_tile(a.n, Gv<T, AB>::NE);
+    float *const stat = a.ws + 2 * gn_sets(a.n) * gn_padded(a.n.channels);
+    const int64_t chunk = gn_chunk(a.n);
+    for (int64_t first = 0; first < a.n.samples; first += chunk) {
+        GnForward c = a;
+        c.n.samples = std::min(chunk, a.n.samples - first);
+        c.x = gn_from<T>(a.x, first);
+        c.y = gn_from<T>(a.y, first);
+        if (a.mean) {
+            c.mean += first * a.n.groups;
+            c.rstd += first * a.n.groups;
+        }
+        const cudaError_t e = gn_forward_chunk<T, AB, ACT>(c, t, stat, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 template <class T, int AB, int ACT, bool ONE>

@@ -630,7 +630,9 @@ FC_API fc_status fc_layernorm_backward(const void *dy, int64_t lddy, const void 
 #define FC_ACT_SILU 2
 
 /* Bytes of scratch that both passes of group norm need; 0 on bad arguments.
- * Needs no filling. */
+ * Needs no filling.  At most 1536 pairs of fp32 sums a channel for up to 512
+ * samples; for more 64 MB of pairs (or those of one sample), and one for each
+ * 8192 samples or 64 MB; beside either 8 bytes a group and sample. */
 FC_API size_t fc_groupnorm_workspace_size(int64_t samples, int64_t positions, int64_t channels,
                                           int64_t groups);
 

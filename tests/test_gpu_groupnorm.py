@@ -165,6 +165,26 @@ def test_many_samples_at_odd_places(n, s, c, groups, lay, act, dtype):
     check(n, s, c, groups, dtype, act=act, **lay)
 
 
+# groups that no cluster holds, of so many samples that they are streamed in chunks
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("n,s,c,groups,lay", [
+    (9000, 1, 4104, 2, {}), (20000, 2, 520, 1, dict(pad=1)), (8193, 3, 521, 1, dict(gap=3)),
+    (5000, 4, 4104, 2, dict(first=True))], ids=str)
+def test_samples_in_chunks(n, s, c, groups, lay, dtype):
+    x, w, b, y, mu, rs, dy, dx, dw, db = check(n, s, c, groups, dtype, act=RELU if s == 2 else SILU,
+                                               gtype=dtype, **lay)
+    ws = scratch(n, s, c, groups)
+    act = RELU if s == 2 else SILU
+    for want in ((None, db), (dw, None), (None, None)):
+        dx2 = torch.empty_like(dx)
+        got = [None if t is None else torch.empty_like(t) for t in want]
+        fc.fc_groupnorm_backward(dy, x, groups, w, b, act, mu, rs, dx2, got[0], got[1], ws)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, dx2)
+        for t, g in zip(want, got):
+            assert t is None or torch.equal(t, g)
+
+
 @pytest.mark.parametrize("gtype", TYPES, ids=ids)
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 def test_gradient_types(dtype, gtype):

@@ -80,6 +80,22 @@ def test_groupnorm_workspace_sizes(fc_lib):
     assert size(64, 4096, 512, 32) < 64 * 4096 * 512 * 2 // 10
 
 
+@pytest.mark.parametrize("n,s,c,groups", [
+    (65536, 1, 4096, 1), (4096, 1, 1024, 2), (1 << 24, 1, 512, 1), (70000, 3, 520, 1),
+    (2000, 16, 1 << 20, 1), (1 << 20, 40, 300, 1), (1 << 24, 1, 8, 1), (513, 1, 1 << 20, 2),
+    (600, 5000, 8192, 8), (1024, 1, 1 << 20, 1 << 18)])
+def test_groupnorm_scratch_of_many_samples(fc_lib, n, s, c, groups):
+    """Not a share of the images, however few positions they have: 2^23 pairs of sums at a
+    time (or those of one sample), a set for each chunk, two values a group and sample."""
+    chunks = -(-n // min(8192, max(1, (1 << 23) // c)))
+    most = 8 * (max(c, 1 << 23) + chunks * c + n * groups) + 768
+    assert fc.fc_groupnorm_workspace_size(n, s, c, groups) <= most
+
+
+def test_groupnorm_scratch_without_samples(fc_lib):
+    assert fc.fc_groupnorm_workspace_size(0, 1 << 16, 1 << 20, 1) <= 768
+
+
 RT = dict(x=FAKE, seq=3, tok=4, e=8, ld=8, kind=2, lengths=FAKE, k=2, norm=1, per=1, chosen=FAKE,
           weights=FAKE, lse=FAKE, counts=FAKE, routed=FAKE, probs=FAKE, loss=FAKE, ws=FAKE,
           nbytes=1 << 20)
