@@ -347,6 +347,42 @@ def test_captured_and_replayed(rows, experts, k):
             assert torch.equal(o[q], want[q]), q
 
 
+@pytest.mark.parametrize("normalise", [False, True])
+@pytest.mark.parametrize("rows,experts,k", [(64, 8, 2), (5000, 256, 8), (900, 60, 3)])
+def test_gradients_captured_and_replayed(rows, experts, k, normalise):
+    """A replay's gradients are those of the calls made one by one, on other logits too."""
+    x, _ = scores(rows, experts, F32)
+    o = outputs(rows, experts, k, 1)
+    ws = scratch(1, rows, experts, False)
+    dw, dl = torch.randn(rows, k, device="cuda"), torch.ones(2, device="cuda")
+    dx = torch.empty_like(x)
+
+    def step():
+        fc.fc_router_forward(x, 1, None, normalise, False, o["chosen"], o["weights"], o["lse"],
+                             o["counts"], o["routed"], o["probs"], o["loss"], ws)
+        fc.fc_router_backward(x, 1, normalise, False, o["chosen"], o["weights"], o["lse"],
+                              o["counts"], o["routed"], dw, dl, dx)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2, 3):
+        x.copy_(scores(rows, experts, F32, seed=seed)[0])
+        for t in (dx, *o.values()):
+            t.fill_(55)
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        got, weights = dx.clone(), o["weights"].clone()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got, dx) and torch.equal(weights, o["weights"])
+        want, bound = ref.router_backward(x, 1, k, normalise, False, o["chosen"], o["weights"],
+                                          o["lse"], o["counts"], o["routed"], dw, dl)
+        assert_within("dlogits", got, want, rounded(bound, want, F32))
+
+
 def test_refusals():
     x = torch.zeros(12, 8, device="cuda")
     o = outputs(12, 8, 2, 1)
