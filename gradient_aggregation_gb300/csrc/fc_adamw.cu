@@ -363,13 +363,6 @@ __device__ __forceinline__ float fast_sqrt(float x)
     return y;
 }
 
-__device__ __forceinline__ float fast_rcp_ftz(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // sqrt(x) for x = 0 or in [2^-126, 2^127]: the approximate reciprocal root, and
 // one Newton step on the root's remainder, after which all but about one root
 // in a million is the nearest fp32 number.
@@ -474,7 +467,7 @@ __device__ __forceinline__ bool adam8_unit(const float *graw, const float *d, co
         const F2 v = add_once(mul2(mul2(r0, r0), b22), mul2(mul2(g, g), omb22));
         r[p] = newton_sqrt2(v);
         const float2 den = un2(fma2(r[p], rc22, eps2));
-        const F2 rden = f2(fast_rcp_ftz(den.x), fast_rcp_ftz(den.y));
+        const F2 rden = f2(rcp_ftz(den.x), rcp_ftz(den.y));
         const F2 w2 = f2(w[2 * p], w[2 * p + 1]);
         const F2 wd = UNIFORM ? f2(wd0, wd0) : f2(-h.lrwd * d[2 * p], -h.lrwd * d[2 * p + 1]);
         const float2 wn = un2(fma2(mul2(lrc2, m[p]), rden, fma2(wd, w2, w2)));

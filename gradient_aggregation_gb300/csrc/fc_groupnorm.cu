@@ -148,10 +148,6 @@ int cluster_limit(const void *kernel)
     return 1;
 }
 
-}  // namespace
-
-namespace {
-
 bool find_plan(const GnShape &n, int ab, int ne, int tensors, const void *kernel, int dev,
                GnPlan *out)
 {

@@ -142,20 +142,6 @@ __device__ __forceinline__ F2 neg2(F2 a)
     return f2(-v.x, -v.y);
 }
 
-__device__ __forceinline__ float gn_ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float gn_rcp(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // 1 / (1 + e^-z) of a vector, off by 10 + 1.5 |z| roundings at most (what is below
 // 2^-126 is flushed).  Two special-function instructions a value; a reciprocal shared
 // by two values spares a quarter of them and costs more issue slots than it gives.
@@ -166,8 +152,8 @@ __device__ __forceinline__ void gn_sigmoid(const F2 (&z)[NP], F2 (&s)[NP])
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const float2 t = un2(mul2(z[p], f2(kL, kL)));
-        const float2 a = un2(add2(f2(gn_ex2(t.x), gn_ex2(t.y)), f2(1.f, 1.f)));
-        s[p] = f2(gn_rcp(a.x), gn_rcp(a.y));
+        const float2 a = un2(add2(f2(ex2_ftz(t.x), ex2_ftz(t.y)), f2(1.f, 1.f)));
+        s[p] = f2(rcp_ftz(a.x), rcp_ftz(a.y));
     }
 }
 

@@ -184,11 +184,6 @@ __device__ __forceinline__ void gn_block_or_cluster_sync(int K)
         __syncthreads();
 }
 
-template <bool YES>
-struct GnYes {
-    static constexpr bool value = YES;
-};
-
 template <class T, int AB, int ACT, bool ONE>
 __global__ void __launch_bounds__(FC_GN_RESIDENT)
     k_gn_fwd(const __grid_constant__ GnForward a, const __grid_constant__ GnPlan p)
@@ -352,13 +347,13 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT)
                 if constexpr (decltype(ahead)::value) cp_async_commit();
             };
             if constexpr (AB == 2) {
-                put(0, s.rows, GnYes<false>());
+                put(0, s.rows, Yes<false>());
                 if (more) copy(n + p.per, 0, s.rows);
             } else if (more) {
-                put(0, half, GnYes<true>());
-                put(half, s.rows, GnYes<true>());
+                put(0, half, Yes<true>());
+                put(half, s.rows, Yes<true>());
             } else {
-                put(0, s.rows, GnYes<false>());
+                put(0, s.rows, Yes<false>());
             }
         }
         if (p.K > 1) cluster_wait();
@@ -584,16 +579,16 @@ __global__ void __launch_bounds__(FC_GN_RESIDENT_BWD)
                 if constexpr (decltype(ahead)::value) cp_async_commit();
             };
             if constexpr (AB == 2) {
-                put(0, s.rows, GnYes<false>());
+                put(0, s.rows, Yes<false>());
                 if (more) {  // the statistics are in the first of two groups here too
                     copy(n + p.per, 0, half);
                     copy(n + p.per, half, s.rows);
                 }
             } else if (more) {
-                put(0, half, GnYes<true>());
-                put(half, s.rows, GnYes<true>());
+                put(0, half, Yes<true>());
+                put(half, s.rows, Yes<true>());
             } else {
-                put(0, s.rows, GnYes<false>());
+                put(0, s.rows, Yes<false>());
             }
         }
         if (p.K > 1) cluster_wait();

@@ -50,6 +50,27 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b)
     return r;
 }
 
+// One special-function instruction each; what is below 2^-126 is taken as 0.
+__device__ __forceinline__ float ex2_ftz(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_ftz(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A truth value as an argument's type.
+template <bool YES>
+struct Yes {
+    static constexpr bool value = YES;
+};
+
 // A 16-byte vector of its pairs: 4 of a 16-bit type, 2 of fp32, each rounded once.
 template <class T>
 __device__ __forceinline__ uint4 from_pairs(const F2 (&f)[8 / sizeof(T)])

@@ -36,13 +36,6 @@ namespace fc {
 
 constexpr float kRtLog2e = 1.44269504f;
 
-__device__ __forceinline__ float rt_ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Eight elements of a row, loaded ahead of their use.  ALIGNED: E is whole 16-byte
 // vectors and so is every row's start; what lies past E, or is not there, is -infinity.
 template <class T, bool ALIGNED>
@@ -217,13 +210,6 @@ __host__ __device__ inline RouterWs router_ws(void *ws, int64_t groups, int64_t 
     return w;
 }
 
-__device__ __forceinline__ float rt_rcp(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Sum over the LPR lanes of a row.
 template <int LPR>
 __device__ __forceinline__ float rt_row_sum(float x)
@@ -264,11 +250,6 @@ __device__ __forceinline__ float rt_row_max(float x)
     for (int o = LPR / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
 }
-
-template <bool YES>
-struct RtYes {
-    static constexpr bool value = YES;
-};
 
 // Rows of a lane at a time.
 template <int LPR, int VPL>
@@ -388,7 +369,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                     for (int p = 0; p < 4; ++p) {
                         const float2 e = un2(fma2(x[u][v][p], f2(kRtLog2e, kRtLog2e),
                                                   f2(shift, shift)));
-                        x[u][v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                        x[u][v][p] = f2(ex2_ftz(e.x), ex2_ftz(e.y));
                         acc = add2(acc, x[u][v][p]);
                     }
                 const float2 both = un2(acc);
@@ -421,7 +402,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                             const float2 e = un2(mul2(d, f2(kRtLog2e, kRtLog2e)));
                             const float2 w = un2(y[p]);
                             nan |= w.x != w.x || w.y != w.y;
-                            const F2 o = f2(rt_ex2(e.x), rt_ex2(e.y));
+                            const F2 o = f2(ex2_ftz(e.x), ex2_ftz(e.y));
                             if (again) x[u][v][p] = o;
                             acc = add2(acc, o);
                         }
@@ -438,7 +419,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int r = r0 + u * RPI + sub;
-                const float inv = rt_rcp(total[u]);
+                const float inv = rcp_ftz(total[u]);
                 const bool on = routes >> u & 1;
                 if (on) {
 #pragma unroll
@@ -451,9 +432,9 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
             }
         };
         if (rows % (RPI * U) == 0 && present == (rows == 32 ? ~0u : (1u << rows) - 1u)) {
-            for (int r0 = 0; r0 < rows; r0 += RPI * U) softmax(r0, RtYes<true>());
+            for (int r0 = 0; r0 < rows; r0 += RPI * U) softmax(r0, Yes<true>());
         } else {
-            for (int r0 = 0; r0 < rows; r0 += RPI * U) softmax(r0, RtYes<false>());
+            for (int r0 = 0; r0 < rows; r0 += RPI * U) softmax(r0, Yes<false>());
         }
         __syncwarp();
         // the choice, a lane a row
@@ -524,7 +505,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                     const bool again = same & (same - 1);
                     mine[g] = RtWord<T>::make(again ? value : left, g,
                                               again ? taken | 1u << at_e : 0);
-                    const float p = rt_ex2(fmaf(value - less, kRtLog2e, shift));
+                    const float p = ex2_ftz(fmaf(value - less, kRtLog2e, shift));
                     chosen_sum += p;
                     chosen[lane * k + j] = 8 * g + at_e;
                     weights[lane * k + j] = p;
@@ -822,7 +803,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                     for (int p = 0; p < 4; ++p) {
                         const float2 e = un2(fma2(x[u][v][p], f2(kRtLog2e, kRtLog2e),
                                                   f2(shift, shift)));
-                        x[u][v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                        x[u][v][p] = f2(ex2_ftz(e.x), ex2_ftz(e.y));
                         acc = fma2(x[u][v][p], c[v][p], acc);
                     }
                 }
@@ -843,7 +824,7 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
                         for (int p = 0; p < 4; ++p) {
                             const F2 d = add2(y[v][p], f2(-st[u].x, -st[u].x));
                             const float2 e = un2(mul2(d, f2(kRtLog2e, kRtLog2e)));
-                            y[v][p] = f2(rt_ex2(e.x), rt_ex2(e.y));
+                            y[v][p] = f2(ex2_ftz(e.x), ex2_ftz(e.y));
                             all = add2(all, y[v][p]);
                             acc = fma2(y[v][p], c[v][p], acc);
                         }
@@ -886,9 +867,9 @@ __global__ void __launch_bounds__(32 * FC_ROUTER_WARPS, rt_blocks<T, VPL>())
             }
         };
         if (rows % (RPI * U) == 0 && live_rows == (rows == 32 ? ~0u : (1u << rows) - 1u)) {
-            for (int r0 = 0; r0 < rows; r0 += RPI * U) gradient(r0, RtYes<true>());
+            for (int r0 = 0; r0 < rows; r0 += RPI * U) gradient(r0, Yes<true>());
         } else {
-            for (int r0 = 0; r0 < rows; r0 += RPI * U) gradient(r0, RtYes<false>());
+            for (int r0 = 0; r0 < rows; r0 += RPI * U) gradient(r0, Yes<false>());
         }
         __syncwarp();
     }
