@@ -672,8 +672,10 @@ FC_API fc_status fc_groupnorm_forward(const void *x, int64_t samples, int64_t po
  *   dx = rstd * (q - sum(q) / M - h * sum(q * h) / M)
  * and over samples and positions:
  *   dweight[c] = sum dz * h,  dbias[c] = sum dz
- * in fp32, each rounded once, the sums in a fixed order.  Which side of 0 a value
- * lies on (FC_ACT_RELU) is as in exact arithmetic with the given mean and rstd.
+ * in fp32, each rounded once, the sums in a fixed order.  rstd^2 is formed on the way:
+ * rstd has to lie below 2^60.  Which side of 0 a value lies on (FC_ACT_RELU) is as in
+ * exact arithmetic with the given mean and rstd, where the bias and the product beside
+ * it are 0 or not below 2^-100.
  *  dy, x, dx   device images of `type` as in the forward pass, each with strides of
  *              its own; dx must not overlap the inputs.
  *  weight, bias, act  as in the forward pass.

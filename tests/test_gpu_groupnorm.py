@@ -280,6 +280,34 @@ def test_relu_side_is_exact():
     assert_within("dx", dx, wdx, rounded(edx, wdx, F32))
 
 
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** -60, 2.0 ** 40])
+def test_relu_side_is_exact_at_any_size(size):
+    """The border again, with parameters far from 1."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    n, s, c, groups = 2, 256, 64, 4
+    mu = torch.randn(n, groups, generator=g, device="cuda")
+    rs = torch.rand(n, groups, generator=g, device="cuda") + 0.5
+    w, b = (t * size for t in params(c, F32, 9))
+    m, r = (t.double().repeat_interleave(c // groups, 1)[:, None, :] for t in (mu, rs))
+    x = (m - b.double() / (r * w.double())).float().expand(n, s, c).contiguous()
+    x.view(torch.int32).add_(torch.randint(-2, 3, (n, s, c), generator=g, device="cuda",
+                                           dtype=torch.int32))
+    dy = torch.randn(n, s, c, generator=g, device="cuda")
+    dx, dw, db = torch.empty_like(x), torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+    fc.fc_groupnorm_backward(dy, x, groups, w, b, RELU, mu, rs, dx, dw, db,
+                             scratch(n, s, c, groups))
+    (wdx, wdw, wdb), (edx, edw, edb) = ref.groupnorm_backward(dy, x, groups, w, b, RELU, mu, rs)
+    assert_within("dbias", db, wdb, rounded(edb, wdb, F32))
+    assert_within("dweight", dw, wdw, rounded(edw, wdw, F32))
+    assert_within("dx", dx, wdx, rounded(edx, wdx, F32))
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -58, 2.0 ** -40])
+@pytest.mark.parametrize("s,c,groups", [(50, 32, 4), (9001, 272, 1)])
+def test_spreads_far_below_one(s, c, groups, scale):
+    check(2, s, c, groups, F32, act=NONE, mean=0.0, scale=scale, eps=0.0)
+
+
 def test_same_bits_again_and_on_another_stream():
     a = check(5, 300, 96, 32, BF16)
     side = torch.cuda.Stream()
