@@ -185,6 +185,26 @@ def test_samples_in_chunks(n, s, c, groups, lay, dtype):
             assert t is None or torch.equal(t, g)
 
 
+def test_chunks_captured_and_replayed():
+    n, s, c, groups = 9000, 1, 4104, 2
+    x, w, b, y, mu, rs, dy, dx, dw, db = check(n, s, c, groups, BF16)
+    ws = scratch(n, s, c, groups)
+    outs = [torch.empty_like(t) for t in (y, mu, rs, dx, dw, db)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fc.fc_groupnorm_forward(x, groups, w, b, EPS, SILU, outs[0], outs[1], outs[2], ws)
+        fc.fc_groupnorm_backward(dy, x, groups, w, b, SILU, outs[1], outs[2], outs[3], outs[4],
+                                 outs[5], ws)
+    for _ in range(2):
+        for t in outs:
+            t.fill_(5.0)
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, want in zip(outs, (y, mu, rs, dx, dw, db)):
+            assert torch.equal(t, want)
+
+
 @pytest.mark.parametrize("gtype", TYPES, ids=ids)
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 def test_gradient_types(dtype, gtype):
